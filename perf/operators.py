@@ -124,7 +124,7 @@ def _quantize(v):
     """[n, m] fp32 -> e4m3 elements [n, m] and e8m0 scales [n, m / 32]."""
     b = v.reshape(v.shape[0], -1, 32)
     m, e = torch.frexp(b.abs().amax(2))  # max|v| = m 2^e with m in [0.5, 1), and 448 = 0.875 * 2^9
-    e = (e - 9 + (m > 0.875)).clamp(-127, 127)
+    e = torch.where(m > 0, e - 9 + (m > 0.875), -127).clamp(-127, 127)
     q = torch.ldexp(b, -e.unsqueeze(2)).to(torch.float8_e4m3fn).reshape(v.shape)
     return q, (e + 127).to(torch.uint8).view(torch.float8_e8m0fnu)
 
