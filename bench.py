@@ -76,7 +76,7 @@ TRAFFIC_SOURCES = ("token_dispatch_grouped_amd/csrc/gemm_bf16.hip", "token_dispa
                    "token_dispatch_grouped_amd/csrc/gemm_bf16_kernel.h", "token_dispatch_grouped_amd/csrc/gemm_common.h",
                    "token_dispatch_grouped_amd/csrc/common.h", "token_dispatch_grouped_amd/build.py")
 TRAFFIC = {
-    "sources_sha256": "5cb16b5d5c047803b0bcdf39d692ce7317c4aa2be384891d536bff0bd5b661b7",
+    "sources_sha256": "067a92a18b39e804fee7f26981ce4fc3b6adb7ffa73806de7ba8d6514463f899",
     "workload": "ep_share_32k",
     "bytes_per_launch": {
         # read GiB + write GiB, x 2^30

@@ -70,7 +70,9 @@ typedef enum moe_status {
   MOE_ERR_HIP = 5               /* a HIP launch failed; see moe_last_error() */
 } moe_status;
 
-enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1 };
+/* MOE_DTYPE_MX8 is the 8-bit block form of the dense feed-forward block (see
+ * moe_mx8_quantize); the routed layer's calls take F32 and BF16. */
+enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_MX8 = 2 };
 
 /* MOE_FLAG_RENORM: renormalise the k selected weights so that they sum to
  * one. Without it the weights are the full-softmax probabilities of the
@@ -458,6 +460,118 @@ moe_status moe_ep_exchange_loopback(int32_t ep, int32_t d, int32_t dtype, void *
                                     void *const *recv_bufs, const int64_t *recv_caps,
                                     const int32_t *const *recv_offsets, const int32_t *const *regroup_rows,
                                     int32_t reverse, moe_stream_t stream);
+
+/*
+ * RMS norm with the residual's addition: the step in front of the expert
+ * layer (its y is the x of moe_route, moe_permute and moe_ffn_fwd).
+ *   r    = x + residual                     [T,d] s   (rounded once)
+ *   rstd = 1 / sqrt(mean_d(r^2) + eps)      [T] fp32
+ *   y    = r * rstd * weight                [T,d] s, or the 8-bit block form
+ * The norm reads the rounded r, which the backward pass reads too. Without a
+ * residual (NULL) r is x, and the r argument must be NULL. weight [d] s. With
+ * y_scale NULL, y is [T,d] s; otherwise y is [T,d] e4m3 bytes and y_scale
+ * [T,d/32] scale bytes, quantised from the fp32 values (moe_mx8_quantize has
+ * the form). r may be x or residual itself. Sums run in fp32 in a fixed
+ * order. T == 0 writes nothing.
+ * Supported: T < 2^24, d a positive multiple of 64, at most 65536, dtype F32
+ * or BF16, eps positive and finite (else MOE_ERR_INVALID_ARGUMENT).
+ *
+ * Backward, from dL/dy, with n = r * rstd and g = dy * weight:
+ *   dx  = rstd * (g - n * mean_d(g * n)) + dres     [T,d] s
+ *   dw += sum_t dy * n                              [d] fp32
+ * dx is the gradient of x and of the residual alike; dres [T,d] s (may be
+ * NULL) is the gradient that reaches r directly (the residual stream behind
+ * the layer). r is the x of a forward without a residual. dx may be dy or
+ * dres itself. dw accumulates like every weight gradient;
+ * MOE_NORM_OVERWRITE_DW writes it instead (T == 0 then writes zeros, and the
+ * other tensors may be NULL). The sum over tokens runs in a fixed order (no
+ * atomics). ws: at least the bytes moe_rmsnorm_workspace_size reports, which
+ * serve every smaller T of the same d.
+ */
+enum { MOE_NORM_OVERWRITE_DW = 1u };
+
+typedef struct moe_norm_shape {
+  int64_t T;      /* rows (>= 0) */
+  int32_t d;      /* hidden size */
+  int32_t dtype;  /* MOE_DTYPE_F32 or MOE_DTYPE_BF16 */
+  float eps;      /* added to the mean square */
+  uint32_t flags; /* MOE_NORM_* */
+} moe_norm_shape;
+
+moe_status moe_rmsnorm_workspace_size(const moe_norm_shape *shape, size_t *bwd_ws);
+moe_status moe_rmsnorm_fwd(const moe_norm_shape *shape, const void *x, const void *residual, const void *weight,
+                           void *r, void *y, void *y_scale, float *rstd, moe_stream_t stream);
+moe_status moe_rmsnorm_bwd(const moe_norm_shape *shape, const void *dy, const void *r, const void *weight,
+                           const float *rstd, const void *dres, void *dx, float *dw, void *ws, size_t ws_bytes,
+                           moe_stream_t stream);
+
+/*
+ * The 8-bit block form of a matrix x [rows, cols] (fp32 or bf16): q [rows,
+ * cols] e4m3 bytes and scale [rows, cols/32] bytes c that stand for 2^(c-127),
+ * one for 32 consecutive elements of a row: the smallest power of two S with
+ * max|x| <= 448 S (at least 2^-127), q = x / S rounded to nearest-even. The
+ * values are q * S. A block that holds an infinity or a NaN has scale byte
+ * 255 and NaN elements: all of it stands for NaN. cols is a positive multiple
+ * of 64, at most 65536. rows == 0 is a no-op.
+ */
+moe_status moe_mx8_quantize(int64_t rows, int32_t cols, int32_t dtype, const void *x, void *q, void *scale,
+                            moe_stream_t stream);
+
+/*
+ * Dense gated feed-forward block: the block that every token takes, beside
+ * the routed experts (a shared expert) or instead of them.
+ *   h = x W_gu^T                       [T,2F] s  (gate in columns [0,F), up in [F,2F))
+ *   a = silu(h[:, :F]) * h[:, F:]      [T,F]  s  (from the fp32 products)
+ *   y = a W_down^T + add               [T,d]  s  (one rounding after the addition)
+ * x [T,d], w_gu [2F,d], w_down [d,F]; add [T,d] may be NULL and may be y
+ * itself (typically the routed experts' output from moe_unpermute_combine).
+ *
+ * MOE_DTYPE_BF16: s is bf16 and the three scale pointers must be NULL. h and
+ * a are both given (a backward follows) or both NULL; then h is not written
+ * and a lives in ws. MOE_DTYPE_MX8 (no backward): x, w_gu and w_down are in
+ * the 8-bit block form with their scales [T,d/32], [2F,d/32], [d,F/32]; a is
+ * quantised to that form too (from fp32, in ws), h and a must be NULL; add
+ * and y are bf16. Products accumulate in fp32.
+ *
+ * Input gradient (bf16), with da = dy W_down and sig = 1 / (1 + exp(-h_gate)):
+ *   dh_gate = da * h_up * sig * (1 + h_gate (1 - sig))
+ *   dh_up   = da * h_gate * sig                       dh [T,2F] s
+ *   dx      = dh W_gu + add                           dx [T,d] s
+ * add [T,d] may be NULL and may be dx itself (the routed experts' input
+ * gradient from moe_permute_bwd).
+ *
+ * Weight gradients (bf16 operands, fp32 sums), a call of their own so that a
+ * schedule may run them later:
+ *   dw_gu [2F,d] += dh^T x,   dw_down [d,F] += dy^T a
+ * MOE_FFN_OVERWRITE_DW writes them instead (T == 0 then writes zeros and the
+ * other tensors may be NULL). The sum over tokens runs in a fixed order that
+ * depends on the shape alone (no atomics).
+ *
+ * Workspaces: fwd_ws serves moe_ffn_fwd (not read when h and a are given),
+ * wgrad_ws serves moe_ffn_wgrad; each may be reused by a smaller T of the
+ * same (d, F, dtype). T == 0 otherwise writes nothing.
+ * Supported: T < 2^24, d and F positive multiples of 64 (MX8: of 128), at
+ * most 65536, T * max(d, 2F) small enough for one launch, dtype BF16 or MX8;
+ * the gradients BF16 only. Anything else is MOE_ERR_UNSUPPORTED.
+ */
+enum { MOE_FFN_OVERWRITE_DW = 1u };
+
+typedef struct moe_ffn_shape {
+  int64_t T;      /* tokens (>= 0) */
+  int32_t d;      /* hidden size */
+  int32_t F;      /* SwiGLU hidden size of the block */
+  int32_t dtype;  /* MOE_DTYPE_BF16 or MOE_DTYPE_MX8 */
+  uint32_t flags; /* MOE_FFN_* */
+} moe_ffn_shape;
+
+moe_status moe_ffn_workspace_size(const moe_ffn_shape *shape, size_t *fwd_ws, size_t *wgrad_ws);
+moe_status moe_ffn_fwd(const moe_ffn_shape *shape, const void *x, const void *x_scale, const void *w_gu,
+                       const void *w_gu_scale, const void *w_down, const void *w_down_scale, const void *add, void *h,
+                       void *a, void *y, void *ws, size_t ws_bytes, moe_stream_t stream);
+moe_status moe_ffn_dgrad(const moe_ffn_shape *shape, const void *dy, const void *h, const void *w_gu,
+                         const void *w_down, const void *add, void *dh, void *dx, moe_stream_t stream);
+moe_status moe_ffn_wgrad(const moe_ffn_shape *shape, const void *dy, const void *x, const void *a, const void *dh,
+                         float *dw_gu, float *dw_down, void *ws, size_t ws_bytes, moe_stream_t stream);
 
 /* Static English text for a status code. */
 const char *moe_status_string(moe_status status);

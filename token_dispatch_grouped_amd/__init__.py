@@ -15,7 +15,11 @@ from ._lib import (  # noqa: F401
     moe_aux_config, moe_aux_loss, moe_peak_mfma, moe_peak_mfma_size, moe_peak_copy,
     MOE_EP_MAX_RANKS, moe_ep_send_plan, moe_ep_recv_plan, moe_ep_regroup, moe_ep_exchange_counts_loopback,
     moe_ep_exchange_loopback,
+    MOE_DTYPE_MX8, MOE_NORM_OVERWRITE_DW, MOE_FFN_OVERWRITE_DW, moe_norm_shape, make_norm_shape,
+    moe_rmsnorm_workspace_size, moe_rmsnorm_fwd, moe_rmsnorm_bwd, moe_mx8_quantize, moe_ffn_shape, make_ffn_shape,
+    moe_ffn_workspace_size, moe_ffn_fwd, moe_ffn_dgrad, moe_ffn_wgrad,
 )
 
 __all__ = [n for n in dir() if n.startswith(("moe_", "MOE_"))] + ["MoeError", "load", "make_shape",
-                                                                  "make_adamw_config", "make_aux_config"]
+                                                                  "make_adamw_config", "make_aux_config",
+                                                                  "make_norm_shape", "make_ffn_shape"]

@@ -24,6 +24,7 @@ MOE_ERR_HIP = 5
 
 MOE_DTYPE_F32 = 0
 MOE_DTYPE_BF16 = 1
+MOE_DTYPE_MX8 = 2
 MOE_FLAG_RENORM = 1
 MOE_FLAG_RECOMPUTE = 2
 MOE_FLAG_ACCUMULATE_DLOGITS = 4
@@ -56,7 +57,23 @@ MOE_ADAMW_ZERO_GRAD = 1
 class moe_aux_config(ctypes.Structure):
     _fields_ = [("balance_coef", ctypes.c_float), ("z_coef", ctypes.c_float), ("flags", ctypes.c_uint32)]
 
+
+class moe_norm_shape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("flags", ctypes.c_uint32)]
+
+
+class moe_ffn_shape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("d", ctypes.c_int32), ("F", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("flags", ctypes.c_uint32)]
+
+
+MOE_NORM_OVERWRITE_DW = 1
+MOE_FFN_OVERWRITE_DW = 1
+
 _S = ctypes.POINTER(moe_shape)
+_NS = ctypes.POINTER(moe_norm_shape)
+_FS = ctypes.POINTER(moe_ffn_shape)
 _SZ = ctypes.c_size_t
 
 _SIGNATURES = {
@@ -87,6 +104,14 @@ _SIGNATURES = {
     "moe_ep_exchange_counts_loopback": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, _P, _P, _P]),
     "moe_ep_exchange_loopback": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _P, _P,
                                                 _P, ctypes.c_int32, _P]),
+    "moe_rmsnorm_workspace_size": (ctypes.c_int, [_NS, ctypes.POINTER(_SZ)]),
+    "moe_rmsnorm_fwd": (ctypes.c_int, [_NS, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_rmsnorm_bwd": (ctypes.c_int, [_NS, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_mx8_quantize": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P]),
+    "moe_ffn_workspace_size": (ctypes.c_int, [_FS, ctypes.POINTER(_SZ), ctypes.POINTER(_SZ)]),
+    "moe_ffn_fwd": (ctypes.c_int, [_FS, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_ffn_dgrad": (ctypes.c_int, [_FS, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_ffn_wgrad": (ctypes.c_int, [_FS, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     # include/moe_peak.h
     "moe_peak_mfma": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.POINTER(ctypes.c_double), _P]),
     "moe_peak_mfma_size": (ctypes.c_int64, []),
@@ -291,6 +316,58 @@ def moe_ep_exchange_loopback(ep, d, dtype, send_bufs, send_caps, send_offsets, r
     rg = _ptr_array(regroup_rows) if regroup_rows is not None else (None, None)
     _check(load().moe_ep_exchange_loopback(int(ep), int(d), int(dtype), *[x[0] for x in a], rg[0],
                                            1 if reverse else 0, _stream(stream)), "moe_ep_exchange_loopback")
+
+
+def make_norm_shape(T: int, d: int, dtype: int, eps: float = 1e-6, flags: int = 0) -> moe_norm_shape:
+    return moe_norm_shape(int(T), int(d), int(dtype), float(eps), int(flags))
+
+
+def moe_rmsnorm_workspace_size(shape: moe_norm_shape) -> int:
+    a = _SZ()
+    _check(load().moe_rmsnorm_workspace_size(ctypes.byref(shape), ctypes.byref(a)), "moe_rmsnorm_workspace_size")
+    return a.value
+
+
+def moe_rmsnorm_fwd(shape, x, residual, weight, r, y, y_scale, rstd, stream=None):
+    _check(load().moe_rmsnorm_fwd(ctypes.byref(shape), ptr(x), ptr(residual), ptr(weight), ptr(r), ptr(y),
+                                  ptr(y_scale), ptr(rstd), _stream(stream)), "moe_rmsnorm_fwd")
+
+
+def moe_rmsnorm_bwd(shape, dy, r, weight, rstd, dres, dx, dw, ws, ws_bytes, stream=None):
+    _check(load().moe_rmsnorm_bwd(ctypes.byref(shape), ptr(dy), ptr(r), ptr(weight), ptr(rstd), ptr(dres), ptr(dx),
+                                  ptr(dw), ptr(ws), int(ws_bytes), _stream(stream)), "moe_rmsnorm_bwd")
+
+
+def moe_mx8_quantize(rows, cols, dtype, x, q, scale, stream=None):
+    _check(load().moe_mx8_quantize(int(rows), int(cols), int(dtype), ptr(x), ptr(q), ptr(scale), _stream(stream)),
+           "moe_mx8_quantize")
+
+
+def make_ffn_shape(T: int, d: int, F: int, dtype: int = MOE_DTYPE_BF16, flags: int = 0) -> moe_ffn_shape:
+    return moe_ffn_shape(int(T), int(d), int(F), int(dtype), int(flags))
+
+
+def moe_ffn_workspace_size(shape: moe_ffn_shape):
+    a, b = _SZ(), _SZ()
+    _check(load().moe_ffn_workspace_size(ctypes.byref(shape), ctypes.byref(a), ctypes.byref(b)),
+           "moe_ffn_workspace_size")
+    return a.value, b.value
+
+
+def moe_ffn_fwd(shape, x, x_scale, w_gu, w_gu_scale, w_down, w_down_scale, add, h, a, y, ws, ws_bytes, stream=None):
+    _check(load().moe_ffn_fwd(ctypes.byref(shape), ptr(x), ptr(x_scale), ptr(w_gu), ptr(w_gu_scale), ptr(w_down),
+                              ptr(w_down_scale), ptr(add), ptr(h), ptr(a), ptr(y), ptr(ws), int(ws_bytes),
+                              _stream(stream)), "moe_ffn_fwd")
+
+
+def moe_ffn_dgrad(shape, dy, h, w_gu, w_down, add, dh, dx, stream=None):
+    _check(load().moe_ffn_dgrad(ctypes.byref(shape), ptr(dy), ptr(h), ptr(w_gu), ptr(w_down), ptr(add), ptr(dh),
+                                ptr(dx), _stream(stream)), "moe_ffn_dgrad")
+
+
+def moe_ffn_wgrad(shape, dy, x, a, dh, dw_gu, dw_down, ws, ws_bytes, stream=None):
+    _check(load().moe_ffn_wgrad(ctypes.byref(shape), ptr(dy), ptr(x), ptr(a), ptr(dh), ptr(dw_gu), ptr(dw_down),
+                                ptr(ws), int(ws_bytes), _stream(stream)), "moe_ffn_wgrad")
 
 
 def moe_peak_mfma_size() -> int:

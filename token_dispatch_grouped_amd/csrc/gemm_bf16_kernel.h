@@ -53,7 +53,9 @@
 
 namespace moe {
 
-enum { EPI_STORE = 0, EPI_SWIGLU_FWD = 1, EPI_SWIGLU_BWD = 2, EPI_ACC_F32 = 3 };
+enum { EPI_STORE = 0, EPI_SWIGLU_FWD = 1, EPI_SWIGLU_BWD = 2, EPI_ACC_F32 = 3, EPI_ST_F32 = 4 };
+// EPI_ST_F32 writes what EPI_ACC_F32 adds (the dense block's weight gradients)
+constexpr bool epi_f32(int epi) { return epi == EPI_ACC_F32 || epi == EPI_ST_F32; }
 
 struct GemmParams {
   const bf16_t *A;
@@ -179,6 +181,19 @@ MOE_DEVICE void epilogue(const GemmParams &p, f32x16_t (&acc)[WM / 32][WN / 32],
         for (int v = 0; v < 16; ++v) cur[v] = nxt[v];
       }
     }
+    return;
+  } else if constexpr (EPI == EPI_ST_F32) {
+    float *C = (float *)p.C + (int64_t)e * p.strideC;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const int c = n_tile * BN + wn * WN + j * 32 + l32;
+          const int r = wm * WM + i * 32 + 8 * (v >> 2) + 4 * lhi + (v & 3);
+          if (r < m_valid && c < p.N) C[(int64_t)(m0 + r) * p.ldc + c] = acc[i][j][v];
+        }
     return;
   } else {  // the bf16 epilogues
 
@@ -647,8 +662,8 @@ MOE_DEVICE void gg_tile(const GemmParams &p, u32x4_t *lds, int e, int m0, int n_
   static_assert(WAVES_M * WAVES_N == NW, "wavefront grid must cover the tile");
   constexpr int FM = WM / 32, FN = WN / 32;
   static_assert(EPI != EPI_SWIGLU_FWD || (FN % 2) == 0, "gate/up pairs need an even fragment count");
-  static_assert(RAGGED_K == (EPI == EPI_ACC_F32), "weight gradients are the ragged-K products");
-  constexpr bool SWAP = EPI != EPI_ACC_F32;
+  static_assert(RAGGED_K == epi_f32(EPI), "weight gradients are the ragged-K products");
+  constexpr bool SWAP = !epi_f32(EPI);
   using OpA = Operand<BM, AKM, NW, BK, RAGGED_K>;
   using OpB = Operand<BN, BKM, NW, BK, RAGGED_K>;
   constexpr int STAGE_BYTES = OpA::BYTES + OpB::BYTES;
@@ -825,8 +840,8 @@ __global__ __launch_bounds__(NW * 64, 1) void gg_dma_kernel(GemmParams p) {
   static_assert(WAVES_M * WAVES_N == NW, "wavefront grid must cover the tile");
   constexpr int FM = WM / 32, FN = WN / 32;
   static_assert(EPI != EPI_SWIGLU_FWD || (FN % 2) == 0, "gate/up pairs need an even fragment count");
-  static_assert(RAGGED_K == (EPI == EPI_ACC_F32), "weight gradients are the ragged-K products");
-  constexpr bool SWAP = EPI != EPI_ACC_F32;
+  static_assert(RAGGED_K == epi_f32(EPI), "weight gradients are the ragged-K products");
+  constexpr bool SWAP = !epi_f32(EPI);
   using OpA = Operand<BM, AKM, NW, BK, RAGGED_K>;
   using OpB = Operand<BN, BKM, NW, BK, RAGGED_K>;
   constexpr int STAGE_BYTES = OpA::BYTES + OpB::BYTES;

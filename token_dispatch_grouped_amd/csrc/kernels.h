@@ -111,6 +111,40 @@ hipError_t launch_aux_loss(const float *logits, const int32_t *counts, float *lo
                            float *partial, int64_t T, int E, int k, float alpha, float beta, bool accumulate,
                            hipStream_t s);
 
+// ----- RMS norm and the 8-bit block form (norm.hip) -----
+struct RmsNormArgs {
+  const void *x, *residual, *w;  // forward; residual may be NULL
+  void *r, *y, *y_scale;         // y_scale: the 8-bit block form, or NULL
+  float *rstd;                   // forward: written; backward: read
+  const void *dy, *dres;         // backward (r is read); dres may be NULL
+  void *dx;
+  float *dw, *partial;
+  int64_t T;
+  int d;
+  float eps;
+  bool bf16, accumulate;
+};
+hipError_t launch_rmsnorm_fwd(const RmsNormArgs &a, hipStream_t s);
+hipError_t launch_rmsnorm_bwd(const RmsNormArgs &a, hipStream_t s);
+hipError_t launch_mx8_quantize(const void *x, void *q, void *scale, int64_t rows, int d, bool bf16, hipStream_t s);
+
+// ----- dense gated feed-forward block (ffn.hip, ffn_wgrad.hip) -----
+struct FfnArgs {
+  const void *x, *w_gu, *w_down, *add;                 // add may be NULL
+  const void *x_scale, *w_gu_scale, *w_down_scale;     // mx8
+  void *h, *a, *a_scale, *y;                           // forward: h may be NULL
+  const void *dy;                                      // backward (h, a are read)
+  void *dh, *dx;
+  float *dw_gu, *dw_down;
+  void *partial;
+  int64_t T;
+  int d, F;
+  bool mx8, accumulate;
+};
+hipError_t launch_ffn_dense_fwd(const FfnArgs &a, hipStream_t s);
+hipError_t launch_ffn_dense_dgrad(const FfnArgs &a, hipStream_t s);
+hipError_t launch_ffn_dense_wgrad(const FfnArgs &a, hipStream_t s);
+
 // ----- expert-parallel exchange (ep.hip) -----
 struct EpPtrs {
   void *p[kEpMaxRanks];

@@ -638,6 +638,204 @@ moe_status moe_ep_exchange_loopback(int32_t ep, int32_t d, int32_t dtype, void *
   return MOE_OK;
 }
 
+moe_status moe_rmsnorm_workspace_size(const moe_norm_shape *shape, size_t *bwd_ws) {
+  std::string why;
+  const moe_status st = validate_norm(shape, &why);
+  if (st != MOE_OK) return report(st, why);
+  if (bwd_ws) *bwd_ws = norm_workspace(*shape);
+  return MOE_OK;
+}
+
+moe_status moe_rmsnorm_fwd(const moe_norm_shape *shape, const void *x, const void *residual, const void *weight,
+                           void *r, void *y, void *y_scale, float *rstd, moe_stream_t stream) {
+  moe::AbiRange range("moe_rmsnorm_fwd");
+  std::string why;
+  moe_status st = validate_norm(shape, &why);
+  if (st != MOE_OK) return report(st, why);
+  const moe_norm_shape &s = *shape;
+  if (s.T == 0) return MOE_OK;
+  const bool res = residual != nullptr;
+  const PtrArg args[] = {{"x", x, true, false},   {"residual", residual, false, false},
+                         {"weight", weight, true, false}, {"r", r, res, !res},
+                         {"y", y, true, false},   {"y_scale", y_scale, false, false},
+                         {"rstd", rstd, true, false}};
+  st = validate_ptrs(args, 7, &why);
+  if (st != MOE_OK) return report(st, why);
+  RmsNormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.w = weight;
+  a.r = r;
+  a.y = y;
+  a.y_scale = y_scale;
+  a.rstd = rstd;
+  a.T = s.T;
+  a.d = s.d;
+  a.eps = s.eps;
+  a.bf16 = s.dtype == MOE_DTYPE_BF16;
+  return hip_status(launch_rmsnorm_fwd(a, as_stream(stream)), "rmsnorm_fwd");
+}
+
+moe_status moe_rmsnorm_bwd(const moe_norm_shape *shape, const void *dy, const void *r, const void *weight,
+                           const float *rstd, const void *dres, void *dx, float *dw, void *ws, size_t ws_bytes,
+                           moe_stream_t stream) {
+  moe::AbiRange range("moe_rmsnorm_bwd");
+  std::string why;
+  moe_status st = validate_norm(shape, &why);
+  if (st != MOE_OK) return report(st, why);
+  const moe_norm_shape &s = *shape;
+  const bool overwrite = (s.flags & MOE_NORM_OVERWRITE_DW) != 0;
+  if (s.T == 0 && !overwrite) return MOE_OK;
+  const bool some = s.T > 0;
+  const PtrArg args[] = {{"dy", dy, some, false},         {"r", r, some, false},
+                         {"weight", weight, some, false}, {"rstd", rstd, some, false},
+                         {"dres", dres, false, false},    {"dx", dx, some, false},
+                         {"dw", dw, true, false}};
+  st = validate_ptrs(args, 7, &why);
+  if (st != MOE_OK) return report(st, why);
+  st = validate_workspace(ws, ws_bytes, norm_workspace(s), &why);
+  if (st != MOE_OK) return report(st, why);
+  RmsNormArgs a{};
+  a.dy = dy;
+  a.r = const_cast<void *>(r);
+  a.w = weight;
+  a.rstd = const_cast<float *>(rstd);
+  a.dres = dres;
+  a.dx = dx;
+  a.dw = dw;
+  a.partial = static_cast<float *>(ws);
+  a.T = s.T;
+  a.d = s.d;
+  a.bf16 = s.dtype == MOE_DTYPE_BF16;
+  a.accumulate = !overwrite;
+  return hip_status(launch_rmsnorm_bwd(a, as_stream(stream)), "rmsnorm_bwd");
+}
+
+moe_status moe_mx8_quantize(int64_t rows, int32_t cols, int32_t dtype, const void *x, void *q, void *scale,
+                            moe_stream_t stream) {
+  moe::AbiRange range("moe_mx8_quantize");
+  std::string why;
+  moe_status st = validate_mx8(rows, cols, dtype, &why);
+  if (st != MOE_OK) return report(st, why);
+  if (rows == 0) return MOE_OK;
+  const PtrArg args[] = {{"x", x, true, false}, {"q", q, true, false}, {"scale", scale, true, false}};
+  st = validate_ptrs(args, 3, &why);
+  if (st != MOE_OK) return report(st, why);
+  return hip_status(launch_mx8_quantize(x, q, scale, rows, cols, dtype == MOE_DTYPE_BF16, as_stream(stream)),
+                    "mx8_quantize");
+}
+
+moe_status moe_ffn_workspace_size(const moe_ffn_shape *shape, size_t *fwd_ws, size_t *wgrad_ws) {
+  std::string why;
+  const moe_status st = validate_ffn(shape, &why);
+  if (st != MOE_OK) return report(st, why);
+  const FfnWorkspace w = ffn_workspace(*shape);
+  if (fwd_ws) *fwd_ws = w.fwd_total;
+  if (wgrad_ws) *wgrad_ws = w.wgrad_total;
+  return MOE_OK;
+}
+
+moe_status moe_ffn_fwd(const moe_ffn_shape *shape, const void *x, const void *x_scale, const void *w_gu,
+                       const void *w_gu_scale, const void *w_down, const void *w_down_scale, const void *add, void *h,
+                       void *a, void *y, void *ws, size_t ws_bytes, moe_stream_t stream) {
+  moe::AbiRange range("moe_ffn_fwd");
+  std::string why;
+  moe_status st = validate_ffn(shape, &why);
+  if (st != MOE_OK) return report(st, why);
+  const moe_ffn_shape &s = *shape;
+  if (s.T == 0) return MOE_OK;
+  const bool mx8 = s.dtype == MOE_DTYPE_MX8;
+  const bool keep = !mx8 && (h || a);
+  const PtrArg args[] = {{"x", x, true, false},           {"x_scale", x_scale, mx8, !mx8},
+                         {"w_gu", w_gu, true, false},     {"w_gu_scale", w_gu_scale, mx8, !mx8},
+                         {"w_down", w_down, true, false}, {"w_down_scale", w_down_scale, mx8, !mx8},
+                         {"add", add, false, false},      {"h", h, keep, mx8},
+                         {"a", a, keep, mx8},             {"y", y, true, false}};
+  st = validate_ptrs(args, 10, &why);
+  if (st != MOE_OK) return report(st, why);
+  const FfnWorkspace w = ffn_workspace(s);
+  if (!keep) st = validate_workspace(ws, ws_bytes, w.fwd_total, &why);
+  if (st != MOE_OK) return report(st, why);
+  FfnArgs f{};
+  f.x = x;
+  f.x_scale = x_scale;
+  f.w_gu = w_gu;
+  f.w_gu_scale = w_gu_scale;
+  f.w_down = w_down;
+  f.w_down_scale = w_down_scale;
+  f.add = add;
+  f.h = h;
+  f.a = keep ? a : ws;
+  f.a_scale = mx8 ? static_cast<char *>(ws) + w.fwd_a : nullptr;
+  f.y = y;
+  f.T = s.T;
+  f.d = s.d;
+  f.F = s.F;
+  f.mx8 = mx8;
+  return hip_status(launch_ffn_dense_fwd(f, as_stream(stream)), "ffn_fwd");
+}
+
+moe_status moe_ffn_dgrad(const moe_ffn_shape *shape, const void *dy, const void *h, const void *w_gu,
+                         const void *w_down, const void *add, void *dh, void *dx, moe_stream_t stream) {
+  moe::AbiRange range("moe_ffn_dgrad");
+  std::string why;
+  moe_status st = validate_ffn(shape, &why);
+  if (st != MOE_OK) return report(st, why);
+  const moe_ffn_shape &s = *shape;
+  if (s.dtype != MOE_DTYPE_BF16) return report(MOE_ERR_UNSUPPORTED, "moe_ffn_dgrad: dtype must be MOE_DTYPE_BF16");
+  if (s.T == 0) return MOE_OK;
+  const PtrArg args[] = {{"dy", dy, true, false},         {"h", h, true, false},     {"w_gu", w_gu, true, false},
+                         {"w_down", w_down, true, false}, {"add", add, false, false}, {"dh", dh, true, false},
+                         {"dx", dx, true, false}};
+  st = validate_ptrs(args, 7, &why);
+  if (st != MOE_OK) return report(st, why);
+  FfnArgs f{};
+  f.dy = dy;
+  f.h = const_cast<void *>(h);
+  f.w_gu = w_gu;
+  f.w_down = w_down;
+  f.add = add;
+  f.dh = dh;
+  f.dx = dx;
+  f.T = s.T;
+  f.d = s.d;
+  f.F = s.F;
+  return hip_status(launch_ffn_dense_dgrad(f, as_stream(stream)), "ffn_dgrad");
+}
+
+moe_status moe_ffn_wgrad(const moe_ffn_shape *shape, const void *dy, const void *x, const void *a, const void *dh,
+                         float *dw_gu, float *dw_down, void *ws, size_t ws_bytes, moe_stream_t stream) {
+  moe::AbiRange range("moe_ffn_wgrad");
+  std::string why;
+  moe_status st = validate_ffn(shape, &why);
+  if (st != MOE_OK) return report(st, why);
+  const moe_ffn_shape &s = *shape;
+  if (s.dtype != MOE_DTYPE_BF16) return report(MOE_ERR_UNSUPPORTED, "moe_ffn_wgrad: dtype must be MOE_DTYPE_BF16");
+  const bool overwrite = (s.flags & MOE_FFN_OVERWRITE_DW) != 0;
+  if (s.T == 0 && !overwrite) return MOE_OK;
+  const bool some = s.T > 0;
+  const PtrArg args[] = {{"dy", dy, some, false}, {"x", x, some, false},         {"a", a, some, false},
+                         {"dh", dh, some, false}, {"dw_gu", dw_gu, true, false}, {"dw_down", dw_down, true, false}};
+  st = validate_ptrs(args, 6, &why);
+  if (st != MOE_OK) return report(st, why);
+  const FfnWorkspace w = ffn_workspace(s);
+  st = validate_workspace(ws, ws_bytes, w.wgrad_total, &why);
+  if (st != MOE_OK) return report(st, why);
+  FfnArgs f{};
+  f.dy = dy;
+  f.x = x;
+  f.a = const_cast<void *>(a);
+  f.dh = const_cast<void *>(dh);
+  f.dw_gu = dw_gu;
+  f.dw_down = dw_down;
+  f.partial = ws;
+  f.T = s.T;
+  f.d = s.d;
+  f.F = s.F;
+  f.accumulate = !overwrite;
+  return hip_status(launch_ffn_dense_wgrad(f, as_stream(stream)), "ffn_wgrad");
+}
+
 static int device_cus() {
   int dev = 0, n = 0;
   if (hipGetDevice(&dev) != hipSuccess) return 0;

@@ -165,4 +165,73 @@ moe_status validate_aux(const moe_aux_config *c, std::string *why) {
   return MOE_OK;
 }
 
+static moe_status validate_rows(int64_t T, int32_t d, std::string *why) {
+  if (T < 0) return fail(why, MOE_ERR_INVALID_ARGUMENT, "T < 0");
+  if (d <= 0) return fail(why, MOE_ERR_INVALID_ARGUMENT, "d must be positive");
+  if (d % 64 != 0 || d > 65536) return fail(why, MOE_ERR_UNSUPPORTED, "d must be a multiple of 64, at most 65536");
+  // a 256-thread workgroup per row: 2^24 rows fill a grid of 2^32 threads
+  if (T >= ((int64_t)1 << 24)) return fail(why, MOE_ERR_UNSUPPORTED, "T >= 2^24");
+  return MOE_OK;
+}
+
+moe_status validate_norm(const moe_norm_shape *s, std::string *why) {
+  if (!s) return fail(why, MOE_ERR_INVALID_ARGUMENT, "norm shape is NULL");
+  const moe_status st = validate_rows(s->T, s->d, why);
+  if (st != MOE_OK) return st;
+  if (s->dtype != MOE_DTYPE_F32 && s->dtype != MOE_DTYPE_BF16)
+    return fail(why, MOE_ERR_UNSUPPORTED, "dtype must be MOE_DTYPE_F32 or MOE_DTYPE_BF16");
+  if (s->flags & ~(uint32_t)MOE_NORM_OVERWRITE_DW) return fail(why, MOE_ERR_UNSUPPORTED, "unknown norm flag bits");
+  if (!std::isfinite(s->eps) || s->eps <= 0.f) return fail(why, MOE_ERR_INVALID_ARGUMENT, "eps must be positive and finite");
+  return MOE_OK;
+}
+
+size_t norm_workspace(const moe_norm_shape &s) { return align256((size_t)norm_bwd_blocks(s.T) * (size_t)s.d * 4); }
+
+moe_status validate_mx8(int64_t rows, int32_t cols, int32_t dtype, std::string *why) {
+  if (rows < 0) return fail(why, MOE_ERR_INVALID_ARGUMENT, "negative row count");
+  if (cols <= 0) return fail(why, MOE_ERR_INVALID_ARGUMENT, "cols must be positive");
+  if (cols % 64 != 0 || cols > 65536) return fail(why, MOE_ERR_UNSUPPORTED, "cols must be a multiple of 64, at most 65536");
+  if (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16)
+    return fail(why, MOE_ERR_UNSUPPORTED, "dtype must be MOE_DTYPE_F32 or MOE_DTYPE_BF16");
+  // one thread per 16 bytes
+  if (rows >= ((int64_t)1 << 32) || rows * (cols / (dtype == MOE_DTYPE_BF16 ? 8 : 4)) >= ((int64_t)1 << 32) - 256)
+    return fail(why, MOE_ERR_UNSUPPORTED, "matrix too large for one launch (2^32 threads per grid dimension)");
+  return MOE_OK;
+}
+
+moe_status validate_ffn(const moe_ffn_shape *s, std::string *why) {
+  if (!s) return fail(why, MOE_ERR_INVALID_ARGUMENT, "ffn shape is NULL");
+  moe_status st = validate_rows(s->T, s->d, why);
+  if (st != MOE_OK) return st;
+  if (s->F <= 0) return fail(why, MOE_ERR_INVALID_ARGUMENT, "F must be positive");
+  if (s->F % 64 != 0 || s->F > 65536) return fail(why, MOE_ERR_UNSUPPORTED, "F must be a multiple of 64, at most 65536");
+  if (s->dtype != MOE_DTYPE_BF16 && s->dtype != MOE_DTYPE_MX8)
+    return fail(why, MOE_ERR_UNSUPPORTED, "dtype must be MOE_DTYPE_BF16 or MOE_DTYPE_MX8");
+  if (s->dtype == MOE_DTYPE_MX8 && (s->d % 128 != 0 || s->F % 128 != 0))
+    return fail(why, MOE_ERR_UNSUPPORTED, "d and F must be multiples of 128 in MOE_DTYPE_MX8");
+  if (s->flags & ~(uint32_t)MOE_FFN_OVERWRITE_DW) return fail(why, MOE_ERR_UNSUPPORTED, "unknown ffn flag bits");
+  // the largest grid: 128 x 128 tiles of [T, 2F] or [T, d], row tiles in whole groups, 256 threads each
+  const int64_t wide = s->d > 2 * (int64_t)s->F ? s->d : 2 * (int64_t)s->F;
+  const int64_t tiles = ceil_div(ceil_div(s->T, 128), kGemmGroupM) * kGemmGroupM * ceil_div(wide, 128);
+  if ((tiles + 8) * 256 >= ((int64_t)1 << 32))
+    return fail(why, MOE_ERR_UNSUPPORTED, "problem too large for one launch (2^32 threads per grid dimension)");
+  return MOE_OK;
+}
+
+FfnWorkspace ffn_workspace(const moe_ffn_shape &s) {
+  FfnWorkspace w{};
+  const bool mx8 = s.dtype == MOE_DTYPE_MX8;
+  const size_t n = (size_t)s.T * (size_t)s.F;
+  w.fwd_a = align256(mx8 ? n : 2 * n);
+  w.fwd_scale = mx8 ? align256(n / 32) : 0;
+  w.fwd_total = w.fwd_a + w.fwd_scale;
+  if (!mx8 && s.T > 0) {
+    const FfnSlices gu = ffn_wgrad_slices(s.T, 2 * s.F, s.d), dn = ffn_wgrad_slices(s.T, s.d, s.F);
+    const size_t m = (size_t)s.d * (size_t)s.F * 4;
+    const size_t a = gu.most > 1 ? 2 * m * (size_t)gu.most : 0, b = dn.most > 1 ? m * (size_t)dn.most : 0;
+    w.wgrad_total = align256(a > b ? a : b);
+  }
+  return w;
+}
+
 }  // namespace moe

@@ -77,6 +77,47 @@ moe_status validate_aux(const moe_aux_config *cfg, std::string *why);
 // when d > 0 is given; capacities >= 0 and below 2^31 rows.
 moe_status validate_ep(int32_t ep, int32_t e_local, int32_t d, int32_t dtype, int64_t rows_cap, std::string *why);
 
+// ----- RMS norm, 8-bit block form, dense feed-forward block -----
+constexpr int kNormWaveRows = 2048;     // rows from which a norm row is one wavefront's
+constexpr int kNormBwdBlocks = 1024;    // workgroups (partial rows) of the norm's backward pass at most
+constexpr int kNormBwdMinRows = 8;      // rows of a workgroup of the norm's backward pass at least
+inline int norm_bwd_blocks(int64_t T) {
+  const int64_t b = ceil_div(T, kNormBwdMinRows);
+  return (int)(b < kNormBwdBlocks ? b : kNormBwdBlocks);
+}
+
+// Token slices of a weight gradient [M, N] of the dense block: enough for
+// kWgradUnits workgroups, each slice at least kWgradMinRows tokens.
+constexpr int kWgradUnits = 512;
+constexpr int kWgradMinRows = 512;
+struct FfnSlices {
+  int slices, chunk;
+  int most;  // slices of the workspace: never fewer for a larger T
+};
+inline FfnSlices ffn_wgrad_slices(int64_t T, int M, int N) {
+  const int64_t tiles = ceil_div(M, kGemmBM) * ceil_div(N, kGemmBN);
+  int64_t n = kWgradUnits / tiles;
+  if (n > T / kWgradMinRows) n = T / kWgradMinRows;
+  if (n < 1) n = 1;
+  const int64_t chunk = ceil_div(ceil_div(T, n), 64) * 64;
+  return FfnSlices{(int)ceil_div(T, chunk), (int)chunk, (int)n};
+}
+
+// Shape of a norm call (d a multiple of 64, at most 65536; T < 2^24).
+moe_status validate_norm(const moe_norm_shape *s, std::string *why);
+size_t norm_workspace(const moe_norm_shape &s);
+
+// Rows and columns of the 8-bit block form (cols a multiple of 64).
+moe_status validate_mx8(int64_t rows, int32_t cols, int32_t dtype, std::string *why);
+
+// Shape of a dense feed-forward call, and its workspaces.
+moe_status validate_ffn(const moe_ffn_shape *s, std::string *why);
+struct FfnWorkspace {
+  size_t fwd_a, fwd_scale, fwd_total;  // a (bf16, or e4m3 and its scales)
+  size_t wgrad_total;                  // fp32 partial sums of the larger weight gradient
+};
+FfnWorkspace ffn_workspace(const moe_ffn_shape &s);
+
 // Workspace check: NULL or short -> MOE_ERR_WORKSPACE (a zero requirement
 // accepts anything).
 moe_status validate_workspace(const void *ws, size_t have, size_t need, std::string *why);
