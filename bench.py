@@ -76,7 +76,7 @@ TRAFFIC_SOURCES = ("token_dispatch_grouped_amd/csrc/gemm_bf16.hip", "token_dispa
                    "token_dispatch_grouped_amd/csrc/gemm_bf16_kernel.h", "token_dispatch_grouped_amd/csrc/gemm_common.h",
                    "token_dispatch_grouped_amd/csrc/common.h", "token_dispatch_grouped_amd/build.py")
 TRAFFIC = {
-    "sources_sha256": "067a92a18b39e804fee7f26981ce4fc3b6adb7ffa73806de7ba8d6514463f899",
+    "sources_sha256": "cf78f584b93dae92ae024aa5245707a655710d1252bf9b43d86820ec53ebda2a",
     "workload": "ep_share_32k",
     "bytes_per_launch": {
         # read GiB + write GiB, x 2^30

@@ -5,9 +5,11 @@
 // into slices: every (tile, slice) pair is a workgroup that writes fp32
 // partial sums to the workspace, and a second kernel adds the slices in
 // order (no atomics: results are the same bits run to run).
-#include "gemm_bf16_kernel.h"
+#include "ffn_wide.h"
 
 namespace moe {
+
+template hipError_t run_ffn_wide<false, EPI_SWIGLU_FWD>(GemmParams, hipStream_t);
 
 constexpr int kWgBM = kGemmBM, kWgBN = kGemmBN;
 

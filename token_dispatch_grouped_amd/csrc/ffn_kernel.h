@@ -226,9 +226,16 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void ffn_tile_kernel
         for (int j = 0; j < FN; ++j) fb[(ks + 1) & 1][j] = load_b(slot, ks + 1, j);
       }
       mma(i, g & 1, ks & 1, ks);
+      if (F8) __builtin_amdgcn_sched_barrier(0);  // reads run one group ahead, not more
     }
     // every fragment of this stage is in registers: its slot takes stage
     // kt + 2 once all wavefronts are here, and stage kt + 1 has landed
+    if constexpr (F8) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(acc[i][j]));  // no product sinks below the branch
+    }
     __builtin_amdgcn_sched_barrier(0);
     wait_lds();
     wait_vm<0>();
@@ -239,9 +246,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void ffn_tile_kernel
     // read of a stale slot)
     const int nslot = slot ^ 1;
     fa[0] = load_a(nslot, 0, 0);
-    frag_t nb[FN];
 #pragma unroll
-    for (int j = 0; j < FN; ++j) nb[j] = load_b(nslot, 0, j);
+    for (int j = 0; j < FN; ++j) fb[0][j] = load_b(nslot, 0, j);
     int nsa[FM], nsb[FN];
     if (F8) {
 #pragma unroll
@@ -250,8 +256,6 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void ffn_tile_kernel
       for (int j = 0; j < FN; ++j) nsb[j] = load_scale(nslot, BM + wn * WN + j * 32 + l32);
     }
     mma(FM - 1, 1, (KS - 1) & 1, KS - 1);
-#pragma unroll
-    for (int j = 0; j < FN; ++j) fb[0][j] = nb[j];
     if (F8) {
 #pragma unroll
       for (int i = 0; i < FM; ++i) sa[i] = nsa[i];
@@ -277,7 +281,10 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void ffn_tile_kernel
     const u32x4_t w = {e0, e1, o0, o1};
     Elem<bf16_t>::unpack(w, v);
   };
-  const int row_l = wm * WM + l32;
+  int el32 = l32, ehi = lhi;
+  // opaque: no address below is formed above the main loop and held there
+  asm volatile("" : "+v"(el32), "+v"(ehi));
+  const int row_l = wm * WM + el32;
   if constexpr (EPI == FFN_STORE) {
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
@@ -288,7 +295,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void ffn_tile_kernel
       for (int j = 0; j < FN; ++j)
 #pragma unroll
         for (int gp = 0; gp < 2; ++gp) {
-          const int c = n_tile * BN + wn * WN + j * 32 + 16 * gp + 8 * lhi;
+          const int c = n_tile * BN + wn * WN + j * 32 + 16 * gp + 8 * ehi;
           const bool ok = rok && c < p.N;
           float v[8];
 #pragma unroll
@@ -317,7 +324,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void ffn_tile_kernel
         if (p.C) {
 #pragma unroll
           for (int gp = 0; gp < 2; ++gp) {
-            const int c = c0 + 16 * gp + 8 * lhi;
+            const int c = c0 + 16 * gp + 8 * ehi;
             float gv[8], uv[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
@@ -352,14 +359,14 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void ffn_tile_kernel
           swap32(w[0], w[2]);  // dwords 0 and 1 of the row's 8 (4 and 5 in the upper half)
           swap32(w[1], w[3]);  // dwords 2 and 3 (6 and 7)
           if (rok && c0 < p.N) {
-            uint8_t *a8 = reinterpret_cast<uint8_t *>(p.C2) + row * p.F + c0 + 16 * lhi;
+            uint8_t *a8 = reinterpret_cast<uint8_t *>(p.C2) + row * p.F + c0 + 16 * ehi;
             st16(a8, u32x4_t{w[0], w[2], w[1], w[3]});
-            if (lhi == 0) p.C2s[row * (p.F / kMx8Block) + c0 / kMx8Block] = (uint8_t)code;
+            if (ehi == 0) p.C2s[row * (p.F / kMx8Block) + c0 / kMx8Block] = (uint8_t)code;
           }
         } else {
 #pragma unroll
           for (int gp = 0; gp < 2; ++gp) {
-            const int c = c0 + 16 * gp + 8 * lhi;
+            const int c = c0 + 16 * gp + 8 * ehi;
             const u32x4_t o = pack_chunk(a + 8 * gp);
             if (rok && c < p.N) st16(p.C2 + row * p.F + c, o);
           }
@@ -376,7 +383,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void ffn_tile_kernel
       for (int j = 0; j < FN; ++j)
 #pragma unroll
         for (int gp = 0; gp < 2; ++gp) {
-          const int c = n_tile * BN + wn * WN + j * 32 + 16 * gp + 8 * lhi;
+          const int c = n_tile * BN + wn * WN + j * 32 + 16 * gp + 8 * ehi;
           const bool ok = rok && c < p.N;
           const int cc = ok ? c : 0;
           float hg[8], hu[8], dg[8], du[8];

@@ -53,16 +53,18 @@
 
 namespace moe {
 
-enum { EPI_STORE = 0, EPI_SWIGLU_FWD = 1, EPI_SWIGLU_BWD = 2, EPI_ACC_F32 = 3, EPI_ST_F32 = 4 };
+enum { EPI_STORE = 0, EPI_SWIGLU_FWD = 1, EPI_SWIGLU_BWD = 2, EPI_ACC_F32 = 3, EPI_ST_F32 = 4, EPI_STORE_ADD = 5 };
 // EPI_ST_F32 writes what EPI_ACC_F32 adds (the dense block's weight gradients)
 constexpr bool epi_f32(int epi) { return epi == EPI_ACC_F32 || epi == EPI_ST_F32; }
+// EPI_STORE_ADD stores the sum of the product and `add` (the dense block)
+constexpr bool epi_store(int epi) { return epi == EPI_STORE || epi == EPI_STORE_ADD; }
 
 struct GemmParams {
   const bf16_t *A;
   const bf16_t *B;
   void *C;                // bf16 output, or fp32 accumulator (EPI_ACC_F32)
   bf16_t *C2;             // EPI_SWIGLU_FWD: the activation a
-  const bf16_t *H;        // EPI_SWIGLU_BWD: saved h
+  const bf16_t *H;        // EPI_SWIGLU_BWD: saved h; EPI_STORE_ADD: the addend, laid out as C
   const int32_t *offsets;
   const int32_t *order;   // ragged K: experts by descending row count
   int E;
@@ -245,7 +247,33 @@ MOE_DEVICE void epilogue(const GemmParams &p, f32x16_t (&acc)[WM / 32][WN / 32],
     }
   };
 
-  if (EPI == EPI_STORE) {
+  if constexpr (EPI == EPI_STORE_ADD) {
+    // the addend in the accumulators' layout, 8 bytes a lane, one row block's
+    // loads in flight together; clamped addresses feed masked outputs only
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int r = wm * WM + i * 32 + l32;
+      const bf16_t *row = p.H + (crow0 + (r < m_valid ? r : m_valid - 1)) * p.ldc;
+      uint2 v[FN][4];
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int c = n_tile * BN + wn * WN + j * 32 + 8 * g + 4 * lhi;
+          v[j][g] = *reinterpret_cast<const uint2 *>(row + (c < p.N ? c : p.N - 4));
+        }
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          acc[i][j][4 * g] += __uint_as_float(v[j][g].x << 16);
+          acc[i][j][4 * g + 1] += __uint_as_float(v[j][g].x & 0xffff0000u);
+          acc[i][j][4 * g + 2] += __uint_as_float(v[j][g].y << 16);
+          acc[i][j][4 * g + 3] += __uint_as_float(v[j][g].y & 0xffff0000u);
+        }
+    }
+  }
+  if (epi_store(EPI)) {
     const int n0 = n_tile * BN;
 #pragma unroll
     for (int h = 0; h < WAVES_M; ++h) {
@@ -670,7 +698,7 @@ MOE_DEVICE void gg_tile(const GemmParams &p, u32x4_t *lds, int e, int m0, int n_
   constexpr int RING_BYTES = STAGES * STAGE_BYTES;
   // staging: one wavefront row in ring slot 1 for EPI_STORE, the whole tile
   // for EPI_SWIGLU_FWD and EPI_SWIGLU_BWD (two band buffers)
-  constexpr int STG_BYTES = EPI == EPI_STORE ? STAGE_BYTES + WM * BN * 2 : !SWAP ? 0 : BM * BN * 2;
+  constexpr int STG_BYTES = epi_store(EPI) ? STAGE_BYTES + WM * BN * 2 : !SWAP ? 0 : BM * BN * 2;
   constexpr int LDS_BYTES = RING_BYTES > STG_BYTES ? RING_BYTES : STG_BYTES;
   static_assert(LDS_BYTES <= 160 * 1024, "LDS budget of one workgroup");
   // opaque copy: nothing derived from the thread index is hoisted out of a
@@ -824,7 +852,7 @@ MOE_DEVICE void gg_tile(const GemmParams &p, u32x4_t *lds, int e, int m0, int n_
       nb.issue(0, p.ldb, kdim, lds0 + OpA::BYTES, wave_u);
     }
   };
-  if (EPI == EPI_STORE) issue_next();
+  if (epi_store(EPI)) issue_next();
   epilogue<BM, BN, WM, WN, EPI, NT, STAGE_BYTES>(p, acc, lds, e, m0, n_tile, m_valid, crow0, wm, wn, issue_next);
 }
 
@@ -848,7 +876,7 @@ __global__ __launch_bounds__(NW * 64, 1) void gg_dma_kernel(GemmParams p) {
   constexpr int RING_BYTES = STAGES * STAGE_BYTES;
   // staging: one wavefront row in ring slot 1 for EPI_STORE, the whole tile
   // for EPI_SWIGLU_FWD and EPI_SWIGLU_BWD (two band buffers)
-  constexpr int STG_BYTES = EPI == EPI_STORE ? STAGE_BYTES + WM * BN * 2 : !SWAP ? 0 : BM * BN * 2;
+  constexpr int STG_BYTES = epi_store(EPI) ? STAGE_BYTES + WM * BN * 2 : !SWAP ? 0 : BM * BN * 2;
   constexpr int LDS_BYTES = RING_BYTES > STG_BYTES ? RING_BYTES : STG_BYTES;
   static_assert(LDS_BYTES <= 160 * 1024, "LDS budget of one workgroup");
   // the weight gradients also run edge tiles, whose ring takes all 160 KB
