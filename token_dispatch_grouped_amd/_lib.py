@@ -154,11 +154,22 @@ def ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_stream_query = None
+
+
 def current_stream() -> Optional[int]:
-    import torch
-    if not torch.cuda.is_available():
-        return None
-    return torch.cuda.current_stream().cuda_stream
+    """The current torch stream of the current device, as a handle. Asked of
+    torch's bindings themselves: building a torch.cuda.Stream for each call
+    costs as much as a launch (3.4 against 0.14 us)."""
+    global _stream_query
+    if _stream_query is None:
+        import torch
+        if not torch.cuda.is_available():
+            return None
+        torch.cuda.init()
+        _stream_query = (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
+    stream, device = _stream_query
+    return stream(device())
 
 
 def make_shape(T: int, d: int, E: int, k: int, F: int, dtype: int, flags: int = 0) -> moe_shape:
