@@ -71,7 +71,8 @@ def _weights(rng, d, F):
 
 # one token, the few-row kernels' steps, tiles with ragged rows and columns, more row tiles than a group
 SHAPES = [(1, 64, 64), (1, 2048, 1408), (2, 64, 192), (15, 192, 64), (16, 128, 128), (17, 256, 320), (33, 1024, 704),
-          (48, 320, 1472), (64, 512, 256), (65, 576, 128), (129, 128, 320), (300, 192, 448), (700, 1088, 576),
+          (48, 320, 1472), (64, 512, 256), (65, 576, 128), (144, 128, 320), (145, 192, 448), (300, 1088, 576), (500, 704, 1024),
+          (700, 1088, 576), (1000, 1984, 1408),
           (1300, 512, 1408)]
 # enough tiles for the 256 x 256 tile in the products with N = d, in those with N = F, and several rounds of it
 LARGE = [(4200, 2048, 128), (6001, 128, 1472), (9000, 320, 1088)]
@@ -203,7 +204,8 @@ def _values(q, s):
 
 
 @pytest.mark.parametrize("T,d,F", [(1, 128, 128), (1, 4096, 2816), (3, 256, 384), (16, 128, 640), (17, 512, 256),
-                                   (48, 384, 1408), (64, 1024, 128), (65, 128, 256), (129, 640, 384),
+                                   (48, 384, 1408), (64, 1024, 128), (65, 128, 256), (144, 640, 384),
+                                   (145, 128, 1152), (250, 1920, 2816),
                                    (700, 1152, 640), (1300, 512, 1408), (4200, 2048, 128), (6001, 128, 1408),
                                    (9000, 384, 1152)])
 def test_forward_mx8(T, d, F):

@@ -1,6 +1,7 @@
 // Host launchers of the dense gated feed-forward block (ffn_kernel.h has the
 // kernels and the mathematics): forward in bf16 and in the 8-bit block form,
 // and the gradient of the input.
+#include "ffn_few.h"
 #include "ffn_kernel.h"
 #include "ffn_wide.h"
 
@@ -21,6 +22,7 @@ static FfnTileParams gateup_params(const FfnArgs &a) {
   p.As = (const uint8_t *)a.x_scale;
   p.Bs = (const uint8_t *)a.w_gu_scale;
   p.C2s = (uint8_t *)a.a_scale;
+  p.a32 = (float *)a.a32;
   return p;
 }
 
@@ -64,34 +66,80 @@ static hipError_t wide_store(const FfnTileParams &t, hipStream_t s) {
   return t.add ? wide<BKM, EPI_STORE_ADD>(t, s) : wide<BKM, EPI_STORE>(t, s);
 }
 
-// Whether a product of M rows and N columns takes the 256 x 256 tile. A card
-// of `cus` compute units runs one such tile per CU at a time, or two of the
-// 128 x 128 ones; a round of the large tiles takes 1.45 times a round of the
-// small ones and does twice the work (measured at K = 2048, N = 2816: 56-59
-// against 38 us a round in bf16, 57 against 40 us in MX8). So the tile whose
-// rounds take less time wins: the small one where the large leaves most CUs
-// idle. n_small, n_large: output columns of a small and a large tile.
-static bool large_tile(int M, int N, int n_small, int n_large) {
+// The kernel of a product of M rows whose B operand has NB rows (gate/up: 2F).
+//   few     M <= kFfnFewTokens, forward: reads the weights once (ffn_few.h)
+//   small   64 x 64 tiles, 4 k groups a workgroup
+//   narrow  64 x 128 tiles, 2 k groups
+//   half    64 x 128 tiles, two workgroups a CU
+//   square  128 x 128 tiles, two workgroups a CU
+//   large   256 x 256 tiles
+// While a tile shape does not fill the card, a smaller one ends sooner (its
+// workgroups are bound by the latency of a stage, which the k groups hide).
+// Forward at d = 2048, F = 1408, us: 256 tokens small 20.6, narrow 26.7,
+// half 29.7, square 39; 512: narrow 28.0, half 29.8, square 40; 1024: half
+// 35, square 41; 1536: square 49, half 55. In the 8-bit form (d = 4096, F =
+// 2816) gate/up 192 tokens narrow 20.3, small 26.7, down small 12.7, narrow
+// 16.3; 512 tokens in all half 46.8, square 47.5; 1024 square 63, half 71.
+// Few against the next: 192 tokens 17.8 against 20.5, 256: 23.6 against 20.6;
+// 8-bit 128: 30.8 against 32.2, 192: 37.9 against 32.2.
+// Large against square: a round of large tiles (one a CU) takes 1.45 times a
+// round of square ones (two a CU) and does twice the work (56-59 against 38 us
+// in bf16 at K = 2048, 57 against 40 us in the 8-bit form).
+enum Tile { kFew, kSmall, kNarrow, kHalf, kSquare, kLarge };
+
+static Tile choose(int M, int NB, bool mx8, bool swiglu, bool kmajor) {
+  if (!kmajor && M <= kFfnFewTokens) return kFew;
   const int64_t cus = persistent_grid();
-  const int64_t small = ceil_div(M, 128) * ceil_div(N, n_small), large = ceil_div(M, 256) * ceil_div(N, n_large);
-  return 145 * ceil_div(large, cus) < 100 * ceil_div(small, 2 * cus);
+  const auto tiles = [&](int bm, int bn) { return ceil_div(M, bm) * ceil_div(NB, bn); };
+  if (!kmajor && !(mx8 && swiglu) && tiles(64, 64) <= cus) return kSmall;
+  if (tiles(64, 128) <= cus) return kNarrow;
+  if (!kmajor && !mx8 && tiles(64, 128) <= 2 * cus) return kHalf;
+  return 145 * ceil_div(tiles(256, 256), cus) < 100 * ceil_div(tiles(128, 128), 2 * cus) ? kLarge : kSquare;
 }
 
 static hipError_t gateup(const FfnTileParams &p, bool mx8, hipStream_t s) {
-  const bool large = large_tile(p.M, p.N, 64, 128);
-  if (mx8)
-    return large ? run_ffn_tile<true, 256, 256, 128, 64, false, FFN_SWIGLU_FWD>(p, s)
-                 : run_ffn_tile<true, 128, 128, 64, 64, false, FFN_SWIGLU_FWD>(p, s);
-  return large ? wide<false, EPI_SWIGLU_FWD>(p, s)
-               : run_ffn_tile<false, 128, 128, 64, 64, false, FFN_SWIGLU_FWD>(p, s);
+  const Tile t = choose(p.M, 2 * p.N, mx8, true, false);
+  if (mx8) {
+    switch (t) {
+      case kFew: {
+        const hipError_t err = run_ffn_few<true, FFN_SWIGLU_FWD>(p, s);
+        if (err != hipSuccess) return err;
+        return launch_mx8_quantize(p.a32, p.C2, p.C2s, p.M, p.F, false, s);
+      }
+      case kNarrow: return run_ffn_tile<true, 64, 128, 32, 64, 2, 3, false, FFN_SWIGLU_FWD>(p, s);
+      case kLarge: return run_ffn_tile<true, 256, 256, 128, 64, 1, 2, false, FFN_SWIGLU_FWD>(p, s);
+      default: return run_ffn_tile<true, 128, 128, 64, 64, 1, 2, false, FFN_SWIGLU_FWD>(p, s);
+    }
+  }
+  switch (t) {
+    case kFew: return run_ffn_few<false, FFN_SWIGLU_FWD>(p, s);
+    case kSmall: return run_ffn_tile<false, 64, 64, 32, 64, 4, 2, false, FFN_SWIGLU_FWD>(p, s);
+    case kNarrow: return run_ffn_tile<false, 64, 128, 32, 64, 2, 3, false, FFN_SWIGLU_FWD>(p, s);
+    case kHalf: return run_ffn_tile<false, 64, 128, 32, 64, 1, 3, false, FFN_SWIGLU_FWD>(p, s);
+    case kLarge: return wide<false, EPI_SWIGLU_FWD>(p, s);
+    default: return run_ffn_tile<false, 128, 128, 64, 64, 1, 2, false, FFN_SWIGLU_FWD>(p, s);
+  }
 }
 
 static hipError_t down(const FfnTileParams &p, bool mx8, hipStream_t s) {
-  const bool large = large_tile(p.M, p.N, 128, 256);
-  if (mx8)
-    return large ? run_ffn_tile<true, 256, 256, 128, 64, false, FFN_STORE>(p, s)
-                 : run_ffn_tile<true, 128, 128, 64, 64, false, FFN_STORE>(p, s);
-  return large ? wide_store<false>(p, s) : run_ffn_tile<false, 128, 128, 64, 64, false, FFN_STORE>(p, s);
+  const Tile t = choose(p.M, p.N, mx8, false, false);
+  if (mx8) {
+    switch (t) {
+      case kFew: return run_ffn_few<true, FFN_STORE>(p, s);
+      case kSmall: return run_ffn_tile<true, 64, 64, 32, 64, 4, 2, false, FFN_STORE>(p, s);
+      case kNarrow: return run_ffn_tile<true, 64, 128, 32, 64, 2, 3, false, FFN_STORE>(p, s);
+      case kLarge: return run_ffn_tile<true, 256, 256, 128, 64, 1, 2, false, FFN_STORE>(p, s);
+      default: return run_ffn_tile<true, 128, 128, 64, 64, 1, 2, false, FFN_STORE>(p, s);
+    }
+  }
+  switch (t) {
+    case kFew: return run_ffn_few<false, FFN_STORE>(p, s);
+    case kSmall: return run_ffn_tile<false, 64, 64, 32, 64, 4, 2, false, FFN_STORE>(p, s);
+    case kNarrow: return run_ffn_tile<false, 64, 128, 32, 64, 2, 3, false, FFN_STORE>(p, s);
+    case kHalf: return run_ffn_tile<false, 64, 128, 32, 64, 1, 3, false, FFN_STORE>(p, s);
+    case kLarge: return wide_store<false>(p, s);
+    default: return run_ffn_tile<false, 128, 128, 64, 64, 1, 2, false, FFN_STORE>(p, s);
+  }
 }
 
 hipError_t launch_ffn_dense_fwd(const FfnArgs &a, hipStream_t s) {
@@ -104,10 +152,26 @@ hipError_t launch_ffn_dense_fwd(const FfnArgs &a, hipStream_t s) {
   return down(down_params(a), a.mx8, s);
 }
 
+static hipError_t down_dgrad(const FfnTileParams &p, hipStream_t s) {
+  switch (choose(p.M, p.N, false, false, true)) {
+    case kNarrow: return run_ffn_tile<false, 64, 128, 32, 64, 2, 2, true, FFN_SWIGLU_BWD>(p, s);
+    case kLarge: return wide<true, EPI_SWIGLU_BWD>(p, s);
+    default: return run_ffn_tile<false, 128, 128, 64, 64, 1, 2, true, FFN_SWIGLU_BWD>(p, s);
+  }
+}
+
+static hipError_t gateup_dgrad(const FfnTileParams &p, hipStream_t s) {
+  switch (choose(p.M, p.N, false, false, true)) {
+    case kNarrow: return run_ffn_tile<false, 64, 128, 32, 64, 2, 2, true, FFN_STORE>(p, s);
+    case kLarge: return wide_store<true>(p, s);
+    default: return run_ffn_tile<false, 128, 128, 64, 64, 1, 2, true, FFN_STORE>(p, s);
+  }
+}
+
 hipError_t launch_ffn_dense_dgrad(const FfnArgs &a, hipStream_t s) {
+  FfnTileParams p{};
   {
     LaunchScope scope("ffn_down_dgrad", s);
-    FfnTileParams p{};
     p.A = (const bf16_t *)a.dy;
     p.B = (const bf16_t *)a.w_down;
     p.C = (bf16_t *)a.dh;
@@ -119,13 +183,11 @@ hipError_t launch_ffn_dense_dgrad(const FfnArgs &a, hipStream_t s) {
     p.lda = a.d;
     p.ldb = a.F;
     p.ldc = 2 * (int64_t)a.F;
-    const hipError_t err = large_tile(p.M, p.N, 128, 256)
-                               ? wide<true, EPI_SWIGLU_BWD>(p, s)
-                               : run_ffn_tile<false, 128, 128, 64, 64, true, FFN_SWIGLU_BWD>(p, s);
+    const hipError_t err = down_dgrad(p, s);
     if (err != hipSuccess) return err;
   }
   LaunchScope scope("ffn_gateup_dgrad", s);
-  FfnTileParams p{};
+  p = FfnTileParams{};
   p.A = (const bf16_t *)a.dh;
   p.B = (const bf16_t *)a.w_gu;
   p.C = (bf16_t *)a.dx;
@@ -137,8 +199,7 @@ hipError_t launch_ffn_dense_dgrad(const FfnArgs &a, hipStream_t s) {
   p.lda = 2 * (int64_t)a.F;
   p.ldb = a.d;
   p.ldc = a.d;
-  return large_tile(p.M, p.N, 128, 256) ? wide_store<true>(p, s)
-                                        : run_ffn_tile<false, 128, 128, 64, 64, true, FFN_STORE>(p, s);
+  return gateup_dgrad(p, s);
 }
 
 }  // namespace moe

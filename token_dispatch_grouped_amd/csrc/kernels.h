@@ -132,7 +132,7 @@ hipError_t launch_mx8_quantize(const void *x, void *q, void *scale, int64_t rows
 struct FfnArgs {
   const void *x, *w_gu, *w_down, *add;                 // add may be NULL
   const void *x_scale, *w_gu_scale, *w_down_scale;     // mx8
-  void *h, *a, *a_scale, *y;                           // forward: h may be NULL
+  void *h, *a, *a_scale, *a32, *y;                     // forward: h may be NULL
   const void *dy;                                      // backward (h, a are read)
   void *dh, *dx;
   float *dw_gu, *dw_down;

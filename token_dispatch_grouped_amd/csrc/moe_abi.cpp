@@ -767,6 +767,7 @@ moe_status moe_ffn_fwd(const moe_ffn_shape *shape, const void *x, const void *x_
   f.h = h;
   f.a = keep ? a : ws;
   f.a_scale = mx8 ? static_cast<char *>(ws) + w.fwd_a : nullptr;
+  f.a32 = mx8 ? static_cast<char *>(ws) + w.fwd_a + w.fwd_scale : nullptr;
   f.y = y;
   f.T = s.T;
   f.d = s.d;

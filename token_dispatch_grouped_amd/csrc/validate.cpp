@@ -210,7 +210,8 @@ moe_status validate_ffn(const moe_ffn_shape *s, std::string *why) {
   if (s->dtype == MOE_DTYPE_MX8 && (s->d % 128 != 0 || s->F % 128 != 0))
     return fail(why, MOE_ERR_UNSUPPORTED, "d and F must be multiples of 128 in MOE_DTYPE_MX8");
   if (s->flags & ~(uint32_t)MOE_FFN_OVERWRITE_DW) return fail(why, MOE_ERR_UNSUPPORTED, "unknown ffn flag bits");
-  // the largest grid: 128 x 128 tiles of [T, 2F] or [T, d], row tiles in whole groups, 256 threads each
+  // the largest grid: 128 x 128 tiles of [T, 2F] or [T, d], row tiles in whole
+  // groups, 256 threads each (smaller tiles are only for grids of a few CUs' worth)
   const int64_t wide = s->d > 2 * (int64_t)s->F ? s->d : 2 * (int64_t)s->F;
   const int64_t tiles = ceil_div(ceil_div(s->T, 128), kGemmGroupM) * kGemmGroupM * ceil_div(wide, 128);
   if ((tiles + 8) * 256 >= ((int64_t)1 << 32))
@@ -224,7 +225,9 @@ FfnWorkspace ffn_workspace(const moe_ffn_shape &s) {
   const size_t n = (size_t)s.T * (size_t)s.F;
   w.fwd_a = align256(mx8 ? n : 2 * n);
   w.fwd_scale = mx8 ? align256(n / 32) : 0;
-  w.fwd_total = w.fwd_a + w.fwd_scale;
+  const size_t few = (size_t)(s.T < kFfnFewTokens ? s.T : kFfnFewTokens);
+  w.fwd_a32 = mx8 ? align256(few * (size_t)s.F * 4) : 0;
+  w.fwd_total = w.fwd_a + w.fwd_scale + w.fwd_a32;
   if (!mx8 && s.T > 0) {
     const FfnSlices gu = ffn_wgrad_slices(s.T, 2 * s.F, s.d), dn = ffn_wgrad_slices(s.T, s.d, s.F);
     const size_t m = (size_t)s.d * (size_t)s.F * 4;

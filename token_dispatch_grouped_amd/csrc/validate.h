@@ -86,6 +86,9 @@ inline int norm_bwd_blocks(int64_t T) {
   return (int)(b < kNormBwdBlocks ? b : kNormBwdBlocks);
 }
 
+// Tokens up to which the block's forward runs the few-token kernels.
+constexpr int kFfnFewTokens = 144;
+
 // Token slices of a weight gradient [M, N] of the dense block: enough for
 // kWgradUnits workgroups, each slice at least kWgradMinRows tokens.
 constexpr int kWgradUnits = 512;
@@ -113,7 +116,8 @@ moe_status validate_mx8(int64_t rows, int32_t cols, int32_t dtype, std::string *
 // Shape of a dense feed-forward call, and its workspaces.
 moe_status validate_ffn(const moe_ffn_shape *s, std::string *why);
 struct FfnWorkspace {
-  size_t fwd_a, fwd_scale, fwd_total;  // a (bf16, or e4m3 and its scales)
+  size_t fwd_a, fwd_scale, fwd_a32;    // a (bf16, or e4m3, its scales, and few tokens' a in fp32)
+  size_t fwd_total;
   size_t wgrad_total;                  // fp32 partial sums of the larger weight gradient
 };
 FfnWorkspace ffn_workspace(const moe_ffn_shape &s);
