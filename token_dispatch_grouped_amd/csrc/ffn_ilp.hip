@@ -1,10 +1,15 @@
 // Weight gradients of the dense gated feed-forward block:
-//   dw_down [d,F]  (+)= dy^T a     dw_gu [2F,d] (+)= dh^T x     (fp32)
+//   dw_gu [2F,d] (+)= dh^T x     dw_down [d,F]  (+)= dy^T a     (fp32)
 // The grouped products' 256 x 256 tile with both operands k-major. There are
 // few output tiles and a long sum over the tokens, so the tokens are split
-// into slices: every (tile, slice) pair is a workgroup that writes fp32
-// partial sums to the workspace, and a second kernel adds the slices in
-// order (no atomics: results are the same bits run to run).
+// into slices: every (slice, tile) pair of either product is a workgroup of
+// one launch that writes fp32 partial sums to the workspace (straight to dw
+// where there is one slice and nothing to add to), and a second launch adds
+// the slices in order (no atomics: the same bits run to run). The tiles of a
+// slice are neighbours, so that the workgroups of an XCD share operand rows.
+//
+// This file also holds the gate/up forward on the same tile, for the sake of
+// the instruction scheduling that both are compiled with.
 #include "ffn_wide.h"
 
 namespace moe {
@@ -13,86 +18,105 @@ template hipError_t run_ffn_wide<false, EPI_SWIGLU_FWD>(GemmParams, hipStream_t)
 
 constexpr int kWgBM = kGemmBM, kWgBN = kGemmBN;
 
-template <int EPI>
-__global__ __launch_bounds__(512, 1) void ffn_wgrad_kernel(GemmParams p, int T, int chunk) {
+struct WgradParams {
+  GemmParams g[2];  // dw_gu, dw_down; total: the product's workgroups
+  int T, chunk;
+};
+
+__global__ __launch_bounds__(512, 1) void ffn_wgrad_kernel(WgradParams w) {
   __shared__ u32x4_t lds[2 * (kWgBM + kWgBN) * kStageK * 2 / 16];
   int lo, hi;
-  xcd_range(blockIdx.x & 7, p.total, lo, hi);
-  const int id = lo + (int)(blockIdx.x >> 3);
+  xcd_range(blockIdx.x & 7, w.g[0].total + w.g[1].total, lo, hi);
+  int id = lo + (int)(blockIdx.x >> 3);
   if (id >= hi) return;
+  const int which = id >= w.g[0].total ? 1 : 0;
+  if (which) id -= w.g[0].total;
+  const GemmParams &p = w.g[which];
   const int tiles = p.m_tiles * p.n_tiles;
   const int slice = id / tiles, r = id - slice * tiles;
   const int mt = r / p.n_tiles, nt = r - mt * p.n_tiles;
-  const int row0 = slice * chunk;
-  const int kdim = min(chunk, T - row0);
+  const int row0 = slice * w.chunk;
+  const int kdim = min(w.chunk, w.T - row0);
   const int m0 = mt * kWgBM;
   auto none = [&](NextTile &nx) { nx.valid = false; };
-  gg_tile<kWgBM, kWgBN, kWgBM / 2, kWgBN / 4, 8, true, true, EPI, true, kStageK, kStages>(
+  gg_tile<kWgBM, kWgBN, kWgBM / 2, kWgBN / 4, 8, true, true, EPI_ST_F32, true, kStageK, kStages>(
       p, lds, slice, m0, nt, min(kWgBM, p.M - m0), kdim, 0, p.A + (int64_t)row0 * p.lda + m0,
       p.B + (int64_t)row0 * p.ldb, false, none);
 }
 
-__global__ __launch_bounds__(256) void ffn_wgrad_reduce_kernel(const float *partial, float *dw, int64_t n4, int slices,
-                                                               int accumulate) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n4) return;
+struct WgradReduce {
+  const float *partial[2];
+  float *dw[2];
+  int64_t n4[2];  // 16-byte chunks of the gradient; 0: nothing to do
+  int slices, accumulate;
+};
+
+__global__ __launch_bounds__(256) void ffn_wgrad_reduce_kernel(WgradReduce p) {
+  int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int which = i >= p.n4[0] ? 1 : 0;
+  if (which) i -= p.n4[0];
+  if (i >= p.n4[which]) return;
+  const f32x4_t *src = reinterpret_cast<const f32x4_t *>(p.partial[which]);
+  f32x4_t *dst = reinterpret_cast<f32x4_t *>(p.dw[which]);
   f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-  if (accumulate) v = reinterpret_cast<const f32x4_t *>(dw)[i];
-  for (int s = 0; s < slices; ++s) {
-    const f32x4_t q = reinterpret_cast<const f32x4_t *>(partial)[s * n4 + i];
+  if (p.accumulate) v = dst[i];
+#pragma unroll 4
+  for (int s = 0; s < p.slices; ++s) {
+    const f32x4_t q = src[s * p.n4[which] + i];
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] += q[e];
   }
-  reinterpret_cast<f32x4_t *>(dw)[i] = v;
+  dst[i] = v;
 }
 
-static hipError_t wgrad(const char *name, const char *reduce_name, const void *A, const void *B, float *dw, int M,
-                        int N, const FfnArgs &a, hipStream_t s) {
-  GemmParams p{};
-  p.A = (const bf16_t *)A;
-  p.B = (const bf16_t *)B;
-  p.M = M;
-  p.N = N;
-  p.lda = M;
-  p.ldb = N;
-  p.ldc = N;
-  p.strideC = (int64_t)M * N;
-  p.m_tiles = (M + kWgBM - 1) / kWgBM;
-  p.n_tiles = (N + kWgBN - 1) / kWgBN;
-  const FfnSlices sl = ffn_wgrad_slices(a.T, M, N);
-  p.total = p.m_tiles * p.n_tiles * sl.slices;
-  const dim3 grid((unsigned)(ceil_div(p.total, 8) * 8));
-  {
-    LaunchScope scope(name, s);
-    if (sl.slices > 1) {
-      p.C = a.partial;
-      ffn_wgrad_kernel<EPI_ST_F32><<<grid, 512, 0, s>>>(p, (int)a.T, sl.chunk);
-    } else {
-      p.C = dw;
-      if (a.accumulate) ffn_wgrad_kernel<EPI_ACC_F32><<<grid, 512, 0, s>>>(p, (int)a.T, sl.chunk);
-      else ffn_wgrad_kernel<EPI_ST_F32><<<grid, 512, 0, s>>>(p, (int)a.T, sl.chunk);
-    }
-    const hipError_t err = hipGetLastError();
-    if (err != hipSuccess || sl.slices == 1) return err;
-  }
-  LaunchScope scope(reduce_name, s);
-  const int64_t n4 = (int64_t)M * N / 4;
-  ffn_wgrad_reduce_kernel<<<(unsigned)ceil_div(n4, 256), 256, 0, s>>>((const float *)a.partial, dw, n4, sl.slices,
-                                                                     a.accumulate ? 1 : 0);
+static hipError_t reduce(const WgradReduce &r, hipStream_t s) {
+  const int64_t n = r.n4[0] + r.n4[1];
+  if (n == 0) return hipSuccess;
+  LaunchScope scope("ffn_wgrad_reduce", s);
+  ffn_wgrad_reduce_kernel<<<(unsigned)ceil_div(n, 256), 256, 0, s>>>(r);
   return hipGetLastError();
 }
 
 hipError_t launch_ffn_dense_wgrad(const FfnArgs &a, hipStream_t s) {
-  if (a.T == 0) {  // no tokens: the gradients are zero
-    const int64_t n = (int64_t)a.d * a.F / 4;
-    LaunchScope scope("ffn_wgrad_zero", s);
-    ffn_wgrad_reduce_kernel<<<(unsigned)ceil_div(n, 256), 256, 0, s>>>(nullptr, a.dw_down, n, 0, 0);
-    ffn_wgrad_reduce_kernel<<<(unsigned)ceil_div(2 * n, 256), 256, 0, s>>>(nullptr, a.dw_gu, 2 * n, 0, 0);
-    return hipGetLastError();
+  WgradParams w{};
+  WgradReduce r{};
+  w.T = (int)a.T;
+  r.accumulate = a.accumulate ? 1 : 0;
+  const FfnWgrad plan = ffn_wgrad_plan(a.T, a.d, a.F);
+  const int slices = plan.slices;  // 0 without tokens
+  r.slices = slices;
+  w.chunk = plan.chunk;
+  float *ws = static_cast<float *>(a.partial);
+  for (int i = 0; i < 2; ++i) {
+    GemmParams &p = w.g[i];
+    p.A = (const bf16_t *)(i == 0 ? a.dh : a.dy);
+    p.B = (const bf16_t *)(i == 0 ? a.x : a.a);
+    p.M = i == 0 ? 2 * a.F : a.d;
+    p.N = i == 0 ? a.d : a.F;
+    p.lda = p.M;
+    p.ldb = p.N;
+    p.ldc = p.N;
+    p.strideC = (int64_t)p.M * p.N;
+    p.m_tiles = (p.M + kWgBM - 1) / kWgBM;
+    p.n_tiles = (p.N + kWgBN - 1) / kWgBN;
+    p.total = p.m_tiles * p.n_tiles * slices;
+    float *dw = i == 0 ? a.dw_gu : a.dw_down;
+    const bool direct = slices == 1 && !a.accumulate;
+    p.C = direct ? dw : ws;
+    if (direct) continue;
+    r.partial[i] = ws;
+    r.dw[i] = dw;
+    r.n4[i] = p.strideC / 4;  // the sum of no slice is zero
+    ws += slices * p.strideC;
   }
-  const hipError_t err = wgrad("ffn_down_wgrad", "ffn_down_wgrad_reduce", a.dy, a.a, a.dw_down, a.d, a.F, a, s);
-  if (err != hipSuccess) return err;
-  return wgrad("ffn_gateup_wgrad", "ffn_gateup_wgrad_reduce", a.dh, a.x, a.dw_gu, 2 * a.F, a.d, a, s);
+  const int total = w.g[0].total + w.g[1].total;
+  if (total > 0) {
+    LaunchScope scope("ffn_wgrad", s);
+    ffn_wgrad_kernel<<<(unsigned)(ceil_div(total, 8) * 8), 512, 0, s>>>(w);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  return reduce(r, s);
 }
 
 }  // namespace moe

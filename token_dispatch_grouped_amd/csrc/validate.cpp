@@ -219,6 +219,38 @@ moe_status validate_ffn(const moe_ffn_shape *s, std::string *why) {
   return MOE_OK;
 }
 
+FfnWgrad ffn_wgrad_plan(int64_t T, int d, int F) {
+  const int64_t tiles = ceil_div(2 * (int64_t)F, kGemmBM) * ceil_div(d, kGemmBN) +
+                        ceil_div(d, kGemmBM) * ceil_div(F, kGemmBN);
+  int64_t most = kWgradUnits / tiles;
+  if (most > T / kWgradMinRows) most = T / kWgradMinRows;
+  if (most < 1) most = 1;
+  // Time of n slices in us, on 256 CUs with one tile each at a time: a stage
+  // of 64 tokens takes 1.35 us while every workgroup has a CU from the start,
+  // 1.6 us beyond (never more than 1060 TFLOP/s in all), and a second launch
+  // writes and reads n times the gradients at 4 TB/s. At d = 2048, F = 1408
+  // measured with 1 and 3 slices: 51 and 75 us at 2000 tokens, 145 and 149 at
+  // 7001, 349 and 312 at 16384, 694 and 589 at 32768.
+  const double bytes = 12.0 * d * F, least = 6.0 * (double)T * d * F / 1.06e9;
+  int64_t best = 1;
+  double best_us = 0.0;
+  for (int64_t n = 1; n <= most; ++n) {
+    const int64_t rounds = ceil_div(tiles * n, 256), stages = ceil_div(ceil_div(T, n), 64);
+    double us = (double)(rounds * stages) * (rounds > 1 ? 1.6 : 1.35);
+    if (us < least) us = least;
+    if (n > 1) us += 5.0 + (double)n * bytes / 4e6;
+    if (n == 1 || us < best_us) {
+      best = n;
+      best_us = us;
+    }
+  }
+  FfnWgrad w{};
+  w.most = (int)most;
+  w.chunk = (int)(ceil_div(ceil_div(T, best), 64) * 64);
+  w.slices = T > 0 ? (int)ceil_div(T, w.chunk) : 0;
+  return w;
+}
+
 FfnWorkspace ffn_workspace(const moe_ffn_shape &s) {
   FfnWorkspace w{};
   const bool mx8 = s.dtype == MOE_DTYPE_MX8;
@@ -228,12 +260,8 @@ FfnWorkspace ffn_workspace(const moe_ffn_shape &s) {
   const size_t few = (size_t)(s.T < kFfnFewTokens ? s.T : kFfnFewTokens);
   w.fwd_a32 = mx8 ? align256(few * (size_t)s.F * 4) : 0;
   w.fwd_total = w.fwd_a + w.fwd_scale + w.fwd_a32;
-  if (!mx8 && s.T > 0) {
-    const FfnSlices gu = ffn_wgrad_slices(s.T, 2 * s.F, s.d), dn = ffn_wgrad_slices(s.T, s.d, s.F);
-    const size_t m = (size_t)s.d * (size_t)s.F * 4;
-    const size_t a = gu.most > 1 ? 2 * m * (size_t)gu.most : 0, b = dn.most > 1 ? m * (size_t)dn.most : 0;
-    w.wgrad_total = align256(a > b ? a : b);
-  }
+  if (!mx8 && s.T > 0)
+    w.wgrad_total = align256((size_t)ffn_wgrad_plan(s.T, s.d, s.F).most * 3 * (size_t)s.d * (size_t)s.F * 4);
   return w;
 }
 

@@ -89,22 +89,17 @@ inline int norm_bwd_blocks(int64_t T) {
 // Tokens up to which the block's forward runs the few-token kernels.
 constexpr int kFfnFewTokens = 144;
 
-// Token slices of a weight gradient [M, N] of the dense block: enough for
-// kWgradUnits workgroups, each slice at least kWgradMinRows tokens.
+// Token slices of the dense block's two weight gradients (dw_gu [2F,d], then
+// dw_down [d,F]): at most as many as make kWgradUnits workgroups, each slice at
+// least kWgradMinRows tokens; among those the count whose time estimate is
+// least (ffn_wgrad_plan).
 constexpr int kWgradUnits = 512;
-constexpr int kWgradMinRows = 512;
-struct FfnSlices {
-  int slices, chunk;
-  int most;  // slices of the workspace: never fewer for a larger T
+constexpr int kWgradMinRows = 256;
+struct FfnWgrad {
+  int slices, chunk;  // tokens of a slice
+  int most;           // slices of the workspace: never fewer for a larger T
 };
-inline FfnSlices ffn_wgrad_slices(int64_t T, int M, int N) {
-  const int64_t tiles = ceil_div(M, kGemmBM) * ceil_div(N, kGemmBN);
-  int64_t n = kWgradUnits / tiles;
-  if (n > T / kWgradMinRows) n = T / kWgradMinRows;
-  if (n < 1) n = 1;
-  const int64_t chunk = ceil_div(ceil_div(T, n), 64) * 64;
-  return FfnSlices{(int)ceil_div(T, chunk), (int)chunk, (int)n};
-}
+FfnWgrad ffn_wgrad_plan(int64_t T, int d, int F);
 
 // Shape of a norm call (d a multiple of 64, at most 65536; T < 2^24).
 moe_status validate_norm(const moe_norm_shape *s, std::string *why);
@@ -118,7 +113,7 @@ moe_status validate_ffn(const moe_ffn_shape *s, std::string *why);
 struct FfnWorkspace {
   size_t fwd_a, fwd_scale, fwd_a32;    // a (bf16, or e4m3, its scales, and few tokens' a in fp32)
   size_t fwd_total;
-  size_t wgrad_total;                  // fp32 partial sums of the larger weight gradient
+  size_t wgrad_total;                  // fp32 partial sums of the two weight gradients
 };
 FfnWorkspace ffn_workspace(const moe_ffn_shape &s);
 
