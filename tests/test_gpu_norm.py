@@ -157,8 +157,8 @@ def test_zero_and_non_finite_rows():
 @pytest.mark.parametrize("T,d", SHAPES + [(8200, 128), (20011, 64)])
 def test_backward(T, d, bf16):
     """dx per element: every term of rstd (g - n mean(g n)) + dres with the fp32 error of its own size, the mean's
-    from a chain of d/64 + 16 additions of signed terms; dw: rows of a workgroup (T / 1024 + 1 of its 1, 4 or 8), then
-    64 partial rows a thread, then 16."""
+    from a chain of d/64 + 16 additions of signed terms; dw: T / 512 + 1 rows of a workgroup of at most 512 at most, its 4
+    slots, 512 / 64 partial rows a thread, then 64 threads."""
     import torch
     m = _moe()
     rng = np.random.default_rng(T * 5 + d)
@@ -180,7 +180,7 @@ def test_backward(T, d, bf16):
         terms = rstd[:, None] * (g + n * np.mean(g * n, axis=1, keepdims=True) * (d / 64 + 20) / 8)
         terms = terms + (0 if dres is None else np.abs(_h(dres)))
         assert np.all(np.abs(_h(dx) - dx64) <= 8 * U * terms + _half(bf16) * np.abs(dx64))
-        chain = T / 1024 + 1 + 8 + 64 + 16 + 4
+        chain = T / 512 + 1 + 4 + 8 + 64 + 4
         bar = chain * U * np.sum(np.abs(_h(dy)) * n, axis=0)
         assert np.all(np.abs(_h(dw) - dw64) <= bar)
         # accumulation, a repeat bit for bit, and dx in place of dy or dres

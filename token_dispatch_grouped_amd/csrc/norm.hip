@@ -16,6 +16,21 @@ namespace moe {
 
 constexpr int kNormThreads = 256;
 
+// Streams of more than half the 256 MB memory-side cache pass it by (NT):
+// 32768 x 2048 bf16 forward 94 -> 87 us, 16384 x 2048 to 8 bits 47 -> 40, 32768
+// x 4096 backward 212 -> 198. Smaller ones stay in it for whoever reads them
+// next, and are faster so (7001 x 1024 fp32 forward 10.5 against 12.2 us).
+constexpr int64_t kNormCachedBytes = (int64_t)128 << 20;
+template <bool NT>
+MOE_DEVICE u32x4_t ld16s(const void *p) {
+  return NT ? ld16_nt(p) : ld16(p);
+}
+template <bool NT>
+MOE_DEVICE void st16s(void *p, const u32x4_t &v) {
+  if (NT) st16_nt(p, v);
+  else st16(p, v);
+}
+
 // Sum over the TPR threads of a row, the same bits in every thread. TPR = 64
 // is one wavefront; 256 is the workgroup, through `part` (4 floats), which
 // must not be in use by an earlier sum.
@@ -64,7 +79,7 @@ struct NormFwdParams {
 };
 
 // A row in TPR threads, NV chunks of 16 bytes each.
-template <typename T, int TPR, int NV, bool MX8>
+template <typename T, int TPR, int NV, bool MX8, bool NT>
 __global__ __launch_bounds__(kNormThreads) void rmsnorm_fwd_kernel(NormFwdParams p) {
   constexpr int V = Elem<T>::kVec;
   __shared__ float part[kNormThreads / kWave];
@@ -79,8 +94,8 @@ __global__ __launch_bounds__(kNormThreads) void rmsnorm_fwd_kernel(NormFwdParams
   for (int j = 0; j < NV; ++j) {
     const int c = j * TPR + lane;
     const int cc = c < n ? c : 0;
-    xv[j] = ld16(x + cc * V);
-    if (res) rv[j] = ld16(res + cc * V);
+    xv[j] = ld16s<NT>(x + cc * V);
+    if (res) rv[j] = ld16s<NT>(res + cc * V);
   }
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -98,7 +113,7 @@ __global__ __launch_bounds__(kNormThreads) void rmsnorm_fwd_kernel(NormFwdParams
 #pragma unroll
       for (int i = 0; i < V; ++i) a[i] += b[i];
       xv[j] = Elem<T>::pack(a);  // rounded once: from here on r is what the row holds
-      if (c < n) st16((T *)p.r + row * p.d + c * V, xv[j]);
+      if (c < n) st16s<NT>((T *)p.r + row * p.d + c * V, xv[j]);
     }
     float a[V];
     Elem<T>::unpack(xv[j], a);
@@ -121,7 +136,7 @@ __global__ __launch_bounds__(kNormThreads) void rmsnorm_fwd_kernel(NormFwdParams
     if (MX8) {
       store_mx8<T>(a, (uint8_t *)p.y, p.y_scale, row, p.d, c, c < n);
     } else if (c < n) {
-      st16((T *)p.y + row * p.d + c * V, Elem<T>::pack(a));
+      st16s<NT>((T *)p.y + row * p.d + c * V, Elem<T>::pack(a));
     }
   }
 }
@@ -214,7 +229,7 @@ struct NormBwdParams {
 // The workgroups share the rows out evenly; a thread keeps the same columns
 // of every row and holds their sums of dy * n in registers, which become one
 // partial row per workgroup.
-template <typename T, int TPR, int NV>
+template <typename T, int TPR, int NV, bool NT>
 __global__ __launch_bounds__(kNormThreads) void rmsnorm_bwd_kernel(NormBwdParams p) {
   constexpr int V = Elem<T>::kVec;
   constexpr int RPB = kNormThreads / TPR;
@@ -233,19 +248,36 @@ __global__ __launch_bounds__(kNormThreads) void rmsnorm_bwd_kernel(NormBwdParams
     const int c = j * TPR + lane;
     wv[j] = ld16((const T *)p.w + (c < n ? c : 0) * V);
   }
-  int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RPB + slot; row < p.T; row += (int64_t)gridDim.x * RPB) {
+  // the next row's loads are in flight while this one is finished
+  u32x4_t gn[NV], rn[NV], en[NV];
+  float rstd_n = 0.f;
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  auto fetch = [&](int64_t row) {
     const int64_t base = row * p.d;
-    u32x4_t gv[NV], rv[NV], ev[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = j * TPR + lane;
       const int64_t o = base + (c < n ? c : 0) * V;
-      gv[j] = ld16((const T *)p.dy + o);
-      rv[j] = ld16((const T *)p.r + o);
-      if (p.dres) ev[j] = ld16((const T *)p.dres + o);
+      gn[j] = ld16s<NT>((const T *)p.dy + o);
+      rn[j] = ld16s<NT>((const T *)p.r + o);
+      if (p.dres) en[j] = ld16s<NT>((const T *)p.dres + o);
     }
-    const float rstd = p.rstd[row];
+    rstd_n = p.rstd[row];
+  };
+  int turn = 0;
+  const int64_t row0 = (int64_t)blockIdx.x * RPB + slot;
+  if (row0 < p.T) fetch(row0);
+  for (int64_t row = row0; row < p.T; row += step) {
+    const int64_t base = row * p.d;
+    u32x4_t gv[NV], rv[NV], ev[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      gv[j] = gn[j];
+      rv[j] = rn[j];
+      ev[j] = en[j];
+    }
+    const float rstd = rstd_n;
+    if (row + step < p.T) fetch(row + step);
     float dot = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -284,7 +316,7 @@ __global__ __launch_bounds__(kNormThreads) void rmsnorm_bwd_kernel(NormBwdParams
 #pragma unroll
         for (int i = 0; i < V; ++i) g[i] += e[i];
       }
-      st16((T *)p.dx + base + c * V, Elem<T>::pack(g));
+      st16s<NT>((T *)p.dx + base + c * V, Elem<T>::pack(g));
     }
   }
   // the slots' sums, in the order of the slots
@@ -365,48 +397,62 @@ __global__ __launch_bounds__(kNormThreads) void rmsnorm_bwd_long_kernel(NormBwdP
   }
 }
 
-// dw[c] (+)= the sum of the partial rows, in a fixed order: 16 threads take
-// every 16th partial row of a column, then their sums are added in turn.
+// dw (+)= the sum of the partial rows, in a fixed order: 64 threads take every
+// 64th partial row of 4 columns, then their sums are added in turn.
 __global__ __launch_bounds__(256) void rmsnorm_dw_reduce_kernel(const float *partial, float *dw, int rows, int d,
                                                                 int accumulate) {
-  __shared__ float s[16][17];
-  const int col = threadIdx.x & 15, grp = threadIdx.x >> 4;
-  const int c = blockIdx.x * 16 + col;  // d is a multiple of 64
-  float v = 0.f;
+  __shared__ f32x4_t s[64][5];
+  const int col = threadIdx.x & 3, grp = threadIdx.x >> 2;
+  const int c = blockIdx.x * 16 + col * 4;  // d is a multiple of 64
+  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-  for (int b = grp; b < rows; b += 16) v += partial[(int64_t)b * d + c];
+  for (int b = grp; b < rows; b += 64) {
+    const f32x4_t q = *reinterpret_cast<const f32x4_t *>(partial + (int64_t)b * d + c);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += q[e];
+  }
   s[grp][col] = v;
   __syncthreads();
   if (threadIdx.x >= 16) return;
   float sum = 0.f;
 #pragma unroll
-  for (int g = 0; g < 16; ++g) sum += s[g][col];
-  dw[c] = accumulate ? dw[c] + sum : sum;
+  for (int g = 0; g < 64; ++g) sum += s[g][threadIdx.x >> 2][threadIdx.x & 3];
+  float *out = dw + blockIdx.x * 16 + threadIdx.x;
+  *out = accumulate ? *out + sum : sum;
 }
 
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
 // Threads of a row: with few rows, as many as fill the row once (latency);
-// otherwise one wavefront, which needs no barrier.
-static bool wave_rows(int64_t T, int chunks) { return T >= kNormWaveRows && chunks <= 8 * kWave; }
+// otherwise one wavefront, which needs no barrier, up to 4 chunks a thread
+// (32768 x 4096 bf16 forward 187 us with 8, 176 with a workgroup a row), in the
+// backward pass, where a thread also holds column sums and the next row, up
+// to 2 (217 against 212 us there).
+static bool wave_rows(int64_t T, int chunks, int most) { return T >= kNormWaveRows && chunks <= most * kWave; }
 
-template <typename T, bool MX8>
+template <typename T, bool MX8, bool NT>
 static void fwd_dispatch(const NormFwdParams &p, hipStream_t s) {
   const int n = p.d / Elem<T>::kVec;
-  if (wave_rows(p.T, n)) {
+  if (wave_rows(p.T, n, 4)) {
     const dim3 g((unsigned)ceil_div(p.T, kNormThreads / kWave)), b(kNormThreads);
-    if (n <= kWave) rmsnorm_fwd_kernel<T, kWave, 1, MX8><<<g, b, 0, s>>>(p);
-    else if (n <= 2 * kWave) rmsnorm_fwd_kernel<T, kWave, 2, MX8><<<g, b, 0, s>>>(p);
-    else if (n <= 4 * kWave) rmsnorm_fwd_kernel<T, kWave, 4, MX8><<<g, b, 0, s>>>(p);
-    else rmsnorm_fwd_kernel<T, kWave, 8, MX8><<<g, b, 0, s>>>(p);
+    if (n <= kWave) rmsnorm_fwd_kernel<T, kWave, 1, MX8, NT><<<g, b, 0, s>>>(p);
+    else if (n <= 2 * kWave) rmsnorm_fwd_kernel<T, kWave, 2, MX8, NT><<<g, b, 0, s>>>(p);
+    else rmsnorm_fwd_kernel<T, kWave, 4, MX8, NT><<<g, b, 0, s>>>(p);
     return;
   }
   const dim3 g((unsigned)p.T), b(kNormThreads);
-  if (n <= kNormThreads) rmsnorm_fwd_kernel<T, kNormThreads, 1, MX8><<<g, b, 0, s>>>(p);
-  else if (n <= 2 * kNormThreads) rmsnorm_fwd_kernel<T, kNormThreads, 2, MX8><<<g, b, 0, s>>>(p);
-  else if (n <= 4 * kNormThreads) rmsnorm_fwd_kernel<T, kNormThreads, 4, MX8><<<g, b, 0, s>>>(p);
+  if (n <= kNormThreads) rmsnorm_fwd_kernel<T, kNormThreads, 1, MX8, NT><<<g, b, 0, s>>>(p);
+  else if (n <= 2 * kNormThreads) rmsnorm_fwd_kernel<T, kNormThreads, 2, MX8, NT><<<g, b, 0, s>>>(p);
+  else if (n <= 4 * kNormThreads) rmsnorm_fwd_kernel<T, kNormThreads, 4, MX8, NT><<<g, b, 0, s>>>(p);
   else rmsnorm_fwd_long_kernel<T, MX8><<<g, b, 0, s>>>(p);
+}
+
+template <typename T, bool MX8>
+static void fwd_streams(const NormFwdParams &p, hipStream_t s) {
+  const int64_t bytes = p.T * p.d * ((int64_t)sizeof(T) * (p.residual ? 3 : 1) + (MX8 ? 1 : sizeof(T)));
+  if (bytes > kNormCachedBytes) fwd_dispatch<T, MX8, true>(p, s);
+  else fwd_dispatch<T, MX8, false>(p, s);
 }
 
 hipError_t launch_rmsnorm_fwd(const RmsNormArgs &a, hipStream_t s) {
@@ -424,30 +470,35 @@ hipError_t launch_rmsnorm_fwd(const RmsNormArgs &a, hipStream_t s) {
   p.inv_d = 1.0f / (float)a.d;
   p.eps = a.eps;
   if (a.bf16) {
-    if (a.y_scale) fwd_dispatch<bf16_t, true>(p, s);
-    else fwd_dispatch<bf16_t, false>(p, s);
+    if (a.y_scale) fwd_streams<bf16_t, true>(p, s);
+    else fwd_streams<bf16_t, false>(p, s);
   } else {
-    if (a.y_scale) fwd_dispatch<float, true>(p, s);
-    else fwd_dispatch<float, false>(p, s);
+    if (a.y_scale) fwd_streams<float, true>(p, s);
+    else fwd_streams<float, false>(p, s);
   }
   return hipGetLastError();
 }
 
-template <typename T>
+template <typename T, bool NT>
 static void bwd_dispatch(const NormBwdParams &p, int blocks, hipStream_t s) {
   const int n = p.d / Elem<T>::kVec;
   const dim3 g((unsigned)blocks), b(kNormThreads);
-  if (wave_rows(p.T, n)) {
-    if (n <= kWave) rmsnorm_bwd_kernel<T, kWave, 1><<<g, b, 0, s>>>(p);
-    else if (n <= 2 * kWave) rmsnorm_bwd_kernel<T, kWave, 2><<<g, b, 0, s>>>(p);
-    else if (n <= 4 * kWave) rmsnorm_bwd_kernel<T, kWave, 4><<<g, b, 0, s>>>(p);
-    else rmsnorm_bwd_kernel<T, kWave, 8><<<g, b, 0, s>>>(p);
+  if (wave_rows(p.T, n, 2)) {
+    if (n <= kWave) rmsnorm_bwd_kernel<T, kWave, 1, NT><<<g, b, 0, s>>>(p);
+    else rmsnorm_bwd_kernel<T, kWave, 2, NT><<<g, b, 0, s>>>(p);
     return;
   }
-  if (n <= kNormThreads) rmsnorm_bwd_kernel<T, kNormThreads, 1><<<g, b, 0, s>>>(p);
-  else if (n <= 2 * kNormThreads) rmsnorm_bwd_kernel<T, kNormThreads, 2><<<g, b, 0, s>>>(p);
-  else if (n <= 4 * kNormThreads) rmsnorm_bwd_kernel<T, kNormThreads, 4><<<g, b, 0, s>>>(p);
+  if (n <= kNormThreads) rmsnorm_bwd_kernel<T, kNormThreads, 1, NT><<<g, b, 0, s>>>(p);
+  else if (n <= 2 * kNormThreads) rmsnorm_bwd_kernel<T, kNormThreads, 2, NT><<<g, b, 0, s>>>(p);
+  else if (n <= 4 * kNormThreads) rmsnorm_bwd_kernel<T, kNormThreads, 4, NT><<<g, b, 0, s>>>(p);
   else rmsnorm_bwd_long_kernel<T><<<g, b, 0, s>>>(p);
+}
+
+template <typename T>
+static void bwd_streams(const NormBwdParams &p, int blocks, hipStream_t s) {
+  const int64_t bytes = p.T * p.d * (int64_t)sizeof(T) * (p.dres ? 4 : 3);
+  if (bytes > kNormCachedBytes) bwd_dispatch<T, true>(p, blocks, s);
+  else bwd_dispatch<T, false>(p, blocks, s);
 }
 
 hipError_t launch_rmsnorm_bwd(const RmsNormArgs &a, hipStream_t s) {
@@ -465,8 +516,8 @@ hipError_t launch_rmsnorm_bwd(const RmsNormArgs &a, hipStream_t s) {
     p.T = a.T;
     p.d = a.d;
     p.inv_d = 1.0f / (float)a.d;
-    if (a.bf16) bwd_dispatch<bf16_t>(p, blocks, s);
-    else bwd_dispatch<float>(p, blocks, s);
+    if (a.bf16) bwd_streams<bf16_t>(p, blocks, s);
+    else bwd_streams<float>(p, blocks, s);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }

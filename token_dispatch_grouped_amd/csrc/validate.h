@@ -79,7 +79,7 @@ moe_status validate_ep(int32_t ep, int32_t e_local, int32_t d, int32_t dtype, in
 
 // ----- RMS norm, 8-bit block form, dense feed-forward block -----
 constexpr int kNormWaveRows = 2048;     // rows from which a norm row is one wavefront's
-constexpr int kNormBwdBlocks = 1024;    // workgroups (partial rows) of the norm's backward pass at most
+constexpr int kNormBwdBlocks = 512;    // workgroups (partial rows) of the norm's backward pass at most
 constexpr int kNormBwdMinRows = 8;      // rows of a workgroup of the norm's backward pass at least
 inline int norm_bwd_blocks(int64_t T) {
   const int64_t b = ceil_div(T, kNormBwdMinRows);
