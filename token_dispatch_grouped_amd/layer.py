@@ -23,6 +23,16 @@ losses (load balancing, router z-loss) and the routing metrics into
 ``aux_losses`` / ``metrics``, and the backward adds the losses' gradient to
 dlogits before the routing-weight gradient (MOE_FLAG_ACCUMULATE_DLOGITS), so
 a router trains on both.
+
+With ``norm_eps`` the layer takes the norm in front of it along: the forward
+adds ``residual`` to x, normalises the sum and gives the result to the router
+and the experts; the backward ends with the norm's. With ``shared_F`` a dense
+gated feed-forward block of that hidden size (a shared expert) takes every
+token beside the routed experts: its output is added to theirs in its last
+product, its input gradient to theirs likewise.
+
+  forward : moe_rmsnorm_fwd -> (the forward above) -> moe_ffn_fwd
+  backward: (the backward above) -> moe_ffn_dgrad, moe_ffn_wgrad -> moe_rmsnorm_bwd
 """
 from __future__ import annotations
 
@@ -32,6 +42,7 @@ from typing import Optional
 import torch
 
 from . import _lib as L
+from .block import GatedFfn, NormOut, RmsNorm
 
 
 def torch_dtype(moe_dtype: int):
@@ -54,12 +65,17 @@ class Saved:
     a: Optional[torch.Tensor]  # None under recompute
     y: torch.Tensor
     out: torch.Tensor
+    norm: Optional[NormOut] = None  # with norm_eps: r, the layer's input u (as y) and rstd
 
 
 class MoeLayer:
     def __init__(self, T_max: int, d: int, E: int, k: int, F: int, dtype: int = L.MOE_DTYPE_BF16,
                  renorm: bool = False, router: bool = False, recompute: bool = False, aux=None,
-                 device: str = "cuda"):
+                 device: str = "cuda", norm_eps: Optional[float] = None, shared_F: int = 0):
+        if shared_F and recompute:
+            raise ValueError("shared_F keeps its activations: not together with recompute")
+        if shared_F and dtype != L.MOE_DTYPE_BF16:
+            raise ValueError("shared_F needs MOE_DTYPE_BF16")
         self.T_max, self.d, self.E, self.k, self.F = T_max, d, E, k, F
         self.dtype = dtype
         self.recompute = recompute
@@ -69,6 +85,9 @@ class MoeLayer:
         self.router = router
         dev = torch.device(device)
         td = torch_dtype(dtype)
+        self.norm = RmsNorm(T_max, d, dtype, norm_eps, device=device) if norm_eps is not None else None
+        self.norm_summed = False  # whether the last forward had a residual
+        self.shared = GatedFfn(T_max, d, shared_F, device=device) if shared_F else None
         R = T_max * k
         shape = self.shape(T_max)
         self.route_ws_bytes, self.fwd_ws_bytes, self.bwd_ws_bytes = L.moe_workspace_size(shape)
@@ -119,9 +138,24 @@ class MoeLayer:
                     self.counts, self.offsets, self.row_of_slot, self.src_of_row, self.route_ws,
                     self.route_ws.numel(), stream)
 
-    def forward(self, T: int, x, w_gu, w_down, logits=None, w_router=None, bias=None, stream=None) -> Saved:
+    def _need(self, part, name: str, *given):
+        if (part is None) != all(g is None for g in given) or (part is not None and any(g is None for g in given)):
+            raise ValueError(f"{name} are needed exactly when the layer was made with that part")
+
+    def forward(self, T: int, x, w_gu, w_down, logits=None, w_router=None, bias=None, stream=None, norm_w=None,
+                residual=None, shared_w_gu=None, shared_w_down=None) -> Saved:
         """One forward. ``logits`` (fp32 [T,E]) are copied into the layer's
-        logits buffer unless a router weight is given."""
+        logits buffer unless a router weight is given. ``norm_w`` (and
+        ``residual``) with norm_eps, the shared block's weights with shared_F."""
+        self._need(self.norm, "norm weights", norm_w)
+        self._need(self.shared, "shared block weights", shared_w_gu, shared_w_down)
+        if self.norm is None and residual is not None:
+            raise ValueError("a residual needs a layer made with norm_eps")
+        normed = None
+        if self.norm is not None:
+            normed = self.norm.forward(T, x, norm_w, residual, stream)
+            self.norm_summed = residual is not None
+            x = normed.y
         s = self.shape(T)
         self.route(T, x=x, logits=logits, w_router=w_router, bias=bias, stream=stream)
         if self.aux is not None:
@@ -131,11 +165,33 @@ class MoeLayer:
         L.moe_grouped_gemm_fwd(s, self.x_perm, w_gu, w_down, self.offsets, self.h, self.a, self.y, self.fwd_ws,
                                self.fwd_ws.numel(), stream)
         L.moe_unpermute_combine(s, self.y, self.topk_w, self.row_of_slot, self.out, stream)
-        return self.saved(T)
+        if self.shared is not None:
+            self.shared.forward(T, x, shared_w_gu, shared_w_down, add=self.out, out=self.out, stream=stream)
+        saved = self.saved(T)
+        saved.norm = normed
+        return saved
 
     def backward(self, T: int, dout, w_gu, w_down, dw_gu, dw_down, x=None, w_router=None, dw_router=None,
-                 stream=None):
-        """One backward from the buffers of the last forward; dw_* accumulate."""
+                 stream=None, norm_w=None, dnorm_w=None, norm_r=None, dres=None, shared_w_gu=None, shared_w_down=None,
+                 dshared_w_gu=None, dshared_w_down=None):
+        """One backward from the buffers of the last forward; dw_* accumulate.
+
+        With norm_eps: ``norm_r`` is what the forward normalised (its x, or
+        nothing if it had a residual: the layer keeps that sum), ``dres`` the
+        gradient that reaches the residual stream directly, and dx is the
+        gradient of the forward's x (and of its residual). With shared_F but
+        no norm, x is needed as with a router."""
+        self._need(self.norm, "norm_w and dnorm_w", norm_w, dnorm_w)
+        self._need(self.shared, "the shared block's weights and their gradients", shared_w_gu, shared_w_down,
+                   dshared_w_gu, dshared_w_down)
+        if self.norm is None and (dres is not None or norm_r is not None):
+            raise ValueError("dres and norm_r need a layer made with norm_eps")
+        if self.norm is not None:
+            if self.norm_summed == (norm_r is not None):
+                raise ValueError("norm_r is needed exactly when the last forward had no residual")
+            x = self.norm.y
+        elif self.shared is not None and x is None:
+            raise ValueError("the shared block's weight gradient needs x")
         s = self.shape(T)
         L.moe_unpermute_combine_bwd(s, dout, self.y, self.topk_w, self.row_of_slot, self.dy, self.dtopk_w, stream)
         use_router = w_router is not None
@@ -149,6 +205,13 @@ class MoeLayer:
                                dw_gu, dw_down, self.bwd_ws, self.bwd_ws.numel(), stream)
         L.moe_permute_bwd(s, self.dx_perm, self.row_of_slot, self.dx_router if use_router else None, self.dx,
                           stream)
+        dx = self.dx
+        if self.shared is not None:
+            self.shared.dgrad(T, dout, shared_w_gu, shared_w_down, add=dx, out=dx, stream=stream)
+            self.shared.wgrad(T, dout, x, dshared_w_gu, dshared_w_down, stream=stream)
+        if self.norm is not None:
+            self.norm.backward(T, dx, self.norm.r if norm_r is None else norm_r, norm_w, dnorm_w, dres=dres, out=dx,
+                               stream=stream)
         R = T * self.k
         return dict(dy=self.dy[:R], dtopk_w=self.dtopk_w[:T], dlogits=self.dlogits[:T], dx_perm=self.dx_perm[:R],
                     dx=self.dx[:T], dh=self.dh_view(T),
