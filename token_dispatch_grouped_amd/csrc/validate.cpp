@@ -220,32 +220,38 @@ moe_status validate_ffn(const moe_ffn_shape *s, std::string *why) {
 }
 
 FfnWgrad ffn_wgrad_plan(int64_t T, int d, int F) {
-  const int64_t tiles = ceil_div(2 * (int64_t)F, kGemmBM) * ceil_div(d, kGemmBN) +
-                        ceil_div(d, kGemmBM) * ceil_div(F, kGemmBN);
-  int64_t most = kWgradUnits / tiles;
-  if (most > T / kWgradMinRows) most = T / kWgradMinRows;
-  if (most < 1) most = 1;
-  // Time of n slices in us, on 256 CUs with one tile each at a time: a stage
-  // of 64 tokens takes 1.35 us while every workgroup has a CU from the start,
-  // 1.6 us beyond (never more than 1060 TFLOP/s in all), and a second launch
-  // writes and reads n times the gradients at 4 TB/s. At d = 2048, F = 1408
-  // measured with 1 and 3 slices: 51 and 75 us at 2000 tokens, 145 and 149 at
-  // 7001, 349 and 312 at 16384, 694 and 589 at 32768.
+  // Time of n slices in us: a fixed 4, then rounds of workgroups, each a run of
+  // stages of 64 tokens. 256 x 256 tiles run one a CU, 1.35 us a stage while
+  // every workgroup has a CU from the start, 1.6 beyond; 128 x 128 tiles two a
+  // CU, 0.65 us a stage alone on one, 1.05 beyond; never more than 1060 TFLOP/s
+  // in all. A second launch writes and reads n times the gradients at 4 TB/s.
+  // Measured (tile, slices: us): d = 2048, F = 1408 at 2000 tokens 256, 1: 51,
+  // 256, 3: 75, 128, 1: 59; at 7001 256, 1: 145, 256, 3: 149, 128, 2: 166; at
+  // 32768 256, 1: 694, 256, 3: 589; d = 512, F = 320 at 3000 256, 11: 27, 128,
+  // 1: 33, 128, 4: 18.5; d = 1088, F = 576 at 700 256, 1: 23, 128, 1: 12.
   const double bytes = 12.0 * d * F, least = 6.0 * (double)T * d * F / 1.06e9;
-  int64_t best = 1;
+  FfnWgrad w{256, 0, 0, 1};
   double best_us = 0.0;
-  for (int64_t n = 1; n <= most; ++n) {
-    const int64_t rounds = ceil_div(tiles * n, 256), stages = ceil_div(ceil_div(T, n), 64);
-    double us = (double)(rounds * stages) * (rounds > 1 ? 1.6 : 1.35);
-    if (us < least) us = least;
-    if (n > 1) us += 5.0 + (double)n * bytes / 4e6;
-    if (n == 1 || us < best_us) {
-      best = n;
-      best_us = us;
+  int64_t best = 1;
+  for (int tile = 256; tile >= 128; tile /= 2) {
+    const int64_t tiles = ceil_div(2 * (int64_t)F, tile) * ceil_div(d, tile) + ceil_div(d, tile) * ceil_div(F, tile);
+    int64_t most = kWgradUnits / tiles;
+    if (most > T / kWgradMinRows) most = T / kWgradMinRows;
+    if (most < 1) most = 1;
+    if (most > w.most) w.most = (int)most;
+    for (int64_t n = 1; n <= most; ++n) {
+      const int64_t rounds = ceil_div(tiles * n, tile == 256 ? 256 : 512), stages = ceil_div(ceil_div(T, n), 64);
+      const double stage = tile == 256 ? (rounds > 1 ? 1.6 : 1.35) : (tiles * n > 256 ? 1.05 : 0.65);
+      double us = 4.0 + (double)(rounds * stages) * stage;
+      if (us < least) us = least;
+      if (n > 1) us += 5.0 + (double)n * bytes / 4e6;
+      if ((tile == 256 && n == 1) || us < best_us) {
+        w.tile = tile;
+        best = n;
+        best_us = us;
+      }
     }
   }
-  FfnWgrad w{};
-  w.most = (int)most;
   w.chunk = (int)(ceil_div(ceil_div(T, best), 64) * 64);
   w.slices = T > 0 ? (int)ceil_div(T, w.chunk) : 0;
   return w;

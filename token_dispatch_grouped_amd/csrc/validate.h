@@ -89,14 +89,15 @@ inline int norm_bwd_blocks(int64_t T) {
 // Tokens up to which the block's forward runs the few-token kernels.
 constexpr int kFfnFewTokens = 144;
 
-// Token slices of the dense block's two weight gradients (dw_gu [2F,d], then
-// dw_down [d,F]): at most as many as make kWgradUnits workgroups, each slice at
-// least kWgradMinRows tokens; among those the count whose time estimate is
-// least (ffn_wgrad_plan).
+// Tile and token slices of the dense block's two weight gradients (dw_gu
+// [2F,d], then dw_down [d,F]): at most as many slices as make kWgradUnits
+// workgroups, each at least kWgradMinRows tokens; among those the tile and
+// count whose time estimate is least (ffn_wgrad_plan).
 constexpr int kWgradUnits = 512;
 constexpr int kWgradMinRows = 256;
 struct FfnWgrad {
-  int slices, chunk;  // tokens of a slice
+  int tile;           // 256 or 128: rows and columns of a tile
+  int slices, chunk;  // chunk: tokens of a slice
   int most;           // slices of the workspace: never fewer for a larger T
 };
 FfnWgrad ffn_wgrad_plan(int64_t T, int d, int F);
