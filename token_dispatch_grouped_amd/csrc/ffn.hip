@@ -80,8 +80,11 @@ static hipError_t wide_store(const FfnTileParams &t, hipStream_t s) {
 // 35, square 41; 1536: square 49, half 55. In the 8-bit form (d = 4096, F =
 // 2816) gate/up 192 tokens narrow 20.3, small 26.7, down small 12.7, narrow
 // 16.3; 512 tokens in all half 46.8, square 47.5; 1024 square 63, half 71.
-// Few against the next: 192 tokens 17.8 against 20.5, 256: 23.6 against 20.6;
-// 8-bit 128: 30.8 against 32.2, 192: 37.9 against 32.2.
+// Few against the next (us, whole forward, no h kept): at 96 tokens 12.4
+// against 18.5 (2048 x 1408), 27.8 against 46.1 (4096 x 2816), 29.9 against
+// 48.7 (7168 x 2048), 8-bit 22.5 against 28.1 (4096 x 2816); at 144 tokens
+// 16.5 against 19.2, 41.5 against 38.8, 49.1 against 44.0, 8-bit 32.8 against
+// 29.0, and 9.2 against 12.2 for 512 x 320: from there on the tiles win more.
 // Large against square: a round of large tiles (one a CU) takes 1.45 times a
 // round of square ones (two a CU) and does twice the work (56-59 against 38 us
 // in bf16 at K = 2048, 57 against 40 us in the 8-bit form).

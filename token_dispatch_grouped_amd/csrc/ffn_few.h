@@ -3,7 +3,8 @@
 //
 // What counts is that every CU draws on the memory at once and has enough in
 // flight. A workgroup owns 16 weight rows (64 rows, 88 workgroups for F =
-// 2816, took 14 us at one token where 16 take 6) and 16 MF tokens; each of its
+// 2816, took 14 us at one token where 16 take 6), or 32 where 16 would make
+// more workgroups than CUs, and 16 MF tokens; each of its
 // wavefronts takes a run of the k steps (a step is 128 contiguous bytes of
 // every row) through an LDS ring of its own, filled by the LDS DMA in whole
 // 128-byte lines: no barrier until the partial sums meet, added in the order
@@ -15,6 +16,11 @@
 // A gate/up fragment is 8 gate rows and the 8 up rows that go with them. Its 8
 // columns of a are a quarter of a block of the 8-bit form, so there a is
 // written in fp32 and quantised by a kernel of its own.
+//
+// Measured: one token, 2048 x 1408, bf16: gate/up 4.0 us (2.9 TB/s of
+// weights), down 3.5 us, of which some 2 us are a kernel's start and end; 48
+// tokens, 4096 x 2816, 8-bit: gate/up 8.4 us (2.8 TB/s), down 5.6 us (2.1 TB/s).
+// Bound by the launch at one token, by what a CU draws (some 40 GB/s) after.
 #pragma once
 
 #include "ffn_kernel.h"

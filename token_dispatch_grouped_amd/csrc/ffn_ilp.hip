@@ -8,7 +8,7 @@
 // (straight to dw where there is one slice and nothing to add to), and a second
 // launch adds the slices in order (no atomics: the same bits run to run). The
 // tiles of a slice are neighbours, so that the workgroups of an XCD share
-// operand rows. At 32768 tokens, d = 2048, F = 1408: 540 us (1050 TFLOP/s) and
+// operand rows. At 32768 tokens, d = 2048, F = 1408: 550 us (1030 TFLOP/s) and
 // 27 us for the sum of three slices.
 //
 // This file also holds the gate/up forward on the same tile, for the sake of

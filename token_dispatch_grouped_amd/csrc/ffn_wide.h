@@ -3,6 +3,10 @@
 // epilogues (gg_tile), one group of p.M rows instead of an offsets table.
 // Persistent, one workgroup per CU, each XCD walking a contiguous share of
 // the tiles; the next tile's first stage is issued during the epilogue.
+// Bound by the main loop's operand stream from L2 to LDS. Measured at d =
+// 2048, F = 1408: 16384 tokens gate/up with SwiGLU 179 us (1.06 PFLOP/s), down
+// 89 us (1.06) and 106-111 us with an addend; 7001 tokens down's input gradient
+// 70 us, gate/up's with an addend 86 us (0.94), one round of tiles each.
 #pragma once
 
 #include "gemm_bf16_kernel.h"
