@@ -46,6 +46,7 @@
  *    dimension: T < 2^24 and T*d < 2^35 (bf16) or 2^34 (fp32), and the
  *    weight-gradient grid of the grouped GEMM within that bound too.
  *    Anything else returns MOE_ERR_UNSUPPORTED.
+ *  - An output overlaps no other argument except where its call says so.
  *  - Calls that overlap on one stream are ordered; calls on different
  *    streams that share buffers race, as with any HIP kernel.
  *

@@ -241,6 +241,45 @@ def test_two_streams_without_synchronisation():
             assert torch.equal(got[k], v), (i, k)
 
 
+def test_memory_made_for_a_call_belongs_to_its_stream():
+    """The current stream is behind: it still writes into memory freed on it when a call on another stream makes its
+    output, which must not be that memory."""
+    import torch
+    from token_dispatch_grouped_amd.block import RmsNorm, quantize_mx8
+    rng = np.random.default_rng(11)
+    T, d = 2048, 1024
+    x, w = _dev(_draw(rng, BF16, T, d), BF16), _dev(_draw(rng, BF16, d, std=0.1, mean=1.0), BF16)
+    dw = torch.zeros(d, device="cuda")
+    side = torch.cuda.Stream()
+    busy = torch.randn(4096, 4096, device="cuda")
+
+    def behind(nbytes):
+        """Keeps the current stream busy, then fills nbytes of memory that is freed at once."""
+        b = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        for _ in range(20):
+            torch.mm(busy, busy, out=busy_out)
+        b.fill_(0x55)
+    busy_out = torch.empty_like(busy)
+    want = quantize_mx8(x)
+    ref = RmsNorm(T, d)
+    ref.forward(T, x, w)
+    want_dx = ref.backward(T, x, x, w, dw)
+    norm = RmsNorm(T, d)
+    norm.forward(T, x, w)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    for nbytes, call in ((T * d, lambda: quantize_mx8(x, stream=side.cuda_stream)),
+                         (T * d * 2, lambda: norm.backward(T, x, x, w, dw, stream=side.cuda_stream))):
+        behind(nbytes)
+        got = call()
+        torch.cuda.synchronize()
+        if isinstance(got, torch.Tensor):
+            assert torch.equal(got, want_dx)
+        else:
+            assert torch.equal(got.q.view(torch.uint8), want.q.view(torch.uint8))
+            assert torch.equal(got.scale.view(torch.uint8), want.scale.view(torch.uint8))
+
+
 def test_offsets_past_32_bits():
     """2.2 billion elements in a tensor: the last rows equal the same rows computed alone."""
     import torch

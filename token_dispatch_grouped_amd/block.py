@@ -69,6 +69,14 @@ def _on(device: torch.device):
     return torch.cuda.device(device)
 
 
+def _made_on(device: torch.device, stream):
+    """Memory made for a call on another stream than the current one belongs to
+    that stream: the current one may still be writing what was freed there."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device))
+
+
 def _check_T(T: int, T_max: int) -> None:
     if not 0 <= T <= T_max:
         raise ValueError(f"T = {T} outside [0, T_max = {T_max}]")
@@ -89,7 +97,8 @@ def quantize_mx8(t: torch.Tensor, out: Optional[Mx8] = None, stream=None) -> Mx8
         raise ValueError("quantize_mx8: expected a contiguous bf16 or fp32 matrix")
     rows, cols = t.shape
     if out is None:
-        out = empty_mx8(rows, cols, t.device)
+        with _made_on(t.device, stream):
+            out = empty_mx8(rows, cols, t.device)
     _check_mx8("out", out, None, (rows, cols), t.device)
     with _on(t.device):
         L.moe_mx8_quantize(rows, cols, types[t.dtype], t, out.q, out.scale, stream)
@@ -148,7 +157,8 @@ class RmsNorm:
         _check("dw", dw, None, (self.d,), torch.float32, self.device)
         if out is None:
             if self.dx is None:
-                self.dx = torch.empty(self.T_max, self.d, dtype=self.td, device=self.device)
+                with _made_on(self.device, stream):
+                    self.dx = torch.empty(self.T_max, self.d, dtype=self.td, device=self.device)
             out = self.dx
         _check("out", out, T, (self.d,), self.td, self.device)
         with _on(self.device):
