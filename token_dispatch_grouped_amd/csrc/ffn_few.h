@@ -20,7 +20,7 @@
 // Measured: one token, 2048 x 1408, bf16: gate/up 4.0 us (2.9 TB/s of
 // weights), down 3.5 us, of which some 2 us are a kernel's start and end; 48
 // tokens, 4096 x 2816, 8-bit: gate/up 8.4 us (2.8 TB/s), down 5.6 us (2.1 TB/s).
-// Bound by the launch at one token, by what a CU draws (some 40 GB/s) after.
+// Bound by the launches and each kernel's start, and by what a CU draws.
 #pragma once
 
 #include "ffn_kernel.h"
