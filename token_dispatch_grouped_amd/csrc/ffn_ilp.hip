@@ -4,9 +4,10 @@
 // small gradients, 128 x 128. There are few output tiles and a long sum over
 // the tokens, so the tokens are split into slices (ffn_wgrad_plan has the rule
 // and what it was measured on): every (slice, tile) pair of either product is a
-// workgroup of one launch that writes fp32 partial sums to the workspace
-// (straight to dw where there is one slice and nothing to add to), and a second
-// launch adds the slices in order (no atomics: the same bits run to run). The
+// workgroup of one launch. With one slice it writes dw or adds to it (7001
+// tokens, adding: 173 us against 184 with a launch of its own for the sum; 128
+// tokens 19.5 against 32); otherwise it writes fp32 partial sums to the workspace
+// and a second launch adds the slices in order (no atomics: the same bits run to run). The
 // tiles of a slice are neighbours, so that the workgroups of an XCD share
 // operand rows. At 32768 tokens, d = 2048, F = 1408: 550 us (1030 TFLOP/s) and
 // 27 us for the sum of three slices.
@@ -25,7 +26,7 @@ struct WgradParams {
 };
 
 // B x B tiles: 8 wavefronts of 128 x 64 (B = 256), or 4 of 64 x 64 (B = 128).
-template <int B>
+template <int B, int EPI>
 __global__ __launch_bounds__(B * 2) void ffn_wgrad_kernel(WgradParams w) {
   constexpr int WN = 64, NW = B / 32;
   __shared__ u32x4_t lds[2 * (B + B) * kStageK * 2 / 16];
@@ -43,7 +44,7 @@ __global__ __launch_bounds__(B * 2) void ffn_wgrad_kernel(WgradParams w) {
   const int kdim = min(w.chunk, w.T - row0);
   const int m0 = mt * B;
   auto none = [&](NextTile &nx) { nx.valid = false; };
-  gg_tile<B, B, B / 2, WN, NW, true, true, EPI_ST_F32, true, kStageK, kStages>(
+  gg_tile<B, B, B / 2, WN, NW, true, true, EPI, true, kStageK, kStages>(
       p, lds, slice, m0, nt, min(B, p.M - m0), kdim, 0, p.A + (int64_t)row0 * p.lda + m0,
       p.B + (int64_t)row0 * p.ldb, false, none);
 }
@@ -105,9 +106,8 @@ hipError_t launch_ffn_dense_wgrad(const FfnArgs &a, hipStream_t s) {
     p.n_tiles = (p.N + plan.tile - 1) / plan.tile;
     p.total = p.m_tiles * p.n_tiles * slices;
     float *dw = i == 0 ? a.dw_gu : a.dw_down;
-    const bool direct = slices == 1 && !a.accumulate;
-    p.C = direct ? dw : ws;
-    if (direct) continue;
+    p.C = slices == 1 ? dw : ws;
+    if (slices == 1) continue;
     r.partial[i] = ws;
     r.dw[i] = dw;
     r.n4[i] = p.strideC / 4;  // the sum of no slice is zero
@@ -117,8 +117,9 @@ hipError_t launch_ffn_dense_wgrad(const FfnArgs &a, hipStream_t s) {
   if (total > 0) {
     LaunchScope scope("ffn_wgrad", s);
     const dim3 grid((unsigned)(ceil_div(total, 8) * 8));
-    if (plan.tile == 256) ffn_wgrad_kernel<256><<<grid, 512, 0, s>>>(w);
-    else ffn_wgrad_kernel<128><<<grid, 256, 0, s>>>(w);
+    const bool add = slices == 1 && a.accumulate;
+    if (plan.tile == 256) (add ? ffn_wgrad_kernel<256, EPI_ACC_F32> : ffn_wgrad_kernel<256, EPI_ST_F32>)<<<grid, 512, 0, s>>>(w);
+    else (add ? ffn_wgrad_kernel<128, EPI_ACC_F32> : ffn_wgrad_kernel<128, EPI_ST_F32>)<<<grid, 256, 0, s>>>(w);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
