@@ -20,29 +20,26 @@ __global__ __launch_bounds__(512, 1) void ffn_wide_kernel(GemmParams p) {
   static_assert(BM * BN * 2 <= 2 * STAGE_BYTES, "the epilogues stage within the ring");
   __shared__ u32x4_t lds[2 * STAGE_BYTES / 16];
   const int per = kGroupM * p.n_tiles;
-  const int64_t L = (int64_t)((p.m_tiles + kGroupM - 1) / kGroupM) * per;
   int lo, hi;
-  xcd_range(blockIdx.x & 7, L, lo, hi);
+  xcd_range(blockIdx.x & 7, (int64_t)p.m_tiles * p.n_tiles, lo, hi);
   const int nW = gridDim.x >> 3;
   auto decode = [&](int bid, int &m0, int &n_tile, int &m_valid) {
     const int grp = bid / per, rem = bid - grp * per;
-    n_tile = rem / kGroupM;
-    m0 = (grp * kGroupM + (rem - n_tile * kGroupM)) * BM;
+    const int rows = min(kGroupM, p.m_tiles - grp * kGroupM);  // of the last group fewer
+    n_tile = rem / rows;
+    m0 = (grp * kGroupM + (rem - n_tile * rows)) * BM;
     m_valid = min(BM, p.M - m0);
-    return m_valid > 0;
   };
   bool pre = false;  // this tile's stage 0 is already in flight
   for (int bid = lo + (int)(blockIdx.x >> 3); bid < hi; bid += nW) {
     int m0, n_tile, m_valid;
-    if (!decode(bid, m0, n_tile, m_valid)) {
-      pre = false;
-      continue;
-    }
+    decode(bid, m0, n_tile, m_valid);
     bool nvalid = false;
     auto next_tile = [&](NextTile &nx) {
       int nm0 = 0;
-      nx.valid = bid + nW < hi && decode(bid + nW, nm0, nx.n_tile, nx.m_valid);
-      nx.Ab = p.A + (int64_t)(nx.valid ? nm0 : 0) * p.lda;
+      nx.valid = bid + nW < hi;
+      if (nx.valid) decode(bid + nW, nm0, nx.n_tile, nx.m_valid);
+      nx.Ab = p.A + (int64_t)nm0 * p.lda;
       nx.Bb = p.B;
       nvalid = nx.valid;
     };
@@ -57,7 +54,7 @@ template <bool BKM, int EPI>
 hipError_t run_ffn_wide(GemmParams p, hipStream_t s) {
   p.m_tiles = (p.M + kGemmBM - 1) / kGemmBM;
   p.n_tiles = EPI == EPI_SWIGLU_FWD ? (p.N + kGemmBN / 2 - 1) / (kGemmBN / 2) : (p.N + kGemmBN - 1) / kGemmBN;
-  const int64_t L = (int64_t)((p.m_tiles + kGroupM - 1) / kGroupM) * kGroupM * p.n_tiles;
+  const int64_t L = (int64_t)p.m_tiles * p.n_tiles;
   const int grid = (int)std::min<int64_t>(persistent_grid(), (L + 7) / 8 * 8);
   ffn_wide_kernel<BKM, EPI><<<dim3((unsigned)grid), 512, 0, s>>>(p);
   return hipGetLastError();
