@@ -70,16 +70,18 @@ static hipError_t wide_store(const FfnTileParams &t, hipStream_t s) {
 //   few     M <= kFfnFewTokens, forward: reads the weights once (ffn_few.h)
 //   small   64 x 64 tiles, 4 k groups a workgroup
 //   narrow  64 x 128 tiles, 2 k groups
+//   pair    128 x 128 tiles, 2 k groups
 //   half    64 x 128 tiles, two workgroups a CU
 //   square  128 x 128 tiles, two workgroups a CU
 //   large   256 x 256 tiles
 // While a tile shape does not fill the card, a smaller one ends sooner (its
 // workgroups are bound by the latency of a stage, which the k groups hide).
-// Forward at d = 2048, F = 1408, us: 256 tokens small 20.6, narrow 26.7,
-// half 29.7, square 39; 512: narrow 28.0, half 29.8, square 40; 1024: half
-// 35, square 41; 1536: square 49, half 55. In the 8-bit form (d = 4096, F =
-// 2816) gate/up 192 tokens narrow 20.3, small 26.7, down small 12.7, narrow
-// 16.3; 512 tokens in all half 46.8, square 47.5; 1024 square 63, half 71.
+// Forward at d = 2048, F = 1408, us: 256 tokens small 20.6, narrow 26.7, square
+// 39; 512: narrow 28.0, half 29.8, square 40; 1400: pair 40.3, half 43.1; 1472:
+// half 43.0, square 49.3; 1536: square 49, half 55; the input gradient at 1400
+// tokens pair 48.5, square 52.4, at 2000 58.0, 62.7. In the 8-bit form (d =
+// 4096, F = 2816) gate/up 192 tokens narrow 20.3, small 26.7, down small 12.7,
+// narrow 16.3; 700 tokens in all pair 55.5, square 57.7.
 // Few against the next (us, whole forward, no h kept): at 96 tokens 12.4
 // against 18.5 (2048 x 1408), 27.8 against 46.1 (4096 x 2816), 29.9 against
 // 48.7 (7168 x 2048), 8-bit 22.5 against 28.1 (4096 x 2816); at 144 tokens
@@ -88,7 +90,7 @@ static hipError_t wide_store(const FfnTileParams &t, hipStream_t s) {
 // Large against square: a round of large tiles (one a CU) takes 1.45 times a
 // round of square ones (two a CU) and does twice the work (56-59 against 38 us
 // in bf16 at K = 2048, 57 against 40 us in the 8-bit form).
-enum Tile { kFew, kSmall, kNarrow, kHalf, kSquare, kLarge };
+enum Tile { kFew, kSmall, kNarrow, kPair, kHalf, kSquare, kLarge };
 
 static Tile choose(int M, int NB, bool mx8, bool swiglu, bool kmajor) {
   if (!kmajor && M <= kFfnFewTokens) return kFew;
@@ -96,6 +98,7 @@ static Tile choose(int M, int NB, bool mx8, bool swiglu, bool kmajor) {
   const auto tiles = [&](int bm, int bn) { return ceil_div(M, bm) * ceil_div(NB, bn); };
   if (!kmajor && !(mx8 && swiglu) && tiles(64, 64) <= cus) return kSmall;
   if (tiles(64, 128) <= cus) return kNarrow;
+  if (tiles(128, 128) <= cus) return kPair;
   if (!kmajor && !mx8 && tiles(64, 128) <= 2 * cus) return kHalf;
   return 145 * ceil_div(tiles(256, 256), cus) < 100 * ceil_div(tiles(128, 128), 2 * cus) ? kLarge : kSquare;
 }
@@ -110,6 +113,7 @@ static hipError_t gateup(const FfnTileParams &p, bool mx8, hipStream_t s) {
         return launch_mx8_quantize(p.a32, p.C2, p.C2s, p.M, p.F, false, s);
       }
       case kNarrow: return run_ffn_tile<true, 64, 128, 32, 64, 2, 3, false, FFN_SWIGLU_FWD>(p, s);
+      case kPair: return run_ffn_tile<true, 128, 128, 64, 64, 2, 2, false, FFN_SWIGLU_FWD>(p, s);
       case kLarge: return run_ffn_tile<true, 256, 256, 128, 64, 1, 2, false, FFN_SWIGLU_FWD>(p, s);
       default: return run_ffn_tile<true, 128, 128, 64, 64, 1, 2, false, FFN_SWIGLU_FWD>(p, s);
     }
@@ -118,6 +122,7 @@ static hipError_t gateup(const FfnTileParams &p, bool mx8, hipStream_t s) {
     case kFew: return run_ffn_few<false, FFN_SWIGLU_FWD>(p, s);
     case kSmall: return run_ffn_tile<false, 64, 64, 32, 64, 4, 2, false, FFN_SWIGLU_FWD>(p, s);
     case kNarrow: return run_ffn_tile<false, 64, 128, 32, 64, 2, 3, false, FFN_SWIGLU_FWD>(p, s);
+    case kPair: return run_ffn_tile<false, 128, 128, 64, 64, 2, 2, false, FFN_SWIGLU_FWD>(p, s);
     case kHalf: return run_ffn_tile<false, 64, 128, 32, 64, 1, 3, false, FFN_SWIGLU_FWD>(p, s);
     case kLarge: return wide<false, EPI_SWIGLU_FWD>(p, s);
     default: return run_ffn_tile<false, 128, 128, 64, 64, 1, 2, false, FFN_SWIGLU_FWD>(p, s);
@@ -131,6 +136,7 @@ static hipError_t down(const FfnTileParams &p, bool mx8, hipStream_t s) {
       case kFew: return run_ffn_few<true, FFN_STORE>(p, s);
       case kSmall: return run_ffn_tile<true, 64, 64, 32, 64, 4, 2, false, FFN_STORE>(p, s);
       case kNarrow: return run_ffn_tile<true, 64, 128, 32, 64, 2, 3, false, FFN_STORE>(p, s);
+      case kPair: return run_ffn_tile<true, 128, 128, 64, 64, 2, 2, false, FFN_STORE>(p, s);
       case kLarge: return run_ffn_tile<true, 256, 256, 128, 64, 1, 2, false, FFN_STORE>(p, s);
       default: return run_ffn_tile<true, 128, 128, 64, 64, 1, 2, false, FFN_STORE>(p, s);
     }
@@ -139,6 +145,7 @@ static hipError_t down(const FfnTileParams &p, bool mx8, hipStream_t s) {
     case kFew: return run_ffn_few<false, FFN_STORE>(p, s);
     case kSmall: return run_ffn_tile<false, 64, 64, 32, 64, 4, 2, false, FFN_STORE>(p, s);
     case kNarrow: return run_ffn_tile<false, 64, 128, 32, 64, 2, 3, false, FFN_STORE>(p, s);
+    case kPair: return run_ffn_tile<false, 128, 128, 64, 64, 2, 2, false, FFN_STORE>(p, s);
     case kHalf: return run_ffn_tile<false, 64, 128, 32, 64, 1, 3, false, FFN_STORE>(p, s);
     case kLarge: return wide_store<false>(p, s);
     default: return run_ffn_tile<false, 128, 128, 64, 64, 1, 2, false, FFN_STORE>(p, s);
@@ -158,6 +165,7 @@ hipError_t launch_ffn_dense_fwd(const FfnArgs &a, hipStream_t s) {
 static hipError_t down_dgrad(const FfnTileParams &p, hipStream_t s) {
   switch (choose(p.M, p.N, false, false, true)) {
     case kNarrow: return run_ffn_tile<false, 64, 128, 32, 64, 2, 2, true, FFN_SWIGLU_BWD>(p, s);
+    case kPair: return run_ffn_tile<false, 128, 128, 64, 64, 2, 2, true, FFN_SWIGLU_BWD>(p, s);
     case kLarge: return wide<true, EPI_SWIGLU_BWD>(p, s);
     default: return run_ffn_tile<false, 128, 128, 64, 64, 1, 2, true, FFN_SWIGLU_BWD>(p, s);
   }
@@ -166,6 +174,7 @@ static hipError_t down_dgrad(const FfnTileParams &p, hipStream_t s) {
 static hipError_t gateup_dgrad(const FfnTileParams &p, hipStream_t s) {
   switch (choose(p.M, p.N, false, false, true)) {
     case kNarrow: return run_ffn_tile<false, 64, 128, 32, 64, 2, 2, true, FFN_STORE>(p, s);
+    case kPair: return run_ffn_tile<false, 128, 128, 64, 64, 2, 2, true, FFN_STORE>(p, s);
     case kLarge: return wide_store<true>(p, s);
     default: return run_ffn_tile<false, 128, 128, 64, 64, 1, 2, true, FFN_STORE>(p, s);
   }
