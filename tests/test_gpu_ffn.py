@@ -77,7 +77,7 @@ SHAPES = [(1, 64, 64), (1, 2048, 1408), (2, 64, 192), (15, 192, 64), (16, 128, 1
 # enough tiles for the 256 x 256 tile in the products with N = d, in those with N = F, and several rounds of it
 LARGE = [(4200, 2048, 128), (6001, 128, 1472), (9000, 320, 1088)]
 # two groups of wavefronts a 128 x 128 tile in each product; a few rows more than whole rounds of the 256 x 256 tile
-LARGE += [(1400, 1472, 320), (1500, 256, 1472), (65793, 256, 128), (65793, 128, 256)]
+LARGE += [(1400, 1472, 320), (1500, 256, 1472), (65793, 256, 128), (65793, 128, 256), (65600, 256, 128)]
 
 
 @pytest.mark.parametrize("T,d,F", SHAPES + LARGE)
@@ -209,7 +209,7 @@ def _values(q, s):
                                    (48, 384, 1408), (64, 1024, 128), (65, 128, 256), (144, 640, 384),
                                    (145, 128, 1152), (250, 1920, 2816),
                                    (700, 1152, 640), (1300, 512, 1408), (4200, 2048, 128), (6001, 128, 1408),
-                                   (9000, 384, 1152), (1500, 1536, 128), (65793, 256, 128)])
+                                   (9000, 384, 1152), (1500, 1536, 128), (65793, 256, 128), (65600, 256, 128)])
 def test_forward_mx8(T, d, F):
     """Rows and weights of widely different block scales, so that a scale applied to a wrong block shows."""
     import torch

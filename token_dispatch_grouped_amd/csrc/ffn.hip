@@ -103,6 +103,58 @@ static Tile choose(int M, int NB, bool mx8, bool swiglu, bool kmajor) {
   return 145 * ceil_div(tiles(256, 256), cus) < 100 * ceil_div(tiles(128, 128), 2 * cus) ? kLarge : kSquare;
 }
 
+// A product that the large tiles compute in a few tiles more than whole rounds
+// of the card leaves most CUs idle for a round, so its last rows go to smaller
+// tiles in a launch of their own where that is shorter. Measured (us, against
+// one launch): d = 2048, F = 1408 forward at 6000 tokens 119 (146), 9000 164
+// (182), 12500 222 (240), 14000 254 (252), input gradient at 8300 170 (209),
+// 17000 333 (370); 8-bit 4096 x 2816 at 3000 tokens 123 (155), 4200 162 (193).
+// `cost`: hundredths of a round of large tiles, from the times above.
+static int cost(int M, int NB, bool mx8, bool swiglu, bool kmajor) {
+  const int64_t cus = persistent_grid();
+  switch (choose(M, NB, mx8, swiglu, kmajor)) {
+    case kFew: return 20;
+    case kSmall: return 25;
+    case kNarrow: return 31;
+    case kPair: return 45;
+    case kHalf: return 50;
+    case kSquare: return 69 * (int)ceil_div(ceil_div(M, 128) * ceil_div(NB, 128), 2 * cus);
+    default: return 100 * (int)ceil_div(ceil_div(M, 256) * ceil_div(NB, 256), cus);
+  }
+}
+
+// Rows of the first launch: M for one launch in all.
+static int head_rows(int M, int NB, bool mx8, bool swiglu, bool kmajor) {
+  const int64_t cus = persistent_grid(), cols = ceil_div(NB, 256);
+  const int64_t rounds = ceil_div(M, 256) * cols / cus;
+  if (rounds == 0 || choose(M, NB, mx8, swiglu, kmajor) != kLarge) return M;
+  const int64_t head = rounds * cus / cols * 256;
+  if (head <= 0 || head >= M) return M;
+  const int tail = cost(M - (int)head, NB, mx8, swiglu, kmajor) + 5;
+  return 100 * rounds + tail < cost(M, NB, mx8, swiglu, kmajor) ? (int)head : M;
+}
+
+// Rows [from, from + count) of a product.
+static FfnTileParams rows(FfnTileParams p, bool mx8, int64_t from, int count) {
+  p.A += from * p.lda;
+  if (p.As) p.As += from * (p.K / 16);
+  if (p.C) p.C += from * p.ldc;
+  if (p.C2) p.C2 = reinterpret_cast<bf16_t *>(reinterpret_cast<char *>(p.C2) + from * p.F * (mx8 ? 1 : 2));
+  if (p.C2s) p.C2s += from * (p.F / kMx8Block);
+  if (p.H) p.H += from * p.ldc;
+  if (p.add) p.add += from * p.ldc;
+  p.M = count;
+  return p;
+}
+
+template <typename Run>
+static hipError_t in_rounds(const FfnTileParams &p, int NB, bool mx8, bool swiglu, bool kmajor, Run run) {
+  const int head = head_rows(p.M, NB, mx8, swiglu, kmajor);
+  if (head == p.M) return run(p);
+  const hipError_t err = run(rows(p, mx8, 0, head));
+  return err != hipSuccess ? err : run(rows(p, mx8, head, p.M - head));
+}
+
 static hipError_t gateup(const FfnTileParams &p, bool mx8, hipStream_t s) {
   const Tile t = choose(p.M, 2 * p.N, mx8, true, false);
   if (mx8) {
@@ -155,11 +207,13 @@ static hipError_t down(const FfnTileParams &p, bool mx8, hipStream_t s) {
 hipError_t launch_ffn_dense_fwd(const FfnArgs &a, hipStream_t s) {
   {
     LaunchScope scope("ffn_gateup_fwd", s);
-    const hipError_t err = gateup(gateup_params(a), a.mx8, s);
+    const hipError_t err = in_rounds(gateup_params(a), 2 * a.F, a.mx8, true, false,
+                                     [&](const FfnTileParams &p) { return gateup(p, a.mx8, s); });
     if (err != hipSuccess) return err;
   }
   LaunchScope scope("ffn_down_fwd", s);
-  return down(down_params(a), a.mx8, s);
+  return in_rounds(down_params(a), a.d, a.mx8, false, false,
+                   [&](const FfnTileParams &p) { return down(p, a.mx8, s); });
 }
 
 static hipError_t down_dgrad(const FfnTileParams &p, hipStream_t s) {
@@ -195,7 +249,8 @@ hipError_t launch_ffn_dense_dgrad(const FfnArgs &a, hipStream_t s) {
     p.lda = a.d;
     p.ldb = a.F;
     p.ldc = 2 * (int64_t)a.F;
-    const hipError_t err = down_dgrad(p, s);
+    const hipError_t err =
+        in_rounds(p, p.N, false, false, true, [&](const FfnTileParams &q) { return down_dgrad(q, s); });
     if (err != hipSuccess) return err;
   }
   LaunchScope scope("ffn_gateup_dgrad", s);
@@ -211,7 +266,7 @@ hipError_t launch_ffn_dense_dgrad(const FfnArgs &a, hipStream_t s) {
   p.lda = 2 * (int64_t)a.F;
   p.ldb = a.d;
   p.ldc = a.d;
-  return gateup_dgrad(p, s);
+  return in_rounds(p, p.N, false, false, true, [&](const FfnTileParams &q) { return gateup_dgrad(q, s); });
 }
 
 }  // namespace moe
