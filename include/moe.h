@@ -473,7 +473,8 @@ moe_status moe_ep_exchange_loopback(int32_t ep, int32_t d, int32_t dtype, void *
  * y_scale NULL, y is [T,d] s; otherwise y is [T,d] e4m3 bytes and y_scale
  * [T,d/32] scale bytes, quantised from the fp32 values (moe_mx8_quantize has
  * the form). r may be x or residual itself. Sums run in fp32 in a fixed
- * order. T == 0 writes nothing.
+ * order; rows of any finite r have their rstd, also those whose squares pass
+ * fp32's range. T == 0 writes nothing.
  * Supported: T < 2^24, d a positive multiple of 64, at most 65536, dtype F32
  * or BF16, eps positive and finite (else MOE_ERR_INVALID_ARGUMENT).
  *

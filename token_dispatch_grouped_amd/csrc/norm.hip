@@ -48,6 +48,18 @@ MOE_DEVICE float row_sum(float v, float *part) {
   return (part[0] + part[1]) + (part[2] + part[3]);
 }
 
+// The squares of a row pass fp32's range from |r| of about 2^60 on, though rstd
+// does not: such a row, whose sum is infinite, is summed again over r 2^-80.
+// That sum stays below 2^112 (65536 values below 2^128), and the largest value
+// of a row that needs it is at least 2^56, so that nothing that counts gets
+// lost below. An infinity in the row leaves the sum infinite and rstd zero.
+constexpr float kNormDown = 0x1p-80f;
+MOE_DEVICE bool norm_again(float sum) { return sum == __builtin_huge_valf(); }
+MOE_DEVICE float norm_rstd(float sum, float inv_d, float eps) { return 1.0f / sqrtf(fmaf(sum, inv_d, eps)); }
+MOE_DEVICE float norm_rstd_down(float sum, float inv_d, float eps) {
+  return kNormDown / sqrtf(fmaf(sum, inv_d, eps * kNormDown * kNormDown));
+}
+
 // One 16-byte chunk's worth of values to the 8-bit form. The 32 values of a
 // block lie in 32 / kVec consecutive lanes, all of them active.
 template <typename T>
@@ -87,7 +99,7 @@ struct NormFwdParams {
 template <typename T, int TPR, int NV, bool MX8, bool NT>
 __global__ __launch_bounds__(kNormThreads) void rmsnorm_fwd_kernel(NormFwdParams p) {
   constexpr int V = Elem<T>::kVec;
-  __shared__ float part[kNormThreads / kWave];
+  __shared__ float part[2][kNormThreads / kWave];
   const int lane = threadIdx.x % TPR;
   const int64_t row = (int64_t)blockIdx.x * (kNormThreads / TPR) + threadIdx.x / TPR;
   if (row >= p.T) return;  // whole wavefronts only, and no barrier below for TPR = 64
@@ -127,8 +139,20 @@ __global__ __launch_bounds__(kNormThreads) void rmsnorm_fwd_kernel(NormFwdParams
     for (int i = 0; i < V; ++i) s = fmaf(a[i], a[i], s);
     if (c < n) sum += s;
   }
-  sum = row_sum<TPR>(sum, part);
-  const float rstd = 1.0f / sqrtf(fmaf(sum, p.inv_d, p.eps));
+  sum = row_sum<TPR>(sum, part[0]);
+  float rstd = norm_rstd(sum, p.inv_d, p.eps);
+  if (norm_again(sum)) {  // all threads of the row alike
+    float down = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float a[V];
+      Elem<T>::unpack(xv[j], a);
+      if (j * TPR + lane >= n) continue;
+#pragma unroll
+      for (int i = 0; i < V; ++i) down = fmaf(a[i] * kNormDown, a[i] * kNormDown, down);
+    }
+    rstd = norm_rstd_down(row_sum<TPR>(down, part[1]), p.inv_d, p.eps);
+  }
   if (lane == 0) p.rstd[row] = rstd;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -152,7 +176,7 @@ __global__ __launch_bounds__(kNormThreads) void rmsnorm_fwd_kernel(NormFwdParams
 template <typename T, bool MX8>
 __global__ __launch_bounds__(kNormThreads) void rmsnorm_fwd_long_kernel(NormFwdParams p) {
   constexpr int V = Elem<T>::kVec;
-  __shared__ float part[kNormThreads / kWave];
+  __shared__ float part[2][kNormThreads / kWave];
   const int64_t row = blockIdx.x;
   const int n = p.d / V;
   const T *x = (const T *)p.x + row * p.d;
@@ -173,10 +197,20 @@ __global__ __launch_bounds__(kNormThreads) void rmsnorm_fwd_long_kernel(NormFwdP
 #pragma unroll
     for (int i = 0; i < V; ++i) sum = fmaf(a[i], a[i], sum);
   }
-  sum = row_sum<kNormThreads>(sum, part);
-  const float rstd = 1.0f / sqrtf(fmaf(sum, p.inv_d, p.eps));
-  if (threadIdx.x == 0) p.rstd[row] = rstd;
+  sum = row_sum<kNormThreads>(sum, part[0]);
   const T *src = p.residual ? (const T *)p.r + row * p.d : x;
+  float rstd = norm_rstd(sum, p.inv_d, p.eps);
+  if (norm_again(sum)) {
+    float down = 0.f;
+    for (int c = threadIdx.x; c < n; c += kNormThreads) {
+      float a[V];
+      Elem<T>::unpack(ld16(src + c * V), a);
+#pragma unroll
+      for (int i = 0; i < V; ++i) down = fmaf(a[i] * kNormDown, a[i] * kNormDown, down);
+    }
+    rstd = norm_rstd_down(row_sum<kNormThreads>(down, part[1]), p.inv_d, p.eps);
+  }
+  if (threadIdx.x == 0) p.rstd[row] = rstd;
   for (int c0 = 0; c0 < n; c0 += kNormThreads) {  // every lane takes every pass: blocks span lanes
     const int c = c0 + threadIdx.x;
     const int cc = c < n ? c : 0;
