@@ -155,15 +155,12 @@ static hipError_t in_rounds(const FfnTileParams &p, int NB, bool mx8, bool swigl
   return err != hipSuccess ? err : run(rows(p, mx8, head, p.M - head));
 }
 
-static hipError_t gateup(const FfnTileParams &p, bool mx8, hipStream_t s) {
-  const Tile t = choose(p.M, 2 * p.N, mx8, true, false);
+// Each launch has a scope of its own: one record of the timer is one launch.
+static hipError_t gateup_product(const FfnTileParams &p, Tile t, bool mx8, hipStream_t s) {
+  LaunchScope scope("ffn_gateup_fwd", s);
   if (mx8) {
     switch (t) {
-      case kFew: {
-        const hipError_t err = run_ffn_few<true, FFN_SWIGLU_FWD>(p, s);
-        if (err != hipSuccess) return err;
-        return launch_mx8_quantize(p.a32, p.C2, p.C2s, p.M, p.F, false, s);
-      }
+      case kFew: return run_ffn_few<true, FFN_SWIGLU_FWD>(p, s);
       case kNarrow: return run_ffn_tile<true, 64, 128, 32, 64, 2, 3, false, FFN_SWIGLU_FWD>(p, s);
       case kPair: return run_ffn_tile<true, 128, 128, 64, 64, 2, 2, false, FFN_SWIGLU_FWD>(p, s);
       case kLarge: return run_ffn_tile<true, 256, 256, 128, 64, 1, 2, false, FFN_SWIGLU_FWD>(p, s);
@@ -181,7 +178,15 @@ static hipError_t gateup(const FfnTileParams &p, bool mx8, hipStream_t s) {
   }
 }
 
+static hipError_t gateup(const FfnTileParams &p, bool mx8, hipStream_t s) {
+  const Tile t = choose(p.M, 2 * p.N, mx8, true, false);
+  const hipError_t err = gateup_product(p, t, mx8, s);
+  if (err != hipSuccess || !mx8 || t != kFew) return err;
+  return launch_mx8_quantize(p.a32, p.C2, p.C2s, p.M, p.F, false, s);
+}
+
 static hipError_t down(const FfnTileParams &p, bool mx8, hipStream_t s) {
+  LaunchScope scope("ffn_down_fwd", s);
   const Tile t = choose(p.M, p.N, mx8, false, false);
   if (mx8) {
     switch (t) {
@@ -205,18 +210,15 @@ static hipError_t down(const FfnTileParams &p, bool mx8, hipStream_t s) {
 }
 
 hipError_t launch_ffn_dense_fwd(const FfnArgs &a, hipStream_t s) {
-  {
-    LaunchScope scope("ffn_gateup_fwd", s);
-    const hipError_t err = in_rounds(gateup_params(a), 2 * a.F, a.mx8, true, false,
-                                     [&](const FfnTileParams &p) { return gateup(p, a.mx8, s); });
-    if (err != hipSuccess) return err;
-  }
-  LaunchScope scope("ffn_down_fwd", s);
+  const hipError_t err = in_rounds(gateup_params(a), 2 * a.F, a.mx8, true, false,
+                                   [&](const FfnTileParams &p) { return gateup(p, a.mx8, s); });
+  if (err != hipSuccess) return err;
   return in_rounds(down_params(a), a.d, a.mx8, false, false,
                    [&](const FfnTileParams &p) { return down(p, a.mx8, s); });
 }
 
 static hipError_t down_dgrad(const FfnTileParams &p, hipStream_t s) {
+  LaunchScope scope("ffn_down_dgrad", s);
   switch (choose(p.M, p.N, false, false, true)) {
     case kNarrow: return run_ffn_tile<false, 64, 128, 32, 64, 2, 2, true, FFN_SWIGLU_BWD>(p, s);
     case kPair: return run_ffn_tile<false, 128, 128, 64, 64, 2, 2, true, FFN_SWIGLU_BWD>(p, s);
@@ -226,6 +228,7 @@ static hipError_t down_dgrad(const FfnTileParams &p, hipStream_t s) {
 }
 
 static hipError_t gateup_dgrad(const FfnTileParams &p, hipStream_t s) {
+  LaunchScope scope("ffn_gateup_dgrad", s);
   switch (choose(p.M, p.N, false, false, true)) {
     case kNarrow: return run_ffn_tile<false, 64, 128, 32, 64, 2, 2, true, FFN_STORE>(p, s);
     case kPair: return run_ffn_tile<false, 128, 128, 64, 64, 2, 2, true, FFN_STORE>(p, s);
@@ -236,24 +239,20 @@ static hipError_t gateup_dgrad(const FfnTileParams &p, hipStream_t s) {
 
 hipError_t launch_ffn_dense_dgrad(const FfnArgs &a, hipStream_t s) {
   FfnTileParams p{};
-  {
-    LaunchScope scope("ffn_down_dgrad", s);
-    p.A = (const bf16_t *)a.dy;
-    p.B = (const bf16_t *)a.w_down;
-    p.C = (bf16_t *)a.dh;
-    p.H = (const bf16_t *)a.h;
-    p.M = (int)a.T;
-    p.N = a.F;
-    p.F = a.F;
-    p.K = a.d;
-    p.lda = a.d;
-    p.ldb = a.F;
-    p.ldc = 2 * (int64_t)a.F;
-    const hipError_t err =
-        in_rounds(p, p.N, false, false, true, [&](const FfnTileParams &q) { return down_dgrad(q, s); });
-    if (err != hipSuccess) return err;
-  }
-  LaunchScope scope("ffn_gateup_dgrad", s);
+  p.A = (const bf16_t *)a.dy;
+  p.B = (const bf16_t *)a.w_down;
+  p.C = (bf16_t *)a.dh;
+  p.H = (const bf16_t *)a.h;
+  p.M = (int)a.T;
+  p.N = a.F;
+  p.F = a.F;
+  p.K = a.d;
+  p.lda = a.d;
+  p.ldb = a.F;
+  p.ldc = 2 * (int64_t)a.F;
+  const hipError_t err =
+      in_rounds(p, p.N, false, false, true, [&](const FfnTileParams &q) { return down_dgrad(q, s); });
+  if (err != hipSuccess) return err;
   p = FfnTileParams{};
   p.A = (const bf16_t *)a.dh;
   p.B = (const bf16_t *)a.w_gu;
