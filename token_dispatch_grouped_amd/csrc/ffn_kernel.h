@@ -227,8 +227,7 @@ __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void ffn_tile_k
   for (int st = 0; st < STAGES; ++st)
     if (st < nk) issue(st);
   wait_stages(min(nk, STAGES) - 1);
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");  // no LDS read moves above the barrier
+  barrier();
   fa[0] = load_a(0, 0, 0);
 #pragma unroll
   for (int j = 0; j < FN; ++j) fb[0][j] = load_b(0, 0, j);
@@ -267,8 +266,7 @@ __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void ffn_tile_k
     __builtin_amdgcn_sched_barrier(0);
     wait_lds();
     wait_stages(min(STAGES - 2, nk - 2 - kt));  // issued so far: up to stage min(kt + STAGES, nk) - 1
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");  // no LDS read moves above the barrier
+    barrier();
     if (kt + STAGES < nk) issue(kt + STAGES);
     // the first fragments of the next stage (on the last pass a harmless
     // read of a stale slot)

@@ -120,6 +120,15 @@ MOE_DEVICE void wait_vm() {
 
 MOE_DEVICE void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
+// The workgroup's barrier alone; the waits before it are explicit. The builtin
+// is no memory operation to the compiler, so the empty asm (no instruction)
+// keeps it from moving a read of what other wavefronts' DMA brought above the
+// barrier.
+MOE_DEVICE void barrier() {
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // Epilogue shared by the grouped GEMM kernels. With EPI_ACC_F32 the
 // accumulators are in MFMA order (lane = column); otherwise in swapped order
 // (lane = row, four consecutive columns per accumulator group) and LDS stages
@@ -814,7 +823,7 @@ MOE_DEVICE void gg_tile(const GemmParams &p, u32x4_t *lds, int e, int m0, int n_
   for (int st = 0; st < STAGES; ++st)
     if (st < nk && !(pre && st == 0)) issue(st);
   wait_stages(min(nk, STAGES) - 1);
-  __builtin_amdgcn_s_barrier();
+  barrier();
   load_frags(0, 0, 0, nk == 1);
 
   for (int kt = 0; kt < nk; ++kt) {
@@ -829,7 +838,7 @@ MOE_DEVICE void gg_tile(const GemmParams &p, u32x4_t *lds, int e, int m0, int n_
     wait_lds();
     // issued so far: stages up to min(kt+STAGES-1, nk-1); stage kt+1 needed
     wait_stages(min(STAGES - 2, nk - 2 - kt));
-    __builtin_amdgcn_s_barrier();
+    barrier();
     if (kt + STAGES < nk) issue(kt + STAGES);
     mfmas((KS - 1) & 1);
     // step 0 of stage kt+1 (on the last pass a harmless read of a stale slot,
