@@ -550,8 +550,9 @@ moe_status moe_mx8_quantize(int64_t rows, int32_t cols, int32_t dtype, const voi
  * depends on the shape alone (no atomics).
  *
  * Workspaces: fwd_ws serves moe_ffn_fwd (not read when h and a are given),
- * wgrad_ws serves moe_ffn_wgrad; each may be reused by a smaller T of the
- * same (d, F, dtype). T == 0 otherwise writes nothing.
+ * wgrad_ws serves moe_ffn_wgrad (0 for large d and F, whose gradients are
+ * written directly); each may be reused by a smaller T of the same
+ * (d, F, dtype). T == 0 otherwise writes nothing.
  * Supported: T < 2^24, d and F positive multiples of 64 (MX8: of 128), at
  * most 65536, T * max(d, 2F) small enough for one launch, dtype BF16 or MX8;
  * the gradients BF16 only. Anything else is MOE_ERR_UNSUPPORTED.

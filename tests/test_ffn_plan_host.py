@@ -55,3 +55,15 @@ def test_slices_cover_the_tokens_once(plan):
             p = plan(T, d, F)
             assert p["chunk"] % 64 == 0 and 1 <= p["slices"] <= p["most"]
             assert (p["slices"] - 1) * p["chunk"] < T <= p["slices"] * p["chunk"]
+
+
+@pytest.mark.parametrize("d,F,none", [(4096, 2816, True), (7168, 2048, True), (65536, 128, True), (2048, 1408, False),
+                                      (64, 64, False)])
+def test_workspace_only_where_tokens_are_sliced(plan, d, F, none):
+    """Partial sums are kept for two slices or more: sizes that have one slice at any T need no workspace."""
+    import token_dispatch_grouped_amd as moe
+    most = max(plan(T, d, F)["most"] for T in (1, 1000, 32768, (1 << 24) - 1))
+    assert (most == 1) == none
+    for T in (1, 700, 7001, 100000):
+        need = moe.moe_ffn_workspace_size(moe.make_ffn_shape(T, d, F))[1]
+        assert need == 0 if none else need >= 12 * d * F * plan(T, d, F)["slices"]

@@ -93,6 +93,28 @@ def test_wgrad_of_a_padded_batch(T, d, F):
         assert torch.isfinite(p).all() and torch.equal(p, q)
 
 
+def test_wgrad_without_a_workspace():
+    """Gradients of 512 tiles: one slice of the tokens whatever their number, nothing kept beside the gradients."""
+    import torch
+    import token_dispatch_grouped_amd as m
+    rng = np.random.default_rng(3)
+    T, d, F = 100, 65536, 128
+    dy, x, a, dh = (base._rand(rng, T, c) for c in (d, d, F, 2 * F))
+    s = m.make_ffn_shape(T, d, F, m.MOE_DTYPE_BF16, m.MOE_FFN_OVERWRITE_DW)
+    assert m.moe_ffn_workspace_size(s)[1] == 0
+    nan = float("nan")
+    dgu, ddn = torch.full((2 * F, d), nan, device="cuda"), torch.full((d, F), nan, device="cuda")
+    print(f"[ffn wgrad] T={T} d={d} F={F} no workspace", flush=True)
+    m.moe_ffn_wgrad(s, dy, x, a, dh, dgu, ddn, None, 0)
+    for got, p, q in ((dgu, dh, x), (ddn, dy, a)):
+        p, q = base._h(p), base._h(q)
+        base._near(base._h(got), p.T @ q, T * base.STEP * (np.abs(p).T @ np.abs(q)), "dw")
+    dgu2, ddn2 = dgu.clone(), ddn.clone()
+    m.moe_ffn_wgrad(m.make_ffn_shape(T, d, F), dy, x, a, dh, dgu2, ddn2, None, 0)
+    # one more addition, of a sum of the same size
+    assert torch.equal(dgu2, dgu + dgu) and torch.equal(ddn2, ddn + ddn)
+
+
 def test_offsets_past_32_bits_in_the_large_tiles():
     """1.1 million rows of 2 x 1024 columns: the rows on both sides of the border between the large tiles' launch and
     the rest's, and rows well inside the first, all beyond 2^31 elements from the start."""

@@ -219,6 +219,11 @@ moe_status validate_ffn(const moe_ffn_shape *s, std::string *why) {
   return MOE_OK;
 }
 
+// Tiles of the two weight gradients together.
+static int64_t wgrad_tiles(int tile, int d, int F) {
+  return ceil_div(2 * (int64_t)F, tile) * ceil_div(d, tile) + ceil_div(d, tile) * ceil_div(F, tile);
+}
+
 FfnWgrad ffn_wgrad_plan(int64_t T, int d, int F) {
   // Time of n slices in us: a fixed 4, then rounds of workgroups, each a run of
   // stages of 64 tokens. 256 x 256 tiles run one a CU, 1.35 us a stage while
@@ -234,7 +239,7 @@ FfnWgrad ffn_wgrad_plan(int64_t T, int d, int F) {
   double best_us = 0.0;
   int64_t best = 1;
   for (int tile = 256; tile >= 128; tile /= 2) {
-    const int64_t tiles = ceil_div(2 * (int64_t)F, tile) * ceil_div(d, tile) + ceil_div(d, tile) * ceil_div(F, tile);
+    const int64_t tiles = wgrad_tiles(tile, d, F);
     int64_t most = kWgradUnits / tiles;
     if (most > T / kWgradMinRows) most = T / kWgradMinRows;
     if (most < 1) most = 1;
@@ -266,7 +271,8 @@ FfnWorkspace ffn_workspace(const moe_ffn_shape &s) {
   const size_t few = (size_t)(s.T < kFfnFewTokens ? s.T : kFfnFewTokens);
   w.fwd_a32 = mx8 ? align256(few * (size_t)s.F * 4) : 0;
   w.fwd_total = w.fwd_a + w.fwd_scale + w.fwd_a32;
-  if (!mx8 && s.T > 0)
+  // gradients of so many tiles that no T is sliced are written to directly
+  if (!mx8 && s.T > 0 && wgrad_tiles(256, s.d, s.F) * 2 <= kWgradUnits)
     w.wgrad_total = align256((size_t)ffn_wgrad_plan(s.T, s.d, s.F).most * 3 * (size_t)s.d * (size_t)s.F * 4);
   return w;
 }

@@ -114,7 +114,7 @@ moe_status validate_ffn(const moe_ffn_shape *s, std::string *why);
 struct FfnWorkspace {
   size_t fwd_a, fwd_scale, fwd_a32;    // a (bf16, or e4m3, its scales, and few tokens' a in fp32)
   size_t fwd_total;
-  size_t wgrad_total;                  // fp32 partial sums of the two weight gradients
+  size_t wgrad_total;                  // fp32 partial sums of the two weight gradients; 0: no T of this d and F has any
 };
 FfnWorkspace ffn_workspace(const moe_ffn_shape &s);
 
