@@ -87,6 +87,7 @@ static hipError_t wide_store(const FfnTileParams &t, hipStream_t s) {
 // 48.7 (7168 x 2048), 8-bit 22.5 against 28.1 (4096 x 2816); at 144 tokens
 // 16.5 against 19.2, 41.5 against 38.8, 49.1 against 44.0, 8-bit 32.8 against
 // 29.0, and 9.2 against 12.2 for 512 x 320: from there on the tiles win more.
+// One border for all sizes costs the larger ones 7-13% just below it.
 // Large against square: a round of large tiles (one a CU) takes 1.45 times a
 // round of square ones (two a CU) and does twice the work (56-59 against 38 us
 // in bf16 at K = 2048, 57 against 40 us in the 8-bit form).

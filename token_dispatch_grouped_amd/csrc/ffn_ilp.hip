@@ -5,8 +5,8 @@
 // the tokens, so the tokens are split into slices (ffn_wgrad_plan has the rule
 // and what it was measured on): every (slice, tile) pair of either product is a
 // workgroup of one launch. With one slice it writes dw or adds to it (7001
-// tokens, adding: 173 us against 184 with a launch of its own for the sum; 128
-// tokens 19.5 against 32); otherwise it writes fp32 partial sums to the workspace
+// tokens, adding: 167-173 us against 184 with a launch of its own for the sum,
+// 160 overwriting; 128 tokens 19.5 against 32); otherwise it writes fp32 partial sums to the workspace
 // and a second launch adds the slices in order (no atomics: the same bits run to run). The
 // tiles of a slice are neighbours, so that the workgroups of an XCD share
 // operand rows. At 32768 tokens, d = 2048, F = 1408: 550 us (1030 TFLOP/s) and

@@ -128,7 +128,7 @@ hipError_t launch_rmsnorm_fwd(const RmsNormArgs &a, hipStream_t s);
 hipError_t launch_rmsnorm_bwd(const RmsNormArgs &a, hipStream_t s);
 hipError_t launch_mx8_quantize(const void *x, void *q, void *scale, int64_t rows, int d, bool bf16, hipStream_t s);
 
-// ----- dense gated feed-forward block (ffn.hip, ffn_wgrad.hip) -----
+// ----- dense gated feed-forward block (ffn.hip, ffn_ilp.hip) -----
 struct FfnArgs {
   const void *x, *w_gu, *w_down, *add;                 // add may be NULL
   const void *x_scale, *w_gu_scale, *w_down_scale;     // mx8

@@ -10,7 +10,7 @@
 // next layer see, so that the gradient is the gradient of what was computed.
 //
 // Measured (a 1 GiB copy reaches 6.7 TB/s here): forward with residual, 32768
-// x 2048 bf16, 87 us, 6.1 TB/s; backward 32768 x 4096 bf16 179 us, 6.0 TB/s;
+// x 2048 bf16, 87 us, 6.1 TB/s; backward 32768 x 4096 bf16 180 us, 6.0 TB/s;
 // 5632 x 4096 bf16 to 8 bits 11.7 us, 6.0 TB/s; one row of 2048 2.1 us, the
 // length of an all but empty kernel.
 #include "common.h"
@@ -22,9 +22,10 @@ namespace moe {
 constexpr int kNormThreads = 256;
 
 // Streams of more than half the 256 MB memory-side cache pass it by (NT):
-// 32768 x 2048 bf16 forward 94 -> 87 us, 16384 x 2048 to 8 bits 47 -> 40, 32768
-// x 4096 backward 212 -> 198. Smaller ones stay in it for whoever reads them
-// next, and are faster so (7001 x 1024 fp32 forward 10.5 against 12.2 us).
+// 32768 x 2048 bf16 forward 87 us (93 through the cache), 32768 x 4096 backward
+// 180 (200), 32768 x 2048 backward 88 (97); 16384 x 2048 to 8 bits, just above
+// the border, 39.4 (38.7). Smaller ones stay in it for whoever reads them next,
+// and are faster so (7001 x 1024 fp32 forward 10.5 against 12.2 us).
 constexpr int64_t kNormCachedBytes = (int64_t)128 << 20;
 template <bool NT>
 MOE_DEVICE u32x4_t ld16s(const void *p) {
