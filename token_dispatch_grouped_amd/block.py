@@ -6,7 +6,8 @@ As in ``layer.py``, PyTorch only allocates and provides the stream; buffers
 and workspaces are made once for the largest microbatch (``T_max``) and serve
 any smaller one, the empty one included. Weight gradients are fp32 and
 accumulate unless ``overwrite`` is asked for. Tensors are checked (type, shape,
-contiguity, device) before anything is called.
+contiguity, device) before anything is called: each call's check is a method of
+its own (``check_*``), which ``MoeLayer`` makes before its first launch.
 """
 from __future__ import annotations
 
@@ -130,37 +131,50 @@ class RmsNorm:
     def shape(self, T: int, overwrite: bool = False) -> L.moe_norm_shape:
         return L.make_norm_shape(T, self.d, self.dtype, self.eps, L.MOE_NORM_OVERWRITE_DW if overwrite else 0)
 
-    def forward(self, T: int, x, weight, residual=None, stream=None) -> NormOut:
-        """y = norm(x + residual) * weight; r = x + residual is the new
-        residual stream (in the object's buffer, valid until the next
-        forward)."""
+    def check_forward(self, T: int, x, weight, residual=None) -> None:
         _check_T(T, self.T_max)
         _check("x", x, T, (self.d,), self.td, self.device)
         _check("weight", weight, None, (self.d,), self.td, self.device)
         if residual is not None:
             _check("residual", residual, T, (self.d,), self.td, self.device)
+
+    def forward(self, T: int, x, weight, residual=None, stream=None) -> NormOut:
+        """y = norm(x + residual) * weight; r = x + residual is the new
+        residual stream (in the object's buffer, valid until the next
+        forward)."""
+        self.check_forward(T, x, weight, residual)
+        return self._forward(T, x, weight, residual, stream)
+
+    def _forward(self, T: int, x, weight, residual, stream) -> NormOut:
         r = self.r if residual is not None else None
         with _on(self.device):
             L.moe_rmsnorm_fwd(self.shape(T), x, residual, weight, r, self.y.q if self.mx8 else self.y,
                               self.y.scale if self.mx8 else None, self.rstd, stream)
         return NormOut(None if r is None else r[:T], self.y.rows(T) if self.mx8 else self.y[:T], self.rstd[:T])
 
-    def backward(self, T: int, dy, r, weight, dw, dres=None, overwrite: bool = False, out=None, stream=None):
-        """Gradient of x (and of the residual alike) from dL/dy, with the
-        ``rstd`` of the last forward; ``r``: that forward's r, or its x if it
-        had no residual; ``dres``: the gradient that reaches r directly.
-        ``dw`` [d] fp32 accumulates (``overwrite``: is written)."""
+    def check_backward(self, T: int, dy, r, weight, dw, dres=None, out=None) -> None:
         _check_T(T, self.T_max)
         for name, t in (("dy", dy), ("r", r)) + ((("dres", dres),) if dres is not None else ()):
             _check(name, t, T, (self.d,), self.td, self.device)
         _check("weight", weight, None, (self.d,), self.td, self.device)
         _check("dw", dw, None, (self.d,), torch.float32, self.device)
+        if out is not None:
+            _check("out", out, T, (self.d,), self.td, self.device)
+
+    def backward(self, T: int, dy, r, weight, dw, dres=None, overwrite: bool = False, out=None, stream=None):
+        """Gradient of x (and of the residual alike) from dL/dy, with the
+        ``rstd`` of the last forward; ``r``: that forward's r, or its x if it
+        had no residual; ``dres``: the gradient that reaches r directly.
+        ``dw`` [d] fp32 accumulates (``overwrite``: is written)."""
+        self.check_backward(T, dy, r, weight, dw, dres, out)
+        return self._backward(T, dy, r, weight, dw, dres, overwrite, out, stream)
+
+    def _backward(self, T: int, dy, r, weight, dw, dres, overwrite, out, stream):
         if out is None:
             if self.dx is None:
                 with _made_on(self.device, stream):
                     self.dx = torch.empty(self.T_max, self.d, dtype=self.td, device=self.device)
             out = self.dx
-        _check("out", out, T, (self.d,), self.td, self.device)
         with _on(self.device):
             L.moe_rmsnorm_bwd(self.shape(T, overwrite), dy, r, weight, self.rstd, dres, out, dw, self.ws,
                               self.ws.numel(), stream)
@@ -202,47 +216,67 @@ class GatedFfn:
         if not self.save:
             raise ValueError("this GatedFfn keeps nothing for a backward (save=False or MOE_DTYPE_MX8)")
 
-    def forward(self, T: int, x, w_gu, w_down, add=None, out=None, stream=None):
-        """y = FFN(x) + add into ``out`` (which may be ``add``) or the object's
-        buffer. MX8: x and the weights are ``Mx8``."""
+    def check_forward(self, T: int, x, w_gu, w_down, add=None, out=None) -> None:
         _check_T(T, self.T_max)
         self._check_weights(w_gu, w_down)
         if self.mx8:
             _check_mx8("x", x, T, (self.d,), self.device)
         else:
             self._rows("x", x, T)
+        for name, t in (("out", out), ("add", add)):
+            if t is not None:
+                self._rows(name, t, T)
+
+    def forward(self, T: int, x, w_gu, w_down, add=None, out=None, stream=None):
+        """y = FFN(x) + add into ``out`` (which may be ``add``) or the object's
+        buffer. MX8: x and the weights are ``Mx8``."""
+        self.check_forward(T, x, w_gu, w_down, add, out)
+        return self._forward(T, x, w_gu, w_down, add, out, stream)
+
+    def _forward(self, T: int, x, w_gu, w_down, add, out, stream):
         out = self.y if out is None else out
-        self._rows("out", out, T)
-        if add is not None:
-            self._rows("add", add, T)
         q = (lambda m: (m.q, m.scale)) if self.mx8 else (lambda m: (m, None))
         with _on(self.device):
             L.moe_ffn_fwd(self.shape(T), *q(x), *q(w_gu), *q(w_down), add, self.h, self.a, out, self.ws,
                           self.ws.numel(), stream)
         return out[:T]
 
-    def dgrad(self, T: int, dy, w_gu, w_down, add=None, out=None, stream=None):
-        """Gradient of x (plus ``add``) from the last forward's h; keeps dh for
-        ``wgrad``."""
+    def check_dgrad(self, T: int, dy, w_gu, w_down, add=None, out=None) -> None:
         self._backward_ready()
         _check_T(T, self.T_max)
         self._check_weights(w_gu, w_down)
+        self._rows("dy", dy, T)
+        for name, t in (("out", out), ("add", add)):
+            if t is not None:
+                self._rows(name, t, T)
+
+    def dgrad(self, T: int, dy, w_gu, w_down, add=None, out=None, stream=None):
+        """Gradient of x (plus ``add``) from the last forward's h; keeps dh for
+        ``wgrad``."""
+        self.check_dgrad(T, dy, w_gu, w_down, add, out)
+        return self._dgrad(T, dy, w_gu, w_down, add, out, stream)
+
+    def _dgrad(self, T: int, dy, w_gu, w_down, add, out, stream):
         out = self.dx if out is None else out
-        for name, t in (("dy", dy), ("out", out)) + ((("add", add),) if add is not None else ()):
-            self._rows(name, t, T)
         with _on(self.device):
             L.moe_ffn_dgrad(self.shape(T), dy, self.h, w_gu, w_down, add, self.dh, out, stream)
         return out[:T]
 
-    def wgrad(self, T: int, dy, x, dw_gu, dw_down, overwrite: bool = False, stream=None):
-        """Weight gradients from the last forward's a and the last dgrad's dh;
-        may run any time before either is written again."""
+    def check_wgrad(self, T: int, dy, x, dw_gu, dw_down) -> None:
         self._backward_ready()
         _check_T(T, self.T_max)
         self._rows("dy", dy, T)
         self._rows("x", x, T)
         _check("dw_gu", dw_gu, None, (2 * self.F, self.d), torch.float32, self.device)
         _check("dw_down", dw_down, None, (self.d, self.F), torch.float32, self.device)
+
+    def wgrad(self, T: int, dy, x, dw_gu, dw_down, overwrite: bool = False, stream=None):
+        """Weight gradients from the last forward's a and the last dgrad's dh;
+        may run any time before either is written again."""
+        self.check_wgrad(T, dy, x, dw_gu, dw_down)
+        self._wgrad(T, dy, x, dw_gu, dw_down, overwrite, stream)
+
+    def _wgrad(self, T: int, dy, x, dw_gu, dw_down, overwrite, stream):
         with _on(self.device):
             L.moe_ffn_wgrad(self.shape(T, overwrite), dy, x, self.a, self.dh, dw_gu, dw_down, self.ws,
                             self.ws.numel(), stream)

@@ -151,9 +151,13 @@ class MoeLayer:
         self._need(self.shared, "shared block weights", shared_w_gu, shared_w_down)
         if self.norm is None and residual is not None:
             raise ValueError("a residual needs a layer made with norm_eps")
+        if self.norm is not None:
+            self.norm.check_forward(T, x, norm_w, residual)
+        if self.shared is not None:
+            self.shared.check_forward(T, x if self.norm is None else self.norm.y, shared_w_gu, shared_w_down)
         normed = None
         if self.norm is not None:
-            normed = self.norm.forward(T, x, norm_w, residual, stream)
+            normed = self.norm._forward(T, x, norm_w, residual, stream)
             self.norm_summed = residual is not None
             x = normed.y
         s = self.shape(T)
@@ -166,7 +170,7 @@ class MoeLayer:
                                self.fwd_ws.numel(), stream)
         L.moe_unpermute_combine(s, self.y, self.topk_w, self.row_of_slot, self.out, stream)
         if self.shared is not None:
-            self.shared.forward(T, x, shared_w_gu, shared_w_down, add=self.out, out=self.out, stream=stream)
+            self.shared._forward(T, x, shared_w_gu, shared_w_down, self.out, self.out, stream)
         saved = self.saved(T)
         saved.norm = normed
         return saved
@@ -192,6 +196,13 @@ class MoeLayer:
             x = self.norm.y
         elif self.shared is not None and x is None:
             raise ValueError("the shared block's weight gradient needs x")
+        # all of it before the first launch: what has run has accumulated
+        if self.shared is not None:
+            self.shared.check_dgrad(T, dout, shared_w_gu, shared_w_down)
+            self.shared.check_wgrad(T, dout, x, dshared_w_gu, dshared_w_down)
+        if self.norm is not None:
+            norm_r = self.norm.r if norm_r is None else norm_r
+            self.norm.check_backward(T, self.dx, norm_r, norm_w, dnorm_w, dres)
         s = self.shape(T)
         L.moe_unpermute_combine_bwd(s, dout, self.y, self.topk_w, self.row_of_slot, self.dy, self.dtopk_w, stream)
         use_router = w_router is not None
@@ -207,11 +218,10 @@ class MoeLayer:
                           stream)
         dx = self.dx
         if self.shared is not None:
-            self.shared.dgrad(T, dout, shared_w_gu, shared_w_down, add=dx, out=dx, stream=stream)
-            self.shared.wgrad(T, dout, x, dshared_w_gu, dshared_w_down, stream=stream)
+            self.shared._dgrad(T, dout, shared_w_gu, shared_w_down, dx, dx, stream)
+            self.shared._wgrad(T, dout, x, dshared_w_gu, dshared_w_down, False, stream)
         if self.norm is not None:
-            self.norm.backward(T, dx, self.norm.r if norm_r is None else norm_r, norm_w, dnorm_w, dres=dres, out=dx,
-                               stream=stream)
+            self.norm._backward(T, dx, norm_r, norm_w, dnorm_w, dres, False, dx, stream)
         R = T * self.k
         return dict(dy=self.dy[:R], dtopk_w=self.dtopk_w[:T], dlogits=self.dlogits[:T], dx_perm=self.dx_perm[:R],
                     dx=self.dx[:T], dh=self.dh_view(T),
