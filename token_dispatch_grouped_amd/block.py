@@ -58,6 +58,15 @@ def _check_mx8(name: str, m, rows: Optional[int], shape: Tuple[int, ...], device
     _check(name + ".scale", m.scale, rows, tail, torch.float8_e8m0fnu, device)
 
 
+def _check_apart(name: str, t: torch.Tensor, T: int, written: torch.Tensor, what: str) -> None:
+    """The first T rows of two contiguous tensors share no memory."""
+    def span(v):
+        return v.data_ptr(), v.data_ptr() + T * v.stride(0) * v.element_size()
+    (a, a_end), (b, b_end) = span(t), span(written)
+    if a < b_end and b < a_end:
+        raise ValueError(f"{name} lies in {what}, which is written before the last read of {name}: give a copy")
+
+
 def _device(device) -> torch.device:
     d = torch.device(device)
     return torch.device("cuda", torch.cuda.current_device()) if d.type == "cuda" and d.index is None else d
@@ -226,10 +235,13 @@ class GatedFfn:
         for name, t in (("out", out), ("add", add)):
             if t is not None:
                 self._rows(name, t, T)
+        if self.save:
+            _check_apart("x", x, T, self.y if out is None else out, "the output")
 
     def forward(self, T: int, x, w_gu, w_down, add=None, out=None, stream=None):
         """y = FFN(x) + add into ``out`` (which may be ``add``) or the object's
-        buffer. MX8: x and the weights are ``Mx8``."""
+        buffer. MX8: x and the weights are ``Mx8``. Where a backward follows
+        the output is not x, which ``wgrad`` reads again."""
         self.check_forward(T, x, w_gu, w_down, add, out)
         return self._forward(T, x, w_gu, w_down, add, out, stream)
 
@@ -249,10 +261,12 @@ class GatedFfn:
         for name, t in (("out", out), ("add", add)):
             if t is not None:
                 self._rows(name, t, T)
+        _check_apart("dy", dy, T, self.dx if out is None else out, "the output")
 
     def dgrad(self, T: int, dy, w_gu, w_down, add=None, out=None, stream=None):
-        """Gradient of x (plus ``add``) from the last forward's h; keeps dh for
-        ``wgrad``."""
+        """Gradient of x (plus ``add``) from the last forward's h into ``out``
+        (which may be ``add``, not dy: ``wgrad`` reads that again) or the
+        object's buffer; keeps dh for ``wgrad``."""
         self.check_dgrad(T, dy, w_gu, w_down, add, out)
         return self._dgrad(T, dy, w_gu, w_down, add, out, stream)
 

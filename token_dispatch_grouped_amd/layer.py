@@ -42,7 +42,7 @@ from typing import Optional
 import torch
 
 from . import _lib as L
-from .block import GatedFfn, NormOut, RmsNorm
+from .block import GatedFfn, NormOut, RmsNorm, _check_apart
 
 
 def torch_dtype(moe_dtype: int):
@@ -146,7 +146,8 @@ class MoeLayer:
                 residual=None, shared_w_gu=None, shared_w_down=None) -> Saved:
         """One forward. ``logits`` (fp32 [T,E]) are copied into the layer's
         logits buffer unless a router weight is given. ``norm_w`` (and
-        ``residual``) with norm_eps, the shared block's weights with shared_F."""
+        ``residual``) with norm_eps, the shared block's weights with shared_F.
+        With shared_F and no norm, x is not the layer's own ``out``."""
         self._need(self.norm, "norm weights", norm_w)
         self._need(self.shared, "shared block weights", shared_w_gu, shared_w_down)
         if self.norm is None and residual is not None:
@@ -155,6 +156,8 @@ class MoeLayer:
             self.norm.check_forward(T, x, norm_w, residual)
         if self.shared is not None:
             self.shared.check_forward(T, x if self.norm is None else self.norm.y, shared_w_gu, shared_w_down)
+            if self.norm is None:
+                _check_apart("x", x, T, self.out, "the layer's output")
         normed = None
         if self.norm is not None:
             normed = self.norm._forward(T, x, norm_w, residual, stream)
@@ -184,7 +187,9 @@ class MoeLayer:
         nothing if it had a residual: the layer keeps that sum), ``dres`` the
         gradient that reaches the residual stream directly, and dx is the
         gradient of the forward's x (and of its residual). With shared_F but
-        no norm, x is needed as with a router."""
+        no norm, x is needed as with a router. The dx of an earlier step lies
+        in the layer's buffer, which this one writes early: with shared_F it
+        is copied before it is given as dout, with norm_eps as dres."""
         self._need(self.norm, "norm_w and dnorm_w", norm_w, dnorm_w)
         self._need(self.shared, "the shared block's weights and their gradients", shared_w_gu, shared_w_down,
                    dshared_w_gu, dshared_w_down)
@@ -198,11 +203,17 @@ class MoeLayer:
             raise ValueError("the shared block's weight gradient needs x")
         # all of it before the first launch: what has run has accumulated
         if self.shared is not None:
-            self.shared.check_dgrad(T, dout, shared_w_gu, shared_w_down)
             self.shared.check_wgrad(T, dout, x, dshared_w_gu, dshared_w_down)
+            _check_apart("dout", dout, T, self.dx, "the layer's dx")
+            self.shared.check_dgrad(T, dout, shared_w_gu, shared_w_down, out=self.dx)
+            if self.norm is None:
+                _check_apart("x", x, T, self.out, "the layer's output")
         if self.norm is not None:
             norm_r = self.norm.r if norm_r is None else norm_r
             self.norm.check_backward(T, self.dx, norm_r, norm_w, dnorm_w, dres)
+            _check_apart("norm_r", norm_r, T, self.out, "the layer's output")
+            if dres is not None:
+                _check_apart("dres", dres, T, self.dx, "the layer's dx")
         s = self.shape(T)
         L.moe_unpermute_combine_bwd(s, dout, self.y, self.topk_w, self.row_of_slot, self.dy, self.dtopk_w, stream)
         use_router = w_router is not None
