@@ -77,16 +77,16 @@ TRAFFIC_SOURCES = ("token_dispatch_grouped_amd/csrc/gemm_bf16.hip", "token_dispa
                    "token_dispatch_grouped_amd/csrc/gemm_bf16_kernel.h", "token_dispatch_grouped_amd/csrc/gemm_common.h",
                    "token_dispatch_grouped_amd/csrc/common.h", "token_dispatch_grouped_amd/build.py")
 TRAFFIC = {
-    "sources_sha256": "35127b82da5950ab555c4a5420aaa8fe9c220576eca6c991acb413d7168b8742",
+    "sources_sha256": "32a9c3f37debdac69938d2a7342b6141bf5e323099fbb7515c76c635462bdf5f",
     "workload": "ep_share_32k",
     "bytes_per_launch": {
         # read GiB + write GiB, x 2^30
-        "gg_gateup_fwd": (6.969 + 2.062) * 2 ** 30,
-        "gg_down_fwd": (2.437 + 1.000) * 2 ** 30,
-        "gg_down_dgrad": (4.509 + 1.375) * 2 ** 30,
-        "gg_down_wgrad": (6.327 + 0.322) * 2 ** 30,
-        "gg_gateup_dgrad": (5.045 + 1.000) * 2 ** 30,
-        "gg_gateup_wgrad": (10.668 + 0.645) * 2 ** 30,
+        "gg_gateup_fwd": (6.765 + 2.062) * 2 ** 30,
+        "gg_down_fwd": (2.435 + 1.000) * 2 ** 30,
+        "gg_down_dgrad": (4.622 + 1.375) * 2 ** 30,
+        "gg_down_wgrad": (6.416 + 0.322) * 2 ** 30,
+        "gg_gateup_dgrad": (5.076 + 1.000) * 2 ** 30,
+        "gg_gateup_wgrad": (10.681 + 0.645) * 2 ** 30,
     },
 }
 

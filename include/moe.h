@@ -576,6 +576,148 @@ moe_status moe_ffn_dgrad(const moe_ffn_shape *shape, const void *dy, const void 
 moe_status moe_ffn_wgrad(const moe_ffn_shape *shape, const void *dy, const void *x, const void *a, const void *dh,
                          float *dw_gu, float *dw_down, void *ws, size_t ws_bytes, moe_stream_t stream);
 
+/*
+ * Layer norm with the residual's addition, for models whose blocks use it
+ * where others use the RMS norm; its y feeds the same calls.
+ *   r    = x + residual                                [T,d] s   (rounded once)
+ *   mean = mean_d(r)                                   [T] fp32
+ *   rstd = 1 / sqrt(mean_d((r - mean)^2) + eps)        [T] fp32
+ *   y    = (r - mean) * rstd * weight + bias           [T,d] s
+ * The shape, the roundings and the rules for r are moe_rmsnorm_fwd's. weight
+ * and bias are [d] s; bias may be NULL (none). Rows whose mean is many times
+ * their spread keep the spread's digits, and rows of any finite r have their
+ * mean and rstd, also those whose sums pass fp32's range. T == 0 writes
+ * nothing.
+ *
+ * Backward, from dL/dy, with n = (r - mean) * rstd and g = dy * weight:
+ *   dx  = rstd * (g - mean_d(g) - n * mean_d(g * n)) + dres     [T,d] s
+ *   dw += sum_t dy * n,   db += sum_t dy                        [d] fp32
+ * db may be NULL (not wanted). dres, dx, MOE_NORM_OVERWRITE_DW (which holds
+ * for dw and db), the order of the sums and ws (the bytes
+ * moe_layernorm_workspace_size reports) are as in moe_rmsnorm_bwd.
+ */
+moe_status moe_layernorm_workspace_size(const moe_norm_shape *shape, size_t *bwd_ws);
+moe_status moe_layernorm_fwd(const moe_norm_shape *shape, const void *x, const void *residual, const void *weight,
+                             const void *bias, void *r, void *y, float *mean, float *rstd, moe_stream_t stream);
+moe_status moe_layernorm_bwd(const moe_norm_shape *shape, const void *dy, const void *r, const void *weight,
+                             const float *mean, const float *rstd, const void *dres, void *dx, float *dw, float *db,
+                             void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * Dense product with bias, activation and residual: a projection, or two of
+ * them as the ungated feed-forward block (the gated one is moe_ffn_fwd).
+ *   z = x w^T + bias              [T,N]
+ *   y = act(z) + residual         [T,N] s   (one rounding, from the fp32 z)
+ * x [T,K] s, w [N,K] s; bias [N] s and residual [T,N] s may be NULL, and
+ * residual may be y itself. z [T,N] s (may be NULL) keeps z, rounded, for a
+ * backward through the activation.
+ *
+ * Activations, with Phi the normal distribution's:
+ *   RELU max(z, 0)    GELU z Phi(z)    SILU z / (1 + e^-z)
+ *   GELU_TANH z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2
+ *
+ * Backward. The gradient in front of this product's own activation is
+ *   dz = dy * act'(z)             [T,N] s   moe_linear_dact; without one dz is dy
+ * and from it, with the activation act_in that made x from z_in [T,K] s
+ * (MOE_ACT_NONE: z_in must be NULL),
+ *   dx = (dz w) * act_in'(z_in) + add         [T,K] s   moe_linear_dgrad
+ *   dw += dz^T x, db += sum_t dz              fp32      moe_linear_wgrad
+ * so that in a chain of products dx is the dz of the one below: only a last
+ * activation needs moe_linear_dact. dz may be dy or z in moe_linear_dact; add
+ * may be NULL or dx itself, and dx may be z_in; db may be NULL (not wanted).
+ * dw [N,K] and db [N] accumulate; MOE_LINEAR_OVERWRITE_DW writes them instead
+ * (T == 0 then writes zeros and the other tensors may be NULL). Sums run in
+ * fp32 in an order that depends on the shape alone (no atomics). ws serves
+ * moe_linear_wgrad and every smaller T of the same K and N. T == 0 otherwise
+ * writes nothing.
+ * Supported: T < 2^24, K and N positive multiples of 64, at most 65536, T *
+ * max(K, N) small enough for one launch, dtype BF16. shape->act is the
+ * product's own activation (moe_linear_fwd, moe_linear_dact); the other calls
+ * do not look at it beyond checking it.
+ */
+enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_GELU = 2, MOE_ACT_GELU_TANH = 3, MOE_ACT_SILU = 4 };
+enum { MOE_LINEAR_OVERWRITE_DW = 1u };
+
+typedef struct moe_linear_shape {
+  int64_t T;      /* tokens (>= 0) */
+  int32_t K;      /* columns of x */
+  int32_t N;      /* columns of y */
+  int32_t dtype;  /* MOE_DTYPE_BF16 */
+  int32_t act;    /* MOE_ACT_* */
+  uint32_t flags; /* MOE_LINEAR_* */
+} moe_linear_shape;
+
+moe_status moe_linear_workspace_size(const moe_linear_shape *shape, size_t *wgrad_ws);
+moe_status moe_linear_fwd(const moe_linear_shape *shape, const void *x, const void *w, const void *bias,
+                          const void *residual, void *z, void *y, moe_stream_t stream);
+moe_status moe_linear_dact(const moe_linear_shape *shape, const void *dy, const void *z, void *dz,
+                           moe_stream_t stream);
+moe_status moe_linear_dgrad(const moe_linear_shape *shape, const void *dz, const void *w, const void *z_in,
+                            int32_t act_in, const void *add, void *dx, moe_stream_t stream);
+moe_status moe_linear_wgrad(const moe_linear_shape *shape, const void *dz, const void *x, float *dw, float *db,
+                            void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * Orthogonalisation of a batch of matrices by Newton-Schulz products, and the
+ * optimiser step built on it (Muon), for expert and dense weights. For each
+ * matrix U [rows, cols] of the batch:
+ *   X = U / (|U| + eps)                    |U| the Frobenius norm
+ *   X = a X + (b A + c A A) X, A = X X^T   `steps` times
+ *   o = X                                  [rows, cols] bf16
+ * (Taller than wide, the same on the transpose.) With a, b, c = 3.4445, -4.7750,
+ * 2.0315 and 5 steps the singular values of o lie near 1, but for those of U
+ * far below its largest. x is fp32 or bf16 (shape->dtype); o may be x itself
+ * where x is bf16. The products take fp16 operands and fp32 sums (X to 22 bits
+ * in the terms that carry it): against the formula the result is off by about
+ * 5e-4 of its norm before o's rounding. A matrix that holds an infinity or a
+ * NaN gives NaN throughout; a matrix of zeros, zeros.
+ *
+ * The step, with G = grad_scale * grad, on fp32 weights and momentum:
+ *   momentum = mu * momentum + G
+ *   U        = G + mu * momentum (MOE_MUON_NESTEROV) or momentum
+ *   param    = param * (1 - lr * weight_decay) - lr * scale * o
+ * with o in fp32; param_bf16 (may be NULL) is written with the rounded new
+ * param, the working copy, and MOE_MUON_ZERO_GRAD clears grad on the way.
+ * `scale` is the caller's: sqrt(max(1, rows / cols)), or 0.2 * sqrt(max(rows,
+ * cols)) for updates of the size AdamW's have, are in use.
+ *
+ * A weight that stacks several matrices along its rows (w_gu [E,2F,d]: gate and
+ * up) is a batch of more, smaller matrices (2E of [F,d]). ws: the bytes
+ * moe_orthogonalize_workspace_size reports, which serve both calls and every
+ * smaller batch of the same rows and cols. batch == 0 writes nothing. Every
+ * sum runs in an order that depends on the shape alone (no atomics).
+ * Supported: rows and cols from 1 to 65536 (any), steps from 1 to 16, eps
+ * positive and finite, batch * rows * cols up to about 2^34, coefficients
+ * whose iterates' singular values stay below fp16's range (checked: with
+ * largest value m, from 1 on, m^2 and max |b l + c l^2|, l <= m^2, at most 15).
+ */
+enum { MOE_MUON_NESTEROV = 1u, MOE_MUON_ZERO_GRAD = 2u };
+
+typedef struct moe_orth_shape {
+  int64_t batch;  /* matrices (>= 0) */
+  int32_t rows;
+  int32_t cols;
+  int32_t dtype;  /* of x: MOE_DTYPE_F32 or MOE_DTYPE_BF16; moe_muon_step: F32 */
+  int32_t steps;
+  float a, b, c;  /* coefficients */
+  float eps;      /* added to the norm */
+} moe_orth_shape;
+
+typedef struct moe_muon_config {
+  float lr;
+  float momentum;      /* mu, in [0, 1) */
+  float weight_decay;
+  float scale;         /* of the orthogonalised update */
+  float grad_scale;
+  uint32_t flags;      /* MOE_MUON_* */
+} moe_muon_config;
+
+moe_status moe_orthogonalize_workspace_size(const moe_orth_shape *shape, size_t *ws);
+moe_status moe_orthogonalize(const moe_orth_shape *shape, const void *x, void *o, void *ws, size_t ws_bytes,
+                             moe_stream_t stream);
+moe_status moe_muon_step(const moe_muon_config *cfg, const moe_orth_shape *shape, float *param, float *grad,
+                         float *momentum, void *param_bf16, void *ws, size_t ws_bytes, moe_stream_t stream);
+
 /* Static English text for a status code. */
 const char *moe_status_string(moe_status status);
 

@@ -10,7 +10,9 @@ the layer's definition; see ``oracle.moe`` for the layer's functions,
 ``oracle.optim`` for the optimizer update, ``oracle.aux`` for the auxiliary
 losses and routing metrics, ``oracle.ep`` for the expert-parallel token
 exchange, ``oracle.norm`` and ``oracle.ffn`` for the norm and the dense block
-beside the experts, and the passages each one follows.
+beside the experts, ``oracle.linear`` for the layer norm and the dense product,
+``oracle.orth`` for the orthogonalised update, and the passages each one
+follows.
 """
 from .moe import *  # noqa: F401,F403
 from .moe import __all__ as _moe_all
@@ -24,5 +26,10 @@ from .norm import *  # noqa: F401,F403
 from .norm import __all__ as _norm_all
 from .ffn import *  # noqa: F401,F403
 from .ffn import __all__ as _ffn_all
+from .linear import *  # noqa: F401,F403
+from .linear import __all__ as _linear_all
+from .orth import *  # noqa: F401,F403
+from .orth import __all__ as _orth_all
 
 __all__ = list(_moe_all) + list(_optim_all) + list(_aux_all) + list(_ep_all) + list(_norm_all) + list(_ffn_all)
+__all__ += list(_linear_all) + list(_orth_all)

@@ -18,8 +18,16 @@ from ._lib import (  # noqa: F401
     MOE_DTYPE_MX8, MOE_NORM_OVERWRITE_DW, MOE_FFN_OVERWRITE_DW, moe_norm_shape, make_norm_shape,
     moe_rmsnorm_workspace_size, moe_rmsnorm_fwd, moe_rmsnorm_bwd, moe_mx8_quantize, moe_ffn_shape, make_ffn_shape,
     moe_ffn_workspace_size, moe_ffn_fwd, moe_ffn_dgrad, moe_ffn_wgrad,
+    moe_layernorm_workspace_size, moe_layernorm_fwd, moe_layernorm_bwd,
+    MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_SILU, MOE_LINEAR_OVERWRITE_DW,
+    moe_linear_shape, make_linear_shape, moe_linear_workspace_size, moe_linear_fwd, moe_linear_dact, moe_linear_dgrad,
+    moe_linear_wgrad,
+    MOE_MUON_NESTEROV, MOE_MUON_ZERO_GRAD, moe_orth_shape, make_orth_shape, moe_muon_config, make_muon_config,
+    moe_orthogonalize_workspace_size, moe_orthogonalize, moe_muon_step,
 )
 
 __all__ = [n for n in dir() if n.startswith(("moe_", "MOE_"))] + ["MoeError", "load", "make_shape",
                                                                   "make_adamw_config", "make_aux_config",
-                                                                  "make_norm_shape", "make_ffn_shape"]
+                                                                  "make_norm_shape", "make_ffn_shape",
+                                                                  "make_linear_shape", "make_orth_shape",
+                                                                  "make_muon_config"]

@@ -68,12 +68,33 @@ class moe_ffn_shape(ctypes.Structure):
                 ("flags", ctypes.c_uint32)]
 
 
+class moe_linear_shape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("K", ctypes.c_int32), ("N", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class moe_orth_shape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("steps", ctypes.c_int32), ("a", ctypes.c_float), ("b", ctypes.c_float),
+                ("c", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class moe_muon_config(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("scale", ctypes.c_float), ("grad_scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
 MOE_NORM_OVERWRITE_DW = 1
 MOE_FFN_OVERWRITE_DW = 1
+MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_SILU = range(5)
+MOE_LINEAR_OVERWRITE_DW = 1
+MOE_MUON_NESTEROV, MOE_MUON_ZERO_GRAD = 1, 2
 
 _S = ctypes.POINTER(moe_shape)
 _NS = ctypes.POINTER(moe_norm_shape)
 _FS = ctypes.POINTER(moe_ffn_shape)
+_LS = ctypes.POINTER(moe_linear_shape)
+_OS = ctypes.POINTER(moe_orth_shape)
 _SZ = ctypes.c_size_t
 
 _SIGNATURES = {
@@ -112,6 +133,17 @@ _SIGNATURES = {
     "moe_ffn_fwd": (ctypes.c_int, [_FS, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "moe_ffn_dgrad": (ctypes.c_int, [_FS, _P, _P, _P, _P, _P, _P, _P, _P]),
     "moe_ffn_wgrad": (ctypes.c_int, [_FS, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_layernorm_workspace_size": (ctypes.c_int, [_NS, ctypes.POINTER(_SZ)]),
+    "moe_layernorm_fwd": (ctypes.c_int, [_NS, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_layernorm_bwd": (ctypes.c_int, [_NS, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_linear_workspace_size": (ctypes.c_int, [_LS, ctypes.POINTER(_SZ)]),
+    "moe_linear_fwd": (ctypes.c_int, [_LS, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_linear_dact": (ctypes.c_int, [_LS, _P, _P, _P, _P]),
+    "moe_linear_dgrad": (ctypes.c_int, [_LS, _P, _P, _P, ctypes.c_int32, _P, _P, _P]),
+    "moe_linear_wgrad": (ctypes.c_int, [_LS, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_orthogonalize_workspace_size": (ctypes.c_int, [_OS, ctypes.POINTER(_SZ)]),
+    "moe_orthogonalize": (ctypes.c_int, [_OS, _P, _P, _P, _SZ, _P]),
+    "moe_muon_step": (ctypes.c_int, [ctypes.POINTER(moe_muon_config), _OS, _P, _P, _P, _P, _P, _SZ, _P]),
     # include/moe_peak.h
     "moe_peak_mfma": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.POINTER(ctypes.c_double), _P]),
     "moe_peak_mfma_size": (ctypes.c_int64, []),
@@ -384,6 +416,86 @@ def moe_ffn_dgrad(shape, dy, h, w_gu, w_down, add, dh, dx, stream=None):
 def moe_ffn_wgrad(shape, dy, x, a, dh, dw_gu, dw_down, ws, ws_bytes, stream=None):
     _check(load().moe_ffn_wgrad(ctypes.byref(shape), ptr(dy), ptr(x), ptr(a), ptr(dh), ptr(dw_gu), ptr(dw_down),
                                 ptr(ws), int(ws_bytes), _stream(stream)), "moe_ffn_wgrad")
+
+
+def moe_layernorm_workspace_size(shape: moe_norm_shape) -> int:
+    a = _SZ()
+    _check(load().moe_layernorm_workspace_size(ctypes.byref(shape), ctypes.byref(a)), "moe_layernorm_workspace_size")
+    return a.value
+
+
+def moe_layernorm_fwd(shape, x, residual, weight, bias, r, y, mean, rstd, stream=None):
+    _check(load().moe_layernorm_fwd(ctypes.byref(shape), ptr(x), ptr(residual), ptr(weight), ptr(bias), ptr(r), ptr(y),
+                                    ptr(mean), ptr(rstd), _stream(stream)), "moe_layernorm_fwd")
+
+
+def moe_layernorm_bwd(shape, dy, r, weight, mean, rstd, dres, dx, dw, db, ws, ws_bytes, stream=None):
+    _check(load().moe_layernorm_bwd(ctypes.byref(shape), ptr(dy), ptr(r), ptr(weight), ptr(mean), ptr(rstd), ptr(dres),
+                                    ptr(dx), ptr(dw), ptr(db), ptr(ws), int(ws_bytes), _stream(stream)),
+           "moe_layernorm_bwd")
+
+
+def make_linear_shape(T: int, K: int, N: int, dtype: int = MOE_DTYPE_BF16, act: int = MOE_ACT_NONE,
+                      flags: int = 0) -> moe_linear_shape:
+    return moe_linear_shape(int(T), int(K), int(N), int(dtype), int(act), int(flags))
+
+
+def moe_linear_workspace_size(shape: moe_linear_shape) -> int:
+    a = _SZ()
+    _check(load().moe_linear_workspace_size(ctypes.byref(shape), ctypes.byref(a)), "moe_linear_workspace_size")
+    return a.value
+
+
+def moe_linear_fwd(shape, x, w, bias, residual, z, y, stream=None):
+    _check(load().moe_linear_fwd(ctypes.byref(shape), ptr(x), ptr(w), ptr(bias), ptr(residual), ptr(z), ptr(y),
+                                 _stream(stream)), "moe_linear_fwd")
+
+
+def moe_linear_dact(shape, dy, z, dz, stream=None):
+    _check(load().moe_linear_dact(ctypes.byref(shape), ptr(dy), ptr(z), ptr(dz), _stream(stream)), "moe_linear_dact")
+
+
+def moe_linear_dgrad(shape, dz, w, z_in, act_in, add, dx, stream=None):
+    _check(load().moe_linear_dgrad(ctypes.byref(shape), ptr(dz), ptr(w), ptr(z_in), int(act_in), ptr(add), ptr(dx),
+                                   _stream(stream)), "moe_linear_dgrad")
+
+
+def moe_linear_wgrad(shape, dz, x, dw, db, ws, ws_bytes, stream=None):
+    _check(load().moe_linear_wgrad(ctypes.byref(shape), ptr(dz), ptr(x), ptr(dw), ptr(db), ptr(ws), int(ws_bytes),
+                                   _stream(stream)), "moe_linear_wgrad")
+
+
+ORTH_COEF = (3.4445, -4.7750, 2.0315)
+
+
+def make_orth_shape(batch: int, rows: int, cols: int, dtype: int = MOE_DTYPE_F32, steps: int = 5, coef=ORTH_COEF,
+                    eps: float = 1e-7) -> moe_orth_shape:
+    a, b, c = coef
+    return moe_orth_shape(int(batch), int(rows), int(cols), int(dtype), int(steps), float(a), float(b), float(c),
+                          float(eps))
+
+
+def make_muon_config(lr: float, momentum: float = 0.95, weight_decay: float = 0.0, scale: float = 1.0,
+                     grad_scale: float = 1.0, nesterov: bool = True, zero_grad: bool = False) -> moe_muon_config:
+    flags = (MOE_MUON_NESTEROV if nesterov else 0) | (MOE_MUON_ZERO_GRAD if zero_grad else 0)
+    return moe_muon_config(float(lr), float(momentum), float(weight_decay), float(scale), float(grad_scale), flags)
+
+
+def moe_orthogonalize_workspace_size(shape: moe_orth_shape) -> int:
+    a = _SZ()
+    _check(load().moe_orthogonalize_workspace_size(ctypes.byref(shape), ctypes.byref(a)),
+           "moe_orthogonalize_workspace_size")
+    return a.value
+
+
+def moe_orthogonalize(shape, x, o, ws, ws_bytes, stream=None):
+    _check(load().moe_orthogonalize(ctypes.byref(shape), ptr(x), ptr(o), ptr(ws), int(ws_bytes), _stream(stream)),
+           "moe_orthogonalize")
+
+
+def moe_muon_step(cfg, shape, param, grad, momentum, param_bf16, ws, ws_bytes, stream=None):
+    _check(load().moe_muon_step(ctypes.byref(cfg), ctypes.byref(shape), ptr(param), ptr(grad), ptr(momentum),
+                                ptr(param_bf16), ptr(ws), int(ws_bytes), _stream(stream)), "moe_muon_step")
 
 
 def moe_peak_mfma_size() -> int:

@@ -1,6 +1,7 @@
 """What stands in front of and beside the expert layer, over the C ABI:
-``RmsNorm`` (``moe_rmsnorm_*``), ``GatedFfn`` (``moe_ffn_*``) and the 8-bit
-block form of a matrix (``moe_mx8_quantize``).
+``RmsNorm`` (``moe_rmsnorm_*``), ``LayerNorm`` (``moe_layernorm_*``),
+``GatedFfn`` (``moe_ffn_*``), ``Linear`` (``moe_linear_*``) and the 8-bit block
+form of a matrix (``moe_mx8_quantize``).
 
 As in ``layer.py``, PyTorch only allocates and provides the stream; buffers
 and workspaces are made once for the largest microbatch (``T_max``) and serve
@@ -294,3 +295,197 @@ class GatedFfn:
         with _on(self.device):
             L.moe_ffn_wgrad(self.shape(T, overwrite), dy, x, self.a, self.dh, dw_gu, dw_down, self.ws,
                             self.ws.numel(), stream)
+
+
+@dataclasses.dataclass
+class LayerNormOut:
+    """Views of a layer norm's outputs for one microbatch."""
+    r: Optional[torch.Tensor]  # the new residual stream; None without a residual (it is x)
+    y: torch.Tensor
+    mean: torch.Tensor
+    rstd: torch.Tensor
+
+
+class LayerNorm:
+    def __init__(self, T_max: int, d: int, dtype: int = L.MOE_DTYPE_BF16, eps: float = 1e-5, device: str = "cuda"):
+        self.T_max, self.d, self.dtype, self.eps = T_max, d, dtype, eps
+        self.ws_bytes = L.moe_layernorm_workspace_size(self.shape(T_max))
+        self.device = dev = _device(device)
+        self.td = _TORCH[dtype]
+        self.ws = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=dev)
+        self.r = torch.empty(T_max, d, dtype=self.td, device=dev)
+        self.y = torch.empty(T_max, d, dtype=self.td, device=dev)
+        self.mean = torch.empty(T_max, dtype=torch.float32, device=dev)
+        self.rstd = torch.empty(T_max, dtype=torch.float32, device=dev)
+        self.dx = None  # made by the first backward: serving needs none
+
+    def shape(self, T: int, overwrite: bool = False) -> L.moe_norm_shape:
+        return L.make_norm_shape(T, self.d, self.dtype, self.eps, L.MOE_NORM_OVERWRITE_DW if overwrite else 0)
+
+    def _vector(self, name, t, dtype):
+        _check(name, t, None, (self.d,), dtype, self.device)
+
+    def check_forward(self, T: int, x, weight, bias=None, residual=None) -> None:
+        _check_T(T, self.T_max)
+        _check("x", x, T, (self.d,), self.td, self.device)
+        self._vector("weight", weight, self.td)
+        if bias is not None:
+            self._vector("bias", bias, self.td)
+        if residual is not None:
+            _check("residual", residual, T, (self.d,), self.td, self.device)
+
+    def forward(self, T: int, x, weight, bias=None, residual=None, stream=None) -> LayerNormOut:
+        """y = norm(x + residual) * weight + bias; r = x + residual is the new
+        residual stream (in the object's buffer, valid until the next
+        forward)."""
+        self.check_forward(T, x, weight, bias, residual)
+        r = self.r if residual is not None else None
+        with _on(self.device):
+            L.moe_layernorm_fwd(self.shape(T), x, residual, weight, bias, r, self.y, self.mean, self.rstd, stream)
+        return LayerNormOut(None if r is None else r[:T], self.y[:T], self.mean[:T], self.rstd[:T])
+
+    def check_backward(self, T: int, dy, r, weight, dw, db=None, dres=None, out=None) -> None:
+        _check_T(T, self.T_max)
+        for name, t in (("dy", dy), ("r", r)) + ((("dres", dres),) if dres is not None else ()):
+            _check(name, t, T, (self.d,), self.td, self.device)
+        self._vector("weight", weight, self.td)
+        self._vector("dw", dw, torch.float32)
+        if db is not None:
+            self._vector("db", db, torch.float32)
+        if out is not None:
+            _check("out", out, T, (self.d,), self.td, self.device)
+
+    def backward(self, T: int, dy, r, weight, dw, db=None, dres=None, overwrite: bool = False, out=None, stream=None):
+        """Gradient of x (and of the residual alike) from dL/dy, with the mean
+        and ``rstd`` of the last forward; ``r``: that forward's r, or its x if
+        it had no residual; ``dres``: the gradient that reaches r directly.
+        ``dw`` and ``db`` [d] fp32 accumulate (``overwrite``: are written)."""
+        self.check_backward(T, dy, r, weight, dw, db, dres, out)
+        if out is None:
+            if self.dx is None:
+                with _made_on(self.device, stream):
+                    self.dx = torch.empty(self.T_max, self.d, dtype=self.td, device=self.device)
+            out = self.dx
+        with _on(self.device):
+            L.moe_layernorm_bwd(self.shape(T, overwrite), dy, r, weight, self.mean, self.rstd, dres, out, dw, db, self.ws,
+                                self.ws.numel(), stream)
+        return out[:T]
+
+
+class Linear:
+    def __init__(self, T_max: int, K: int, N: int, act: int = L.MOE_ACT_NONE, save: bool = True, device: str = "cuda"):
+        """y = act(x w^T + bias) + residual with w [N, K], bf16. ``save``: a
+        backward follows (z is kept where there is an activation). Without it
+        only the forward runs."""
+        self.T_max, self.K, self.N, self.act, self.save = T_max, K, N, act, save
+        wgrad = L.moe_linear_workspace_size(self.shape(T_max))
+        self.device = dev = _device(device)
+        new = lambda cols: torch.empty(T_max, cols, dtype=torch.bfloat16, device=dev)  # noqa: E731
+        self.ws = torch.empty(max(wgrad if save else 0, 256), dtype=torch.uint8, device=dev)
+        self.y = new(N)
+        self.z = new(N) if save and act != L.MOE_ACT_NONE else None
+        self.dz = None  # made by the first dact: a product inside a chain needs none
+        self.dx = new(K) if save else None
+
+    def shape(self, T: int, overwrite: bool = False) -> L.moe_linear_shape:
+        return L.make_linear_shape(T, self.K, self.N, L.MOE_DTYPE_BF16, self.act,
+                                   L.MOE_LINEAR_OVERWRITE_DW if overwrite else 0)
+
+    def _rows(self, name, t, T, cols):
+        _check(name, t, T, (cols,), torch.bfloat16, self.device)
+
+    def _weight(self, w):
+        _check("w", w, None, (self.N, self.K), torch.bfloat16, self.device)
+
+    def _backward_ready(self):
+        if not self.save:
+            raise ValueError("this Linear keeps nothing for a backward (save=False)")
+
+    def check_forward(self, T: int, x, w, bias=None, residual=None, out=None) -> None:
+        _check_T(T, self.T_max)
+        self._weight(w)
+        self._rows("x", x, T, self.K)
+        if bias is not None:
+            _check("bias", bias, None, (self.N,), torch.bfloat16, self.device)
+        for name, t in (("residual", residual), ("out", out)):
+            if t is not None:
+                self._rows(name, t, T, self.N)
+        written = self.y if out is None else out
+        _check_apart("x", x, T, written, "the output")
+        if self.z is not None:
+            _check_apart("x", x, T, self.z, "z")
+            _check_apart("the output", written, T, self.z, "z")
+            if residual is not None:
+                _check_apart("residual", residual, T, self.z, "z")
+
+    def forward(self, T: int, x, w, bias=None, residual=None, out=None, stream=None):
+        """y into ``out`` (which may be ``residual``) or the object's buffer."""
+        self.check_forward(T, x, w, bias, residual, out)
+        out = self.y if out is None else out
+        with _on(self.device):
+            L.moe_linear_fwd(self.shape(T), x, w, bias, residual, self.z, out, stream)
+        return out[:T]
+
+    def check_dact(self, T: int, dy, out=None) -> None:
+        self._backward_ready()
+        if self.z is None:
+            raise ValueError("without an activation dz is dy")
+        _check_T(T, self.T_max)
+        self._rows("dy", dy, T, self.N)
+        if out is not None:
+            self._rows("out", out, T, self.N)
+
+    def dact(self, T: int, dy, out=None, stream=None):
+        """dz = dy * act'(z) with the last forward's z, into ``out`` (which may
+        be dy) or the object's buffer: for an activation that ends a chain."""
+        self.check_dact(T, dy, out)
+        if out is None:
+            if self.dz is None:
+                with _made_on(self.device, stream):
+                    self.dz = torch.empty(self.T_max, self.N, dtype=torch.bfloat16, device=self.device)
+            out = self.dz
+        with _on(self.device):
+            L.moe_linear_dact(self.shape(T), dy, self.z, out, stream)
+        return out[:T]
+
+    def check_dgrad(self, T: int, dz, w, below: Optional["Linear"] = None, add=None, out=None) -> None:
+        self._backward_ready()
+        _check_T(T, self.T_max)
+        self._weight(w)
+        self._rows("dz", dz, T, self.N)
+        for name, t in (("add", add), ("out", out)):
+            if t is not None:
+                self._rows(name, t, T, self.K)
+        if below is not None:
+            if below.z is None or below.N != self.K:
+                raise ValueError(f"below: expected a Linear with an activation and N = {self.K} that keeps its z")
+            self._rows("below.z", below.z, T, self.K)
+        _check_apart("dz", dz, T, self.dx if out is None else out, "the output")
+
+    def dgrad(self, T: int, dz, w, below: Optional["Linear"] = None, add=None, out=None, stream=None):
+        """Gradient of x, plus ``add``, into ``out`` (which may be ``add``, not
+        dz: ``wgrad`` reads that again) or the object's buffer. ``below``: the
+        Linear whose last output was x; the result, times the derivative of its
+        activation, is then its dz."""
+        self.check_dgrad(T, dz, w, below, add, out)
+        out = self.dx if out is None else out
+        z, act = (None, L.MOE_ACT_NONE) if below is None else (below.z, below.act)
+        with _on(self.device):
+            L.moe_linear_dgrad(self.shape(T), dz, w, z, act, add, out, stream)
+        return out[:T]
+
+    def check_wgrad(self, T: int, dz, x, dw, db=None) -> None:
+        self._backward_ready()
+        _check_T(T, self.T_max)
+        self._rows("dz", dz, T, self.N)
+        self._rows("x", x, T, self.K)
+        _check("dw", dw, None, (self.N, self.K), torch.float32, self.device)
+        if db is not None:
+            _check("db", db, None, (self.N,), torch.float32, self.device)
+
+    def wgrad(self, T: int, dz, x, dw, db=None, overwrite: bool = False, stream=None):
+        """Weight and bias gradients; may run any time before dz or x is
+        written again."""
+        self.check_wgrad(T, dz, x, dw, db)
+        with _on(self.device):
+            L.moe_linear_wgrad(self.shape(T, overwrite), dz, x, dw, db, self.ws, self.ws.numel(), stream)

@@ -21,7 +21,8 @@ LIB_NAME = "libmoe_mi355x.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 
 SOURCES = ["moe_abi.cpp", "validate.cpp", "route.hip", "dispatch.hip", "gemm_bf16.hip", "gemm_bf16_ilp.hip",
-           "gemm_f32.hip", "optim.hip", "aux.hip", "peak.hip", "ep.hip", "norm.hip", "ffn.hip", "ffn_ilp.hip"]
+           "gemm_f32.hip", "optim.hip", "aux.hip", "peak.hip", "ep.hip", "norm.hip", "ffn.hip", "ffn_ilp.hip",
+           "layernorm.hip", "linear.hip", "orth.hip"]
 # Per-source compiler options: the gate/up forward and weight-gradient GEMM
 # kernels (gemm_bf16_ilp.hip) are scheduled for instruction-level parallelism,
 # which makes them 0.5-1.8% faster and the dgrad kernels slower (those are in

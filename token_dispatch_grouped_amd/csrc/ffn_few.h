@@ -168,7 +168,25 @@ __global__ __launch_bounds__(WAVES * 64, 2) void ffn_few_kernel(FfnTileParams p)
     if (t >= p.M) continue;
     const int c = n0 + f / MF * (EPI == FFN_SWIGLU_FWD ? 8 : 16) + (l >> 4) * 4;
     f32x4_t v = total(f, l);
-    if constexpr (EPI == FFN_STORE) {
+    if constexpr (EPI == FFN_LINEAR) {
+      const int64_t o = (int64_t)t * p.ldc + c;
+      auto plus = [&](const bf16_t *a) {
+        const uint2 b = *reinterpret_cast<const uint2 *>(a);
+        v[0] += __uint_as_float(b.x << 16);
+        v[1] += __uint_as_float(b.x & 0xffff0000u);
+        v[2] += __uint_as_float(b.y << 16);
+        v[3] += __uint_as_float(b.y & 0xffff0000u);
+      };
+      if (p.bias) plus(p.bias + c);
+      if (p.C2) store4(p.C2 + o, v);
+      const ActSigmoid sg = act_sigmoid(p.act);
+      with_act(p.act, [&](auto act) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = act_value<decltype(act)::value>(v[e], sg);
+      });
+      if (p.add) plus(p.add + o);
+      store4(p.C + o, v);
+    } else if constexpr (EPI == FFN_STORE) {
       const int64_t o = (int64_t)t * p.ldc + c;
       if (p.add) {
         const uint2 b = *reinterpret_cast<const uint2 *>(p.add + o);

@@ -82,22 +82,29 @@ static hipError_t reduce(const WgradReduce &r, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_ffn_dense_wgrad(const FfnArgs &a, hipStream_t s) {
+// dw (+)= A^T B over the tokens for one or two products: product i is
+// [M[i], N[i]], its operands [T, M[i]] and [T, N[i]].
+struct WgradProduct {
+  const void *a, *b;
+  int M, N;
+  float *dw;
+};
+
+static hipError_t wgrad(const WgradProduct *prod, int count, const FfnWgrad &plan, int64_t T, float *ws, bool accumulate,
+                        const char *name, hipStream_t s) {
   WgradParams w{};
   WgradReduce r{};
-  w.T = (int)a.T;
-  r.accumulate = a.accumulate ? 1 : 0;
-  const FfnWgrad plan = ffn_wgrad_plan(a.T, a.d, a.F);
+  w.T = (int)T;
+  r.accumulate = accumulate ? 1 : 0;
   const int slices = plan.slices;  // 0 without tokens
   r.slices = slices;
   w.chunk = plan.chunk;
-  float *ws = static_cast<float *>(a.partial);
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < count; ++i) {
     GemmParams &p = w.g[i];
-    p.A = (const bf16_t *)(i == 0 ? a.dh : a.dy);
-    p.B = (const bf16_t *)(i == 0 ? a.x : a.a);
-    p.M = i == 0 ? 2 * a.F : a.d;
-    p.N = i == 0 ? a.d : a.F;
+    p.A = (const bf16_t *)prod[i].a;
+    p.B = (const bf16_t *)prod[i].b;
+    p.M = prod[i].M;
+    p.N = prod[i].N;
     p.lda = p.M;
     p.ldb = p.N;
     p.ldc = p.N;
@@ -105,25 +112,36 @@ hipError_t launch_ffn_dense_wgrad(const FfnArgs &a, hipStream_t s) {
     p.m_tiles = (p.M + plan.tile - 1) / plan.tile;
     p.n_tiles = (p.N + plan.tile - 1) / plan.tile;
     p.total = p.m_tiles * p.n_tiles * slices;
-    float *dw = i == 0 ? a.dw_gu : a.dw_down;
-    p.C = slices == 1 ? dw : ws;
+    p.C = slices == 1 ? prod[i].dw : ws;
     if (slices == 1) continue;
     r.partial[i] = ws;
-    r.dw[i] = dw;
+    r.dw[i] = prod[i].dw;
     r.n4[i] = p.strideC / 4;  // the sum of no slice is zero
     ws += slices * p.strideC;
   }
   const int total = w.g[0].total + w.g[1].total;
   if (total > 0) {
-    LaunchScope scope("ffn_wgrad", s);
+    LaunchScope scope(name, s);
     const dim3 grid((unsigned)(ceil_div(total, 8) * 8));
-    const bool add = slices == 1 && a.accumulate;
+    const bool add = slices == 1 && accumulate;
     if (plan.tile == 256) (add ? ffn_wgrad_kernel<256, EPI_ACC_F32> : ffn_wgrad_kernel<256, EPI_ST_F32>)<<<grid, 512, 0, s>>>(w);
     else (add ? ffn_wgrad_kernel<128, EPI_ACC_F32> : ffn_wgrad_kernel<128, EPI_ST_F32>)<<<grid, 256, 0, s>>>(w);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
   return reduce(r, s);
+}
+
+hipError_t launch_ffn_dense_wgrad(const FfnArgs &a, hipStream_t s) {
+  const WgradProduct prod[2] = {{a.dh, a.x, 2 * a.F, a.d, a.dw_gu}, {a.dy, a.a, a.d, a.F, a.dw_down}};
+  return wgrad(prod, 2, ffn_wgrad_plan(a.T, a.d, a.F), a.T, static_cast<float *>(a.partial), a.accumulate, "ffn_wgrad", s);
+}
+
+// The dense product's weight gradient dW = dz^T x: the same launch with one
+// product.
+hipError_t launch_linear_dw(const LinearArgs &a, hipStream_t s) {
+  const WgradProduct prod = {a.dz, a.x, a.N, a.K, a.dw};
+  return wgrad(&prod, 1, linear_wgrad_plan(a.T, a.K, a.N), a.T, a.partial, a.accumulate, "linear_wgrad", s);
 }
 
 }  // namespace moe

@@ -36,22 +36,25 @@
 // global memory straight from registers.
 #pragma once
 
+#include "act.h"
 #include "gemm_bf16_kernel.h"
 #include "mx8.h"
 
 namespace moe {
 
-enum { FFN_SWIGLU_FWD = 0, FFN_STORE = 1, FFN_SWIGLU_BWD = 2 };
+enum { FFN_SWIGLU_FWD = 0, FFN_STORE = 1, FFN_SWIGLU_BWD = 2, FFN_LINEAR = 3, FFN_LINEAR_DX = 4 };
 
 struct FfnTileParams {
   const bf16_t *A, *B;         // F8: e4m3 bytes; lda, ldb count pairs of them
   const uint8_t *As, *Bs;      // F8: scales [rows, K / 32]
   bf16_t *C;                   // STORE: the output; SWIGLU_FWD: h or NULL; SWIGLU_BWD: dh
-  bf16_t *C2;                  // SWIGLU_FWD: a (bf16, or e4m3 bytes when C2s is given)
+  bf16_t *C2;                  // SWIGLU_FWD: a (bf16, or e4m3 bytes when C2s is given); LINEAR: z or NULL
   uint8_t *C2s;                // SWIGLU_FWD, F8: scales of a
   float *a32;                  // SWIGLU_FWD, F8, few tokens: a in fp32
-  const bf16_t *H;             // SWIGLU_BWD: saved h
-  const bf16_t *add;           // STORE: [M, N] added before the rounding, or NULL; may be C
+  const bf16_t *H;             // SWIGLU_BWD: saved h; LINEAR_DX: z of the activation below, or NULL
+  const bf16_t *add;           // STORE, LINEAR*: [M, N] added before the rounding, or NULL; may be C
+  const bf16_t *bias;          // LINEAR: [N] or NULL
+  int act;                     // LINEAR, LINEAR_DX
   int M, N, K;                 // N: columns of C (SWIGLU: F); K: 16-bit units of a row
   int64_t lda, ldb, ldc;
   int F;
@@ -426,6 +429,99 @@ __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void ffn_tile_k
           }
         }
       }
+    }
+  } else if constexpr (EPI == FFN_LINEAR) {
+    // y = act(acc + bias) + add, and z = acc + bias where it is kept
+    if (p.bias) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int c = n_tile * BN + wn * WN + j * 32 + 8 * g + 4 * ehi;
+          const uint2 b = *reinterpret_cast<const uint2 *>(p.bias + (c < p.N ? c : 0));
+          const float bv[4] = {__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xffff0000u),
+                               __uint_as_float(b.y << 16), __uint_as_float(b.y & 0xffff0000u)};
+#pragma unroll
+          for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[i][j][4 * g + q] += bv[q];
+        }
+    }
+    auto store = [&](bf16_t *C, const bf16_t *add) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        const int r = row_l + i * 32;
+        const bool rok = r < m_valid;
+        const int64_t ro = (int64_t)(m0 + (rok ? r : 0)) * p.ldc;
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int gp = 0; gp < 2; ++gp) {
+            const int c = n_tile * BN + wn * WN + j * 32 + 16 * gp + 8 * ehi;
+            const bool ok = rok && c < p.N;
+            float v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = acc[i][j][8 * gp + q];
+            if (add) {
+              float b[8];
+              unpack_chunk(ok ? ld16(add + ro + c) : u32x4_t{0u, 0u, 0u, 0u}, b);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) v[q] += b[q];
+            }
+            const u32x4_t o = pack_chunk(v);
+            if (ok) st16(C + ro + c, o);
+          }
+      }
+    };
+    if (p.C2) store(p.C2, nullptr);
+    const ActSigmoid sg = act_sigmoid(p.act);
+    with_act(p.act, [&](auto act) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int q = 0; q < 16; ++q) acc[i][j][q] = act_value<decltype(act)::value>(acc[i][j][q], sg);
+    });
+    store(p.C, p.add);
+  } else if constexpr (EPI == FFN_LINEAR_DX) {
+    // dx = acc act'(z) + add
+    const ActSigmoid sg = act_sigmoid(p.act);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int r = row_l + i * 32;
+      const bool rok = r < m_valid;
+      const int64_t ro = (int64_t)(m0 + (rok ? r : 0)) * p.ldc;
+      with_act(p.act, [&](auto act) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int gp = 0; gp < 2; ++gp) {
+            const int c = n_tile * BN + wn * WN + j * 32 + 16 * gp + 8 * ehi;
+            float z[8];
+            unpack_chunk(rok && c < p.N ? ld16(p.H + ro + c) : u32x4_t{0u, 0u, 0u, 0u}, z);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) acc[i][j][8 * gp + q] *= act_slope<decltype(act)::value>(z[q], sg);
+          }
+      });
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int gp = 0; gp < 2; ++gp) {
+          const int c = n_tile * BN + wn * WN + j * 32 + 16 * gp + 8 * ehi;
+          const bool ok = rok && c < p.N;
+          float v[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[q] = acc[i][j][8 * gp + q];
+          if (p.add) {
+            float b[8];
+            unpack_chunk(ok ? ld16(p.add + ro + c) : u32x4_t{0u, 0u, 0u, 0u}, b);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] += b[q];
+          }
+          const u32x4_t o = pack_chunk(v);
+          if (ok) st16(p.C + ro + c, o);
+        }
     }
   } else {  // FFN_SWIGLU_BWD
 #pragma unroll

@@ -145,6 +145,56 @@ hipError_t launch_ffn_dense_fwd(const FfnArgs &a, hipStream_t s);
 hipError_t launch_ffn_dense_dgrad(const FfnArgs &a, hipStream_t s);
 hipError_t launch_ffn_dense_wgrad(const FfnArgs &a, hipStream_t s);
 
+// ----- layer norm (layernorm.hip) -----
+struct LayerNormArgs {
+  const void *x, *residual, *w, *b;  // forward; residual and b may be NULL
+  void *r, *y;
+  float *mean, *rstd;                // forward: written; backward: read
+  const void *dy, *dres;             // backward (r is read); dres may be NULL
+  void *dx;
+  float *dw, *db, *partial;          // db may be NULL
+  int64_t T;
+  int d;
+  float eps;
+  bool bf16, accumulate;
+};
+hipError_t launch_layernorm_fwd(const LayerNormArgs &a, hipStream_t s);
+hipError_t launch_layernorm_bwd(const LayerNormArgs &a, hipStream_t s);
+
+// ----- dense product with bias, activation and residual (linear.hip; the
+// weight gradient in ffn_ilp.hip) -----
+struct LinearArgs {
+  const void *x, *w, *bias, *add;  // bias, add may be NULL
+  void *z, *y;                     // forward: z may be NULL
+  const void *dy;                  // dact
+  void *dz, *dx;                   // dact writes dz, the others read it; dgrad: z is the z of x, act its activation
+  float *dw, *db;
+  float *partial, *db_partial;
+  int64_t T;
+  int K, N, act;
+  bool accumulate;
+};
+hipError_t launch_linear_fwd(const LinearArgs &a, hipStream_t s);
+hipError_t launch_linear_dact(const LinearArgs &a, hipStream_t s);
+hipError_t launch_linear_dgrad(const LinearArgs &a, hipStream_t s);
+hipError_t launch_linear_dw(const LinearArgs &a, hipStream_t s);
+hipError_t launch_linear_db(const LinearArgs &a, hipStream_t s);
+
+// ----- orthogonalisation and the step around it (orth.hip) -----
+struct OrthArgs {
+  const void *x;                    // orthogonalise
+  void *o;
+  float *param, *grad, *momentum;   // step (param != NULL)
+  void *param_bf16;                 // may be NULL
+  void *ws;
+  int64_t batch;
+  int rows, cols, steps;
+  float coef[3], eps;
+  float mu, grad_scale, decay, step_size;
+  bool bf16, nesterov, zero_grad;
+};
+hipError_t launch_orth(const OrthArgs &a, hipStream_t s);
+
 // ----- expert-parallel exchange (ep.hip) -----
 struct EpPtrs {
   void *p[kEpMaxRanks];

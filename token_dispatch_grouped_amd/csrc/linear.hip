@@ -1,0 +1,153 @@
+// The dense product with bias, activation and residual:
+//   z = x W^T + b,  y = act(z) + residual            x [T,K], W [N,K]
+//   dz = dy act'(z)                                  (linear_dact)
+//   dx = (dz W) act_in'(z_in) + add                  (linear_dgrad)
+//   dW (+)= dz^T x, db (+)= sum over tokens of dz    (linear_wgrad)
+// on the dense block's kernels (ffn_kernel.h, ffn_few.h; the weight
+// gradient's in ffn_ilp.hip), with epilogues of its own: bias, activation and
+// residual are applied to the fp32 sums, so that z and y are each rounded once.
+// The input gradient's epilogue applies the derivative of the activation that
+// made x, so a chain of layers needs no elementwise pass between its products.
+#include "act.h"
+#include "ffn_few.h"
+#include "ffn_kernel.h"
+#include "ffn_plan.h"
+
+namespace moe {
+
+static hipError_t forward(const FfnTileParams &p, hipStream_t s) {
+  LaunchScope scope("linear_fwd", s);
+  switch (choose(p.M, p.N, false, false, false)) {
+    case kFew: return run_ffn_few<false, FFN_LINEAR>(p, s);
+    case kSmall: return run_ffn_tile<false, 64, 64, 32, 64, 4, 2, false, FFN_LINEAR>(p, s);
+    case kNarrow: return run_ffn_tile<false, 64, 128, 32, 64, 2, 3, false, FFN_LINEAR>(p, s);
+    case kPair: return run_ffn_tile<false, 128, 128, 64, 64, 2, 2, false, FFN_LINEAR>(p, s);
+    case kHalf: return run_ffn_tile<false, 64, 128, 32, 64, 1, 3, false, FFN_LINEAR>(p, s);
+    case kLarge: return run_ffn_tile<false, 256, 256, 128, 64, 1, 2, false, FFN_LINEAR>(p, s);
+    default: return run_ffn_tile<false, 128, 128, 64, 64, 1, 2, false, FFN_LINEAR>(p, s);
+  }
+}
+
+hipError_t launch_linear_fwd(const LinearArgs &a, hipStream_t s) {
+  FfnTileParams p{};
+  p.A = (const bf16_t *)a.x;
+  p.B = (const bf16_t *)a.w;
+  p.C = (bf16_t *)a.y;
+  p.C2 = (bf16_t *)a.z;
+  p.add = (const bf16_t *)a.add;
+  p.bias = (const bf16_t *)a.bias;
+  p.act = a.act;
+  p.M = (int)a.T;
+  p.N = p.F = a.N;
+  p.K = a.K;
+  p.lda = p.ldb = a.K;
+  p.ldc = a.N;
+  return in_rounds(p, p.N, false, false, false, [&](const FfnTileParams &q) { return forward(q, s); });
+}
+
+static hipError_t dgrad(const FfnTileParams &p, hipStream_t s) {
+  LaunchScope scope("linear_dgrad", s);
+  switch (choose(p.M, p.N, false, false, true)) {
+    case kNarrow: return run_ffn_tile<false, 64, 128, 32, 64, 2, 2, true, FFN_LINEAR_DX>(p, s);
+    case kPair: return run_ffn_tile<false, 128, 128, 64, 64, 2, 2, true, FFN_LINEAR_DX>(p, s);
+    case kLarge: return run_ffn_tile<false, 256, 256, 128, 64, 1, 2, true, FFN_LINEAR_DX>(p, s);
+    default: return run_ffn_tile<false, 128, 128, 64, 64, 1, 2, true, FFN_LINEAR_DX>(p, s);
+  }
+}
+
+hipError_t launch_linear_dgrad(const LinearArgs &a, hipStream_t s) {
+  FfnTileParams p{};
+  p.A = (const bf16_t *)a.dz;
+  p.B = (const bf16_t *)a.w;
+  p.C = (bf16_t *)a.dx;
+  p.H = (const bf16_t *)a.z;
+  p.add = (const bf16_t *)a.add;
+  p.act = a.act;
+  p.M = (int)a.T;
+  p.N = p.F = a.K;
+  p.K = a.N;
+  p.lda = a.N;
+  p.ldb = a.K;
+  p.ldc = a.K;
+  return in_rounds(p, p.N, false, false, true, [&](const FfnTileParams &q) { return dgrad(q, s); });
+}
+
+// ---------------------------------------------------------------------------
+// dz = dy act'(z), a thread 16 bytes of each; dz may be dy or z.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void linear_dact_kernel(const bf16_t *dy, const bf16_t *z, bf16_t *dz, int64_t chunks,
+                                                          int act) {
+  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (c >= chunks) return;
+  float g[8], v[8];
+  Elem<bf16_t>::unpack(ld16(dy + c * 8), g);
+  Elem<bf16_t>::unpack(ld16(z + c * 8), v);
+  const ActSigmoid sg = act_sigmoid(act);
+  with_act(act, [&](auto a) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] *= act_slope<decltype(a)::value>(v[i], sg);
+  });
+  st16(dz + c * 8, Elem<bf16_t>::pack(g));
+}
+
+hipError_t launch_linear_dact(const LinearArgs &a, hipStream_t s) {
+  LaunchScope scope("linear_dact", s);
+  const int64_t chunks = a.T * (a.N / 8);
+  linear_dact_kernel<<<(unsigned)ceil_div(chunks, 256), 256, 0, s>>>((const bf16_t *)a.dy, (const bf16_t *)a.z,
+                                                                      (bf16_t *)a.dz, chunks, a.act);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// db: column sums of dz. A workgroup sums a slice of the tokens of 64
+// columns, 8 to a thread and 32 tokens abreast; a second launch adds the slices
+// in order.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void linear_db_partial_kernel(const bf16_t *dz, float *partial, int T, int N,
+                                                                int chunk) {
+  __shared__ float s[32][65];
+  const int col = threadIdx.x & 7, lane = threadIdx.x >> 3;
+  const int c = blockIdx.x * 64 + col * 8;
+  const int first = blockIdx.y * chunk, last = min(first + chunk, T);
+  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int t = first + lane; t < last; t += 32) {
+    float v[8];
+    Elem<bf16_t>::unpack(ld16(dz + (int64_t)t * N + c), v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] += v[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[lane][col * 8 + i] = sum[i];
+  __syncthreads();
+  if (threadIdx.x >= 64) return;
+  float v = 0.f;
+#pragma unroll
+  for (int l = 0; l < 32; ++l) v += s[l][threadIdx.x];
+  partial[(int64_t)blockIdx.y * N + blockIdx.x * 64 + threadIdx.x] = v;
+}
+
+__global__ __launch_bounds__(64) void linear_db_reduce_kernel(const float *partial, float *db, int N, int slices,
+                                                              int accumulate) {
+  const int c = blockIdx.x * 64 + threadIdx.x;  // N is a multiple of 64
+  float v = 0.f;
+#pragma unroll 8
+  for (int i = 0; i < slices; ++i) v += partial[(int64_t)i * N + c];
+  db[c] = accumulate ? db[c] + v : v;
+}
+
+hipError_t launch_linear_db(const LinearArgs &a, hipStream_t s) {
+  const int slices = linear_db_slices(a.T);
+  LaunchScope scope("linear_db", s);
+  if (slices > 0) {
+    const int chunk = (int)(ceil_div(ceil_div(a.T, slices), 32) * 32);
+    linear_db_partial_kernel<<<dim3((unsigned)(a.N / 64), (unsigned)slices), 256, 0, s>>>(
+        (const bf16_t *)a.dz, a.db_partial, (int)a.T, a.N, chunk);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  linear_db_reduce_kernel<<<(unsigned)(a.N / 64), 64, 0, s>>>(a.db_partial, a.db, a.N, slices, a.accumulate ? 1 : 0);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -837,6 +837,282 @@ moe_status moe_ffn_wgrad(const moe_ffn_shape *shape, const void *dy, const void 
   return hip_status(launch_ffn_dense_wgrad(f, as_stream(stream)), "ffn_wgrad");
 }
 
+// ----- layer norm, dense product, orthogonalisation -----
+moe_status moe_layernorm_workspace_size(const moe_norm_shape *shape, size_t *bwd_ws) {
+  std::string why;
+  const moe_status st = validate_norm(shape, &why);
+  if (st != MOE_OK) return report(st, why);
+  if (bwd_ws) *bwd_ws = layernorm_workspace(*shape);
+  return MOE_OK;
+}
+
+moe_status moe_layernorm_fwd(const moe_norm_shape *shape, const void *x, const void *residual, const void *weight,
+                             const void *bias, void *r, void *y, float *mean, float *rstd, moe_stream_t stream) {
+  moe::AbiRange range("moe_layernorm_fwd");
+  std::string why;
+  moe_status st = validate_norm(shape, &why);
+  if (st != MOE_OK) return report(st, why);
+  const moe_norm_shape &s = *shape;
+  if (s.T == 0) return MOE_OK;
+  const bool res = residual != nullptr;
+  const PtrArg args[] = {{"x", x, true, false},           {"residual", residual, false, false},
+                         {"weight", weight, true, false}, {"bias", bias, false, false},
+                         {"r", r, res, !res},             {"y", y, true, false},
+                         {"mean", mean, true, false},     {"rstd", rstd, true, false}};
+  st = validate_ptrs(args, 8, &why);
+  if (st != MOE_OK) return report(st, why);
+  LayerNormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.w = weight;
+  a.b = bias;
+  a.r = r;
+  a.y = y;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.T = s.T;
+  a.d = s.d;
+  a.eps = s.eps;
+  a.bf16 = s.dtype == MOE_DTYPE_BF16;
+  return hip_status(launch_layernorm_fwd(a, as_stream(stream)), "layernorm_fwd");
+}
+
+moe_status moe_layernorm_bwd(const moe_norm_shape *shape, const void *dy, const void *r, const void *weight,
+                             const float *mean, const float *rstd, const void *dres, void *dx, float *dw, float *db,
+                             void *ws, size_t ws_bytes, moe_stream_t stream) {
+  moe::AbiRange range("moe_layernorm_bwd");
+  std::string why;
+  moe_status st = validate_norm(shape, &why);
+  if (st != MOE_OK) return report(st, why);
+  const moe_norm_shape &s = *shape;
+  const bool overwrite = (s.flags & MOE_NORM_OVERWRITE_DW) != 0;
+  if (s.T == 0 && !overwrite) return MOE_OK;
+  const bool some = s.T > 0;
+  const PtrArg args[] = {{"dy", dy, some, false},         {"r", r, some, false},       {"weight", weight, some, false},
+                         {"mean", mean, some, false},     {"rstd", rstd, some, false}, {"dres", dres, false, false},
+                         {"dx", dx, some, false},         {"dw", dw, true, false},     {"db", db, false, false}};
+  st = validate_ptrs(args, 9, &why);
+  if (st != MOE_OK) return report(st, why);
+  st = validate_workspace(ws, ws_bytes, layernorm_workspace(s), &why);
+  if (st != MOE_OK) return report(st, why);
+  LayerNormArgs a{};
+  a.dy = dy;
+  a.r = const_cast<void *>(r);
+  a.w = weight;
+  a.mean = const_cast<float *>(mean);
+  a.rstd = const_cast<float *>(rstd);
+  a.dres = dres;
+  a.dx = dx;
+  a.dw = dw;
+  a.db = db;
+  a.partial = static_cast<float *>(ws);
+  a.T = s.T;
+  a.d = s.d;
+  a.bf16 = s.dtype == MOE_DTYPE_BF16;
+  a.accumulate = !overwrite;
+  return hip_status(launch_layernorm_bwd(a, as_stream(stream)), "layernorm_bwd");
+}
+
+moe_status moe_linear_workspace_size(const moe_linear_shape *shape, size_t *wgrad_ws) {
+  std::string why;
+  const moe_status st = validate_linear(shape, &why);
+  if (st != MOE_OK) return report(st, why);
+  if (wgrad_ws) *wgrad_ws = linear_workspace(*shape).total;
+  return MOE_OK;
+}
+
+moe_status moe_linear_fwd(const moe_linear_shape *shape, const void *x, const void *w, const void *bias,
+                          const void *residual, void *z, void *y, moe_stream_t stream) {
+  moe::AbiRange range("moe_linear_fwd");
+  std::string why;
+  moe_status st = validate_linear(shape, &why);
+  if (st != MOE_OK) return report(st, why);
+  const moe_linear_shape &s = *shape;
+  if (s.T == 0) return MOE_OK;
+  const PtrArg args[] = {{"x", x, true, false},       {"w", w, true, false},
+                         {"bias", bias, false, false}, {"residual", residual, false, false},
+                         {"z", z, false, false},      {"y", y, true, false}};
+  st = validate_ptrs(args, 6, &why);
+  if (st != MOE_OK) return report(st, why);
+  if (z && (z == y || z == residual))
+    return report(MOE_ERR_INVALID_ARGUMENT, "moe_linear_fwd: z is written beside y and may be neither y nor residual");
+  LinearArgs a{};
+  a.x = x;
+  a.w = w;
+  a.bias = bias;
+  a.add = residual;
+  a.z = z;
+  a.y = y;
+  a.T = s.T;
+  a.K = s.K;
+  a.N = s.N;
+  a.act = s.act;
+  return hip_status(launch_linear_fwd(a, as_stream(stream)), "linear_fwd");
+}
+
+moe_status moe_linear_dact(const moe_linear_shape *shape, const void *dy, const void *z, void *dz,
+                           moe_stream_t stream) {
+  moe::AbiRange range("moe_linear_dact");
+  std::string why;
+  moe_status st = validate_linear(shape, &why);
+  if (st != MOE_OK) return report(st, why);
+  const moe_linear_shape &s = *shape;
+  if (s.act == MOE_ACT_NONE)
+    return report(MOE_ERR_INVALID_ARGUMENT, "moe_linear_dact: without an activation dz is dy");
+  if (s.T == 0) return MOE_OK;
+  const PtrArg args[] = {{"dy", dy, true, false}, {"z", z, true, false}, {"dz", dz, true, false}};
+  st = validate_ptrs(args, 3, &why);
+  if (st != MOE_OK) return report(st, why);
+  LinearArgs a{};
+  a.dy = dy;
+  a.z = const_cast<void *>(z);
+  a.dz = dz;
+  a.T = s.T;
+  a.K = s.K;
+  a.N = s.N;
+  a.act = s.act;
+  return hip_status(launch_linear_dact(a, as_stream(stream)), "linear_dact");
+}
+
+moe_status moe_linear_dgrad(const moe_linear_shape *shape, const void *dz, const void *w, const void *z_in,
+                            int32_t act_in, const void *add, void *dx, moe_stream_t stream) {
+  moe::AbiRange range("moe_linear_dgrad");
+  std::string why;
+  moe_status st = validate_linear(shape, &why);
+  if (st != MOE_OK) return report(st, why);
+  st = validate_act(act_in, &why);
+  if (st != MOE_OK) return report(st, why);
+  const moe_linear_shape &s = *shape;
+  if (s.T == 0) return MOE_OK;
+  const bool act = act_in != MOE_ACT_NONE;
+  const PtrArg args[] = {{"dz", dz, true, false},
+                         {"w", w, true, false},
+                         {"z_in", z_in, act, !act},
+                         {"add", add, false, false},
+                         {"dx", dx, true, false}};
+  st = validate_ptrs(args, 5, &why);
+  if (st != MOE_OK) return report(st, why);
+  LinearArgs a{};
+  a.dz = const_cast<void *>(dz);
+  a.w = w;
+  a.z = const_cast<void *>(z_in);
+  a.act = act_in;
+  a.add = add;
+  a.dx = dx;
+  a.T = s.T;
+  a.K = s.K;
+  a.N = s.N;
+  return hip_status(launch_linear_dgrad(a, as_stream(stream)), "linear_dgrad");
+}
+
+moe_status moe_linear_wgrad(const moe_linear_shape *shape, const void *dz, const void *x, float *dw, float *db,
+                            void *ws, size_t ws_bytes, moe_stream_t stream) {
+  moe::AbiRange range("moe_linear_wgrad");
+  std::string why;
+  moe_status st = validate_linear(shape, &why);
+  if (st != MOE_OK) return report(st, why);
+  const moe_linear_shape &s = *shape;
+  const bool overwrite = (s.flags & MOE_LINEAR_OVERWRITE_DW) != 0;
+  if (s.T == 0 && !overwrite) return MOE_OK;
+  const bool some = s.T > 0;
+  const PtrArg args[] = {
+      {"dz", dz, some, false}, {"x", x, some, false}, {"dw", dw, true, false}, {"db", db, false, false}};
+  st = validate_ptrs(args, 4, &why);
+  if (st != MOE_OK) return report(st, why);
+  const LinearWorkspace w = linear_workspace(s);
+  st = validate_workspace(ws, ws_bytes, w.total, &why);
+  if (st != MOE_OK) return report(st, why);
+  LinearArgs a{};
+  a.dz = const_cast<void *>(dz);
+  a.x = x;
+  a.dw = dw;
+  a.db = db;
+  a.partial = static_cast<float *>(ws);
+  a.db_partial = reinterpret_cast<float *>(static_cast<char *>(ws) + w.dw);
+  a.T = s.T;
+  a.K = s.K;
+  a.N = s.N;
+  a.accumulate = !overwrite;
+  const hipError_t err = launch_linear_dw(a, as_stream(stream));
+  if (err != hipSuccess || !db) return hip_status(err, "linear_wgrad");
+  return hip_status(launch_linear_db(a, as_stream(stream)), "linear_wgrad");
+}
+
+moe_status moe_orthogonalize_workspace_size(const moe_orth_shape *shape, size_t *ws) {
+  std::string why;
+  const moe_status st = validate_orth(shape, &why);
+  if (st != MOE_OK) return report(st, why);
+  if (ws) *ws = orth_workspace(shape->batch, shape->rows, shape->cols).total;
+  return MOE_OK;
+}
+
+static OrthArgs orth_args(const moe_orth_shape &s, void *ws) {
+  OrthArgs a{};
+  a.ws = ws;
+  a.batch = s.batch;
+  a.rows = s.rows;
+  a.cols = s.cols;
+  a.steps = s.steps;
+  a.coef[0] = s.a;
+  a.coef[1] = s.b;
+  a.coef[2] = s.c;
+  a.eps = s.eps;
+  a.bf16 = s.dtype == MOE_DTYPE_BF16;
+  return a;
+}
+
+moe_status moe_orthogonalize(const moe_orth_shape *shape, const void *x, void *o, void *ws, size_t ws_bytes,
+                             moe_stream_t stream) {
+  moe::AbiRange range("moe_orthogonalize");
+  std::string why;
+  moe_status st = validate_orth(shape, &why);
+  if (st != MOE_OK) return report(st, why);
+  const moe_orth_shape &s = *shape;
+  if (s.batch == 0) return MOE_OK;
+  const PtrArg args[] = {{"x", x, true, false}, {"o", o, true, false}};
+  st = validate_ptrs(args, 2, &why);
+  if (st != MOE_OK) return report(st, why);
+  st = validate_workspace(ws, ws_bytes, orth_workspace(s.batch, s.rows, s.cols).total, &why);
+  if (st != MOE_OK) return report(st, why);
+  OrthArgs a = orth_args(s, ws);
+  a.x = x;
+  a.o = o;
+  return hip_status(launch_orth(a, as_stream(stream)), "orthogonalize");
+}
+
+moe_status moe_muon_step(const moe_muon_config *cfg, const moe_orth_shape *shape, float *param, float *grad,
+                         float *momentum, void *param_bf16, void *ws, size_t ws_bytes, moe_stream_t stream) {
+  moe::AbiRange range("moe_muon_step");
+  std::string why;
+  moe_status st = validate_muon(cfg, &why);
+  if (st != MOE_OK) return report(st, why);
+  st = validate_orth(shape, &why);
+  if (st != MOE_OK) return report(st, why);
+  const moe_orth_shape &s = *shape;
+  if (s.dtype != MOE_DTYPE_F32) return report(MOE_ERR_UNSUPPORTED, "moe_muon_step: dtype must be MOE_DTYPE_F32");
+  if (s.batch == 0) return MOE_OK;
+  const PtrArg args[] = {{"param", param, true, false},
+                         {"grad", grad, true, false},
+                         {"momentum", momentum, true, false},
+                         {"param_bf16", param_bf16, false, false}};
+  st = validate_ptrs(args, 4, &why);
+  if (st != MOE_OK) return report(st, why);
+  st = validate_workspace(ws, ws_bytes, orth_workspace(s.batch, s.rows, s.cols).total, &why);
+  if (st != MOE_OK) return report(st, why);
+  OrthArgs a = orth_args(s, ws);
+  a.param = param;
+  a.grad = grad;
+  a.momentum = momentum;
+  a.param_bf16 = param_bf16;
+  a.mu = cfg->momentum;
+  a.grad_scale = cfg->grad_scale;
+  a.decay = (float)(1.0 - (double)cfg->lr * (double)cfg->weight_decay);
+  a.step_size = (float)((double)cfg->lr * (double)cfg->scale);
+  a.nesterov = (cfg->flags & MOE_MUON_NESTEROV) != 0;
+  a.zero_grad = (cfg->flags & MOE_MUON_ZERO_GRAD) != 0;
+  return hip_status(launch_orth(a, as_stream(stream)), "muon_step");
+}
+
 static int device_cus() {
   int dev = 0, n = 0;
   if (hipGetDevice(&dev) != hipSuccess) return 0;

@@ -1,0 +1,406 @@
+// Orthogonalisation of a batch of matrices by Newton-Schulz products, and the
+// optimiser step around it (Muon). orth_kernel.h has the products.
+//
+//   norm    per matrix sum(U^2) in 64 bits, as partial sums in a fixed order
+//   prep    X0 = U / (|U| + eps) to two fp16 halves, short side first, padded
+//           with zeros; the step also writes the momentum and clears the
+//           gradient here
+//   5 x     gram, poly, step
+//   finish  O, or w = w (1 - lr wd) - lr scale O and its bf16 copy
+//
+// U is the matrix given, or  buf = mu buf + g,  U = g + mu buf (Nesterov) or
+// buf; it is formed twice, in norm and in prep, from the same inputs.
+#include "kernels.h"
+#include "orth_kernel.h"
+
+namespace moe {
+
+constexpr int kOrthThreads = 256;
+
+struct OrthIo {
+  const void *x;          // orthogonalise: fp32 or bf16
+  float *grad, *mom;      // step
+  float mu, grad_scale;
+  int nesterov, zero_grad;
+  int rows, cols;         // of the matrices given
+  int parts;              // partial sums of a matrix
+  double *partial;        // [batch, parts]
+  float eps;
+  int tall;               // rows > cols: X is the transpose
+  half_t *hi, *lo;        // X [S, L] per matrix
+  int64_t ldx, stride_x;
+  void *o;                // bf16
+  float *param;
+  bf16_t *param_bf16;     // or NULL
+  float decay, step_size;
+};
+
+enum { SRC_F32 = 0, SRC_BF16 = 1, SRC_MUON = 2 };
+
+// U at 4 consecutive elements from `e` on (of the whole batch), `n` of them
+// there; vec: they are one aligned vector.
+template <int SRC>
+MOE_DEVICE void orth_u(const OrthIo &p, int64_t e, int n, bool vec, float (&u)[4], float (&buf)[4]) {
+  float g[4] = {0.f, 0.f, 0.f, 0.f};
+  if constexpr (SRC == SRC_BF16) {
+    const bf16_t *x = (const bf16_t *)p.x + e;
+    if (vec) {
+      const uint2 v = *reinterpret_cast<const uint2 *>(x);
+      g[0] = __uint_as_float(v.x << 16);
+      g[1] = __uint_as_float(v.x & 0xffff0000u);
+      g[2] = __uint_as_float(v.y << 16);
+      g[3] = __uint_as_float(v.y & 0xffff0000u);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (q < n) g[q] = bf2f(x[q]);
+    }
+  } else {
+    const float *x = SRC == SRC_F32 ? (const float *)p.x + e : p.grad + e;
+    float m[4] = {0.f, 0.f, 0.f, 0.f};
+    if (vec) {
+      const f32x4_t v = *reinterpret_cast<const f32x4_t *>(x);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) g[q] = v[q];
+      if (SRC == SRC_MUON) {
+        const f32x4_t w = *reinterpret_cast<const f32x4_t *>(p.mom + e);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) m[q] = w[q];
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (q < n) {
+          g[q] = x[q];
+          if (SRC == SRC_MUON) m[q] = p.mom[e + q];
+        }
+    }
+    if (SRC == SRC_MUON) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float gs = g[q] * p.grad_scale;
+        buf[q] = fmaf(p.mu, m[q], gs);
+        g[q] = p.nesterov ? fmaf(p.mu, buf[q], gs) : buf[q];
+      }
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) u[q] = g[q];
+}
+
+MOE_DEVICE double wave_sum64(double v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
+  return v;
+}
+
+// Squares are summed in 64 bits: no gradient is too small or too large for it.
+template <int SRC>
+__global__ __launch_bounds__(kOrthThreads) void orth_norm_kernel(OrthIo p) {
+  __shared__ double part[kOrthThreads / kWave];
+  const int64_t n = (int64_t)p.rows * p.cols;
+  const int64_t mat = blockIdx.x / p.parts;
+  const int part_id = (int)(blockIdx.x - mat * p.parts);
+  const int64_t chunk = ((n + p.parts - 1) / p.parts + 3) & ~(int64_t)3;
+  const int64_t first = part_id * chunk, last = first + chunk < n ? first + chunk : n;
+  const bool aligned = (n & 3) == 0;  // every matrix starts on a vector
+  double sum = 0.0;
+#pragma unroll 4
+  for (int64_t i = first + threadIdx.x * 4; i < last; i += kOrthThreads * 4) {
+    float u[4], b[4];
+    const int left = (int)(last - i < 4 ? last - i : 4);
+    orth_u<SRC>(p, mat * n + i, left, aligned && left == 4, u, b);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sum = fma((double)u[q], (double)u[q], sum);
+  }
+  sum = wave_sum64(sum);
+  if ((threadIdx.x & (kWave - 1)) == 0) part[threadIdx.x / kWave] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) p.partial[blockIdx.x] = (part[0] + part[1]) + (part[2] + part[3]);
+}
+
+// A 64 x 64 tile of a matrix given; rows and columns past its end are zeros
+// (the padding of X).
+template <int SRC>
+__global__ __launch_bounds__(kOrthThreads) void orth_prep_kernel(OrthIo p) {
+  __shared__ float tile[64][65];
+  const int rt = (p.rows + 63) / 64, ct = (p.cols + 63) / 64;
+  const int64_t mat = blockIdx.x / ((int64_t)rt * ct);
+  const int t = (int)(blockIdx.x - mat * rt * ct);
+  const int r0 = t / ct * 64, c0 = t % ct * 64;
+  const int lane = threadIdx.x & (kWave - 1);
+  double sum = 0.0;
+  for (int i = lane; i < p.parts; i += kWave) sum += p.partial[mat * p.parts + i];
+  sum = wave_sum64(sum);
+  // a matrix that holds an infinity or a NaN becomes NaN altogether
+  const double scale = sum < __builtin_huge_val() ? (double)kOrthScale / (sqrt(sum) + (double)p.eps) : __builtin_nan("");
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int64_t base = mat * p.rows * p.cols;
+  auto put = [&](int64_t o, const float (&v)[4]) {
+    float l[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) l[q] = v[q] - h2f(f2h(v[q]));
+    *reinterpret_cast<uint2 *>(p.hi + mat * p.stride_x + o) = make_uint2(pack_h2(v[0], v[1]), pack_h2(v[2], v[3]));
+    *reinterpret_cast<uint2 *>(p.lo + mat * p.stride_x + o) = make_uint2(pack_h2(l[0], l[1]), pack_h2(l[2], l[3]));
+  };
+  const bool vec = (p.cols & 3) == 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int r = r0 + ty + 16 * k, c = c0 + tx * 4;
+    const int left = r < p.rows ? min(4, p.cols - c) : 0;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (left > 0) {
+      const int64_t e = base + (int64_t)r * p.cols + c;
+      float u[4], buf[4];
+      orth_u<SRC>(p, e, left, vec, u, buf);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (q < left) v[q] = (float)((double)u[q] * scale);
+      if constexpr (SRC == SRC_MUON) {
+        if (vec) {
+          *reinterpret_cast<f32x4_t *>(p.mom + e) = f32x4_t{buf[0], buf[1], buf[2], buf[3]};
+          if (p.zero_grad) *reinterpret_cast<f32x4_t *>(p.grad + e) = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (q < left) {
+              p.mom[e + q] = buf[q];
+              if (p.zero_grad) p.grad[e + q] = 0.f;
+            }
+        }
+      }
+    }
+    if (!p.tall) {
+      put((int64_t)r * p.ldx + c, v);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tile[ty + 16 * k][tx * 4 + q] = v[q];
+    }
+  }
+  if (!p.tall) return;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = tile[tx * 4 + q][ty + 16 * k];
+    put((int64_t)(c0 + ty + 16 * k) * p.ldx + r0 + tx * 4, v);
+  }
+}
+
+// A 64 x 64 tile of X back into the matrices given.
+template <bool MUON>
+__global__ __launch_bounds__(kOrthThreads) void orth_finish_kernel(OrthIo p) {
+  __shared__ float tile[64][65];
+  const int rt = (p.rows + 63) / 64, ct = (p.cols + 63) / 64;
+  const int64_t mat = blockIdx.x / ((int64_t)rt * ct);
+  const int t = (int)(blockIdx.x - mat * rt * ct);
+  const int r0 = t / ct * 64, c0 = t % ct * 64;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int64_t base = mat * p.rows * p.cols;
+  auto get = [&](int64_t o, float (&v)[4]) {
+    const uint2 h = *reinterpret_cast<const uint2 *>(p.hi + mat * p.stride_x + o);
+    const uint2 l = *reinterpret_cast<const uint2 *>(p.lo + mat * p.stride_x + o);
+    float a[4], b[4];
+    unpack_h2(h.x, a[0], a[1]);
+    unpack_h2(h.y, a[2], a[3]);
+    unpack_h2(l.x, b[0], b[1]);
+    unpack_h2(l.y, b[2], b[3]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = (a[q] + b[q]) * kOrthUnscale;
+  };
+  if (p.tall) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float v[4];
+      get((int64_t)(c0 + ty + 16 * k) * p.ldx + r0 + tx * 4, v);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tile[ty + 16 * k][tx * 4 + q] = v[q];
+    }
+    __syncthreads();
+  }
+  const bool vec = (p.cols & 3) == 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int r = r0 + ty + 16 * k, c = c0 + tx * 4;
+    const int left = r < p.rows ? min(4, p.cols - c) : 0;
+    if (left <= 0) continue;
+    float v[4];
+    if (p.tall) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = tile[tx * 4 + q][ty + 16 * k];
+    } else {
+      get((int64_t)r * p.ldx + c, v);
+    }
+    const int64_t e = base + (int64_t)r * p.cols + c;
+    bf16_t *lowp = MUON ? p.param_bf16 : (bf16_t *)p.o;
+    if constexpr (MUON) {
+      if (vec) {
+        f32x4_t w = *reinterpret_cast<const f32x4_t *>(p.param + e);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w[q] = v[q] = fmaf(-p.step_size, v[q], w[q] * p.decay);
+        *reinterpret_cast<f32x4_t *>(p.param + e) = w;
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (q < left) p.param[e + q] = v[q] = fmaf(-p.step_size, v[q], p.param[e + q] * p.decay);
+      }
+      if (!lowp) continue;
+    }
+    if (vec) {
+      *reinterpret_cast<uint2 *>(lowp + e) = make_uint2(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]));
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (q < left) lowp[e + q] = f2bf(v[q]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+//   small   64 x 64 (step: 64 x 128) tiles, 4 (2) k groups a workgroup
+//   pair    128 x 128 tiles, 2 k groups
+//   square  128 x 128 tiles, two workgroups a CU
+//   large   256 x 256 tiles
+enum OrthTile { kSmall, kPair, kSquare, kLarge };
+
+static OrthTile choose(int M, int N, int64_t batch, bool sym) {
+  const int64_t cus = persistent_grid();
+  const auto tiles = [&](int bm, int bn) {
+    const int64_t m = ceil_div(M, bm), n = ceil_div(N, bn);
+    return batch * (sym ? m * (m + 1) / 2 : m * n);
+  };
+  if (tiles(64, sym ? 64 : 128) <= cus) return kSmall;
+  if (tiles(128, 128) <= cus) return kPair;
+  return 145 * ceil_div(tiles(256, 256), cus) < 100 * ceil_div(tiles(128, 128), 2 * cus) ? kLarge : kSquare;
+}
+
+static hipError_t sym_product(const OrthTileParams &p, int64_t batch, bool gram, hipStream_t s) {
+  LaunchScope scope(gram ? "orth_gram" : "orth_poly", s);
+  const OrthTile t = choose(p.M, p.N, batch, true);
+  if (gram) {
+    switch (t) {
+      case kSmall: return run_orth_tile<64, 64, 32, 64, 4, 2, ORTH_GRAM>(p, batch, s);
+      case kPair: return run_orth_tile<128, 128, 64, 64, 2, 2, ORTH_GRAM>(p, batch, s);
+      case kSquare: return run_orth_tile<128, 128, 64, 64, 1, 2, ORTH_GRAM>(p, batch, s);
+      default: return run_orth_tile<256, 256, 128, 64, 1, 2, ORTH_GRAM>(p, batch, s);
+    }
+  }
+  switch (t) {
+    case kSmall: return run_orth_tile<64, 64, 32, 64, 4, 2, ORTH_POLY>(p, batch, s);
+    case kPair: return run_orth_tile<128, 128, 64, 64, 2, 2, ORTH_POLY>(p, batch, s);
+    case kSquare: return run_orth_tile<128, 128, 64, 64, 1, 2, ORTH_POLY>(p, batch, s);
+    default: return run_orth_tile<256, 256, 128, 64, 1, 2, ORTH_POLY>(p, batch, s);
+  }
+}
+
+static hipError_t step_product(const OrthTileParams &p, int64_t batch, hipStream_t s) {
+  LaunchScope scope("orth_step", s);
+  switch (choose(p.M, p.N, batch, false)) {
+    case kSmall: return run_orth_tile<64, 128, 32, 64, 2, 2, ORTH_STEP>(p, batch, s);
+    case kPair: return run_orth_tile<128, 128, 64, 64, 2, 2, ORTH_STEP>(p, batch, s);
+    case kSquare: return run_orth_tile<128, 128, 64, 64, 1, 2, ORTH_STEP>(p, batch, s);
+    default: return run_orth_tile<256, 256, 128, 64, 1, 2, ORTH_STEP>(p, batch, s);
+  }
+}
+
+template <int SRC>
+static hipError_t enter(const OrthIo &io, int64_t batch, hipStream_t s) {
+  {
+    LaunchScope scope("orth_norm", s);
+    orth_norm_kernel<SRC><<<(unsigned)(batch * io.parts), kOrthThreads, 0, s>>>(io);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  LaunchScope scope("orth_prep", s);
+  const int64_t blocks = batch * ceil_div(io.rows, 64) * ceil_div(io.cols, 64);
+  orth_prep_kernel<SRC><<<(unsigned)blocks, kOrthThreads, 0, s>>>(io);
+  return hipGetLastError();
+}
+
+hipError_t launch_orth(const OrthArgs &a, hipStream_t s) {
+  const OrthWorkspace w = orth_workspace(a.batch, a.rows, a.cols);
+  char *ws = static_cast<char *>(a.ws);
+  half_t *hi[2] = {(half_t *)(ws + w.hi[0]), (half_t *)(ws + w.hi[1])};
+  half_t *lo[2] = {(half_t *)(ws + w.lo[0]), (half_t *)(ws + w.lo[1])};
+  half_t *A = (half_t *)(ws + w.a), *B = (half_t *)(ws + w.b);
+  float *da = (float *)(ws + w.da), *db = (float *)(ws + w.db);
+  OrthIo io{};
+  io.x = a.x;
+  io.grad = a.grad;
+  io.mom = a.momentum;
+  io.mu = a.mu;
+  io.grad_scale = a.grad_scale;
+  io.nesterov = a.nesterov ? 1 : 0;
+  io.zero_grad = a.zero_grad ? 1 : 0;
+  io.rows = a.rows;
+  io.cols = a.cols;
+  io.parts = w.parts;
+  io.partial = (double *)(ws + w.partial);
+  io.eps = a.eps;
+  io.tall = a.rows > a.cols ? 1 : 0;
+  io.hi = hi[0];
+  io.lo = lo[0];
+  io.ldx = w.L;
+  io.stride_x = (int64_t)w.S * w.L;
+  io.o = a.o;
+  io.param = a.param;
+  io.param_bf16 = (bf16_t *)a.param_bf16;
+  io.decay = a.decay;
+  io.step_size = a.step_size;
+  const bool muon = a.param != nullptr;
+  hipError_t err = muon      ? enter<SRC_MUON>(io, a.batch, s)
+                   : a.bf16 ? enter<SRC_BF16>(io, a.batch, s)
+                            : enter<SRC_F32>(io, a.batch, s);
+  int cur = 0;
+  for (int k = 0; k < a.steps && err == hipSuccess; ++k) {
+    OrthTileParams p{};
+    p.ca = a.coef[0];
+    p.cb = a.coef[1];
+    p.cc = a.coef[2];
+    p.S = w.S;
+    p.A = p.B = hi[cur];
+    p.C = A;
+    p.diag_out = da;
+    p.M = p.N = w.S;
+    p.K = w.L;
+    p.lda = p.ldb = w.L;
+    p.ldc = w.S;
+    p.strideA = p.strideB = io.stride_x;
+    p.strideC = (int64_t)w.S * w.S;
+    err = sym_product(p, a.batch, true, s);
+    if (err != hipSuccess) break;
+    p.A = p.B = A;
+    p.C = B;
+    p.diag = da;
+    p.diag_out = db;
+    p.K = w.S;
+    p.lda = p.ldb = w.S;
+    p.strideA = p.strideB = p.strideC;
+    err = sym_product(p, a.batch, false, s);
+    if (err != hipSuccess) break;
+    p.A = B;
+    p.B = hi[cur];
+    p.Xlo = lo[cur];
+    p.C = hi[cur ^ 1];
+    p.Clo = lo[cur ^ 1];
+    p.diag = db;
+    p.N = w.L;
+    p.ldb = p.ldc = w.L;
+    p.strideB = p.strideC = io.stride_x;
+    err = step_product(p, a.batch, s);
+    cur ^= 1;
+  }
+  if (err != hipSuccess) return err;
+  io.hi = hi[cur];
+  io.lo = lo[cur];
+  LaunchScope scope("orth_finish", s);
+  const int64_t blocks = a.batch * ceil_div(io.rows, 64) * ceil_div(io.cols, 64);
+  if (muon) orth_finish_kernel<true><<<(unsigned)blocks, kOrthThreads, 0, s>>>(io);
+  else orth_finish_kernel<false><<<(unsigned)blocks, kOrthThreads, 0, s>>>(io);
+  return hipGetLastError();
+}
+
+}  // namespace moe

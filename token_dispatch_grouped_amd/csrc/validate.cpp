@@ -5,6 +5,7 @@
 // is consumed (review note on Add MoE expert parallel training runtime).
 #include "validate.h"
 
+#include <algorithm>
 #include <cmath>
 
 #include <stdio.h>
@@ -224,7 +225,9 @@ static int64_t wgrad_tiles(int tile, int d, int F) {
   return ceil_div(2 * (int64_t)F, tile) * ceil_div(d, tile) + ceil_div(d, tile) * ceil_div(F, tile);
 }
 
-FfnWgrad ffn_wgrad_plan(int64_t T, int d, int F) {
+// `tiles(tile)`: tiles of all products; elems: their elements.
+template <typename Tiles>
+static FfnWgrad wgrad_plan(int64_t T, double elems, Tiles count) {
   // Time of n slices in us: a fixed 4, then rounds of workgroups, each a run of
   // stages of 64 tokens. 256 x 256 tiles run one a CU, 1.35 us a stage while
   // every workgroup has a CU from the start, 1.6 beyond; 128 x 128 tiles two a
@@ -234,12 +237,12 @@ FfnWgrad ffn_wgrad_plan(int64_t T, int d, int F) {
   // 256, 3: 75, 128, 1: 59; at 7001 256, 1: 145, 256, 3: 149, 128, 2: 166; at
   // 32768 256, 1: 694, 256, 3: 589; d = 512, F = 320 at 3000 256, 11: 27, 128,
   // 1: 33, 128, 4: 18.5; d = 1088, F = 576 at 700 256, 1: 23, 128, 1: 12.
-  const double bytes = 12.0 * d * F, least = 6.0 * (double)T * d * F / 1.06e9;
+  const double bytes = 4.0 * elems, least = 2.0 * (double)T * elems / 1.06e9;
   FfnWgrad w{256, 0, 0, 1};
   double best_us = 0.0;
   int64_t best = 1;
   for (int tile = 256; tile >= 128; tile /= 2) {
-    const int64_t tiles = wgrad_tiles(tile, d, F);
+    const int64_t tiles = count(tile);
     int64_t most = kWgradUnits / tiles;
     if (most > T / kWgradMinRows) most = T / kWgradMinRows;
     if (most < 1) most = 1;
@@ -262,6 +265,10 @@ FfnWgrad ffn_wgrad_plan(int64_t T, int d, int F) {
   return w;
 }
 
+FfnWgrad ffn_wgrad_plan(int64_t T, int d, int F) {
+  return wgrad_plan(T, 3.0 * d * F, [&](int tile) { return wgrad_tiles(tile, d, F); });
+}
+
 FfnWorkspace ffn_workspace(const moe_ffn_shape &s) {
   FfnWorkspace w{};
   const bool mx8 = s.dtype == MOE_DTYPE_MX8;
@@ -274,6 +281,142 @@ FfnWorkspace ffn_workspace(const moe_ffn_shape &s) {
   // gradients of so many tiles that no T is sliced are written to directly
   if (!mx8 && s.T > 0 && wgrad_tiles(256, s.d, s.F) * 2 <= kWgradUnits)
     w.wgrad_total = align256((size_t)ffn_wgrad_plan(s.T, s.d, s.F).most * 3 * (size_t)s.d * (size_t)s.F * 4);
+  return w;
+}
+
+// ----- layer norm, dense product, orthogonalisation -----
+size_t layernorm_workspace(const moe_norm_shape &s) {
+  return align256((size_t)norm_bwd_blocks(s.T) * 2 * (size_t)s.d * 4);
+}
+
+moe_status validate_act(int32_t act, std::string *why) {
+  if (act < MOE_ACT_NONE || act > MOE_ACT_SILU) return fail(why, MOE_ERR_UNSUPPORTED, "unknown activation");
+  return MOE_OK;
+}
+
+moe_status validate_linear(const moe_linear_shape *s, std::string *why) {
+  if (!s) return fail(why, MOE_ERR_INVALID_ARGUMENT, "linear shape is NULL");
+  if (s->T < 0) return fail(why, MOE_ERR_INVALID_ARGUMENT, "T < 0");
+  if (s->K <= 0 || s->N <= 0) return fail(why, MOE_ERR_INVALID_ARGUMENT, "K and N must be positive");
+  if (s->K % 64 != 0 || s->K > 65536 || s->N % 64 != 0 || s->N > 65536)
+    return fail(why, MOE_ERR_UNSUPPORTED, "K and N must be multiples of 64, at most 65536");
+  if (s->T >= ((int64_t)1 << 24)) return fail(why, MOE_ERR_UNSUPPORTED, "T >= 2^24");
+  if (s->dtype != MOE_DTYPE_BF16) return fail(why, MOE_ERR_UNSUPPORTED, "dtype must be MOE_DTYPE_BF16");
+  const moe_status st = validate_act(s->act, why);
+  if (st != MOE_OK) return st;
+  if (s->flags & ~(uint32_t)MOE_LINEAR_OVERWRITE_DW) return fail(why, MOE_ERR_UNSUPPORTED, "unknown linear flag bits");
+  // the largest grid: 128 x 128 tiles of [T, N] or [T, K], row tiles in whole
+  // groups, 256 threads each; the elementwise pass has a thread for 8 values
+  const int64_t wide = s->K > s->N ? s->K : s->N;
+  const int64_t tiles = ceil_div(ceil_div(s->T, 128), kGemmGroupM) * kGemmGroupM * ceil_div(wide, 128);
+  if ((tiles + 8) * 256 >= ((int64_t)1 << 32) || s->T * (wide / 8) >= ((int64_t)1 << 32) - 256)
+    return fail(why, MOE_ERR_UNSUPPORTED, "problem too large for one launch (2^32 threads per grid dimension)");
+  return MOE_OK;
+}
+
+static int64_t linear_tiles(int tile, int K, int N) { return ceil_div(N, tile) * ceil_div(K, tile); }
+
+FfnWgrad linear_wgrad_plan(int64_t T, int K, int N) {
+  return wgrad_plan(T, (double)K * N, [&](int tile) { return linear_tiles(tile, K, N); });
+}
+
+LinearWorkspace linear_workspace(const moe_linear_shape &s) {
+  LinearWorkspace w{};
+  if (s.T > 0 && linear_tiles(256, s.K, s.N) * 2 <= kWgradUnits)
+    w.dw = align256((size_t)linear_wgrad_plan(s.T, s.K, s.N).most * (size_t)s.K * (size_t)s.N * 4);
+  w.db = align256((size_t)linear_db_slices(s.T) * (size_t)s.N * 4);
+  w.total = w.dw + w.db;
+  return w;
+}
+
+// Largest |p| of p(x) = a x + b x^3 + c x^5 on [0, m].
+static double quintic_peak(double a, double b, double c, double m) {
+  const auto p = [&](double x) { return std::fabs(x * (a + x * x * (b + x * x * c))); };
+  double top = p(m);
+  const auto at = [&](double s) {  // s = x^2 where p' may vanish
+    if (s > 0.0 && s < m * m) top = std::max(top, p(std::sqrt(s)));
+  };
+  if (c == 0.0) {
+    if (b != 0.0) at(-a / (3.0 * b));
+  } else {
+    const double disc = 9.0 * b * b - 20.0 * a * c;
+    if (disc >= 0.0) {
+      at((-3.0 * b + std::sqrt(disc)) / (10.0 * c));
+      at((-3.0 * b - std::sqrt(disc)) / (10.0 * c));
+    }
+  }
+  return top;
+}
+
+moe_status validate_orth(const moe_orth_shape *s, std::string *why) {
+  if (!s) return fail(why, MOE_ERR_INVALID_ARGUMENT, "orth shape is NULL");
+  if (s->batch < 0) return fail(why, MOE_ERR_INVALID_ARGUMENT, "batch < 0");
+  if (s->rows <= 0 || s->cols <= 0) return fail(why, MOE_ERR_INVALID_ARGUMENT, "rows and cols must be positive");
+  if (s->rows > 65536 || s->cols > 65536) return fail(why, MOE_ERR_UNSUPPORTED, "rows and cols must be at most 65536");
+  if (s->dtype != MOE_DTYPE_F32 && s->dtype != MOE_DTYPE_BF16)
+    return fail(why, MOE_ERR_UNSUPPORTED, "dtype must be MOE_DTYPE_F32 or MOE_DTYPE_BF16");
+  if (s->steps < 1 || s->steps > 16) return fail(why, MOE_ERR_UNSUPPORTED, "steps must be between 1 and 16");
+  if (!std::isfinite(s->eps) || s->eps <= 0.f) return fail(why, MOE_ERR_INVALID_ARGUMENT, "eps must be positive and finite");
+  const double a = s->a, b = s->b, c = s->c;
+  if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c))
+    return fail(why, MOE_ERR_INVALID_ARGUMENT, "non-finite coefficient");
+  // Singular values start at most 1; X, X X^T and b X X^T + c (X X^T)^2 are held
+  // in fp16 times 2^12, whose largest number is below 16 times that.
+  double m = 1.0;
+  for (int k = 0; k < s->steps; ++k) {
+    const double l = m * m;
+    double poly = std::fabs(b * l + c * l * l);
+    if (c != 0.0 && -b / (2.0 * c) > 0.0 && -b / (2.0 * c) < l) poly = std::max(poly, b * b / (4.0 * std::fabs(c)));
+    if (l > 15.0 || poly > 15.0)
+      return fail(why, MOE_ERR_UNSUPPORTED, "the coefficients let singular values grow past fp16's range");
+    m = quintic_peak(a, b, c, m);
+  }
+  if (m > 15.0) return fail(why, MOE_ERR_UNSUPPORTED, "the coefficients let singular values grow past fp16's range");
+  // the largest grids: 64 x 64 tiles of all matrices, 512 threads each, twice
+  // that per tile of the smallest product shapes
+  const int64_t tiles = ceil_div(s->rows, 64) * ceil_div(s->cols, 64);
+  if (s->batch >= ((int64_t)1 << 22) || s->batch * tiles >= ((int64_t)1 << 22))
+    return fail(why, MOE_ERR_UNSUPPORTED, "problem too large for one launch (2^32 threads per grid dimension)");
+  return MOE_OK;
+}
+
+moe_status validate_muon(const moe_muon_config *c, std::string *why) {
+  if (!c) return fail(why, MOE_ERR_INVALID_ARGUMENT, "muon config is NULL");
+  if (c->flags & ~(uint32_t)(MOE_MUON_NESTEROV | MOE_MUON_ZERO_GRAD))
+    return fail(why, MOE_ERR_UNSUPPORTED, "unknown muon flag bits");
+  if (!std::isfinite(c->lr) || !std::isfinite(c->weight_decay) || !std::isfinite(c->scale) ||
+      !std::isfinite(c->grad_scale) || !std::isfinite(c->momentum))
+    return fail(why, MOE_ERR_INVALID_ARGUMENT, "non-finite muon scalar");
+  if (c->momentum < 0.f || c->momentum >= 1.f)
+    return fail(why, MOE_ERR_INVALID_ARGUMENT, "momentum must lie in [0, 1)");
+  return MOE_OK;
+}
+
+OrthWorkspace orth_workspace(int64_t batch, int rows, int cols) {
+  OrthWorkspace w{};
+  const int small = rows < cols ? rows : cols, large = rows < cols ? cols : rows;
+  w.S = (small + 63) / 64 * 64;
+  w.L = (large + 63) / 64 * 64;
+  // partial sums of 16384 elements or more, 256 of a matrix at most
+  const int64_t parts = ceil_div((int64_t)rows * cols, 16384);
+  w.parts = (int)(parts < 256 ? parts : 256);
+  size_t at = 0;
+  const auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += align256(bytes);
+    return o;
+  };
+  const size_t n = (size_t)batch;
+  w.partial = take(n * (size_t)w.parts * 8);
+  for (int i = 0; i < 2; ++i) {
+    w.hi[i] = take(n * (size_t)w.S * (size_t)w.L * 2);
+    w.lo[i] = take(n * (size_t)w.S * (size_t)w.L * 2);
+  }
+  w.a = take(n * (size_t)w.S * (size_t)w.S * 2);
+  w.b = take(n * (size_t)w.S * (size_t)w.S * 2);
+  w.da = take(n * (size_t)w.S * 4);
+  w.db = take(n * (size_t)w.S * 4);
+  w.total = at;
   return w;
 }
 

@@ -118,6 +118,36 @@ struct FfnWorkspace {
 };
 FfnWorkspace ffn_workspace(const moe_ffn_shape &s);
 
+// ----- layer norm, dense product, orthogonalisation -----
+size_t layernorm_workspace(const moe_norm_shape &s);
+
+// Shape of a dense product's call, its weight gradient's tile and slices (as
+// ffn_wgrad_plan, for dW [N,K] alone) and its workspace.
+moe_status validate_linear(const moe_linear_shape *s, std::string *why);
+moe_status validate_act(int32_t act, std::string *why);
+FfnWgrad linear_wgrad_plan(int64_t T, int K, int N);
+constexpr int kLinearDbSlices = 64;   // token slices of the bias gradient at most
+constexpr int kLinearDbRows = 256;    // tokens of such a slice at least
+inline int linear_db_slices(int64_t T) {
+  const int64_t n = ceil_div(T, kLinearDbRows);
+  return (int)(n < kLinearDbSlices ? n : kLinearDbSlices);
+}
+struct LinearWorkspace {
+  size_t dw, db, total;  // fp32 partial sums of dW, then of db
+};
+LinearWorkspace linear_workspace(const moe_linear_shape &s);
+
+// Shape of an orthogonalisation (its coefficients among it: every singular
+// value of every iterate stays in fp16's range) and its workspace.
+moe_status validate_orth(const moe_orth_shape *s, std::string *why);
+moe_status validate_muon(const moe_muon_config *cfg, std::string *why);
+struct OrthWorkspace {
+  int S, L;                              // padded short and long side
+  int parts;                             // partial sums of a matrix
+  size_t partial, hi[2], lo[2], a, b, da, db, total;  // byte offsets
+};
+OrthWorkspace orth_workspace(int64_t batch, int rows, int cols);
+
 // Workspace check: NULL or short -> MOE_ERR_WORKSPACE (a zero requirement
 // accepts anything).
 moe_status validate_workspace(const void *ws, size_t have, size_t need, std::string *why);
