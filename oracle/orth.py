@@ -9,9 +9,9 @@ TEST INFRASTRUCTURE ONLY (see the package docstring).
 
 (Jordan et al., "Muon: an optimizer for hidden layers in neural networks", with
 its coefficients.) ``orthogonalize_halves`` is the same iteration with its
-tensors held as the kernels hold them, fp16 times 2^12 with X in two halves and
-the diagonals of A and b A + c A A apart, and sums without rounding: what that
-choice of types alone costs on a given matrix.
+tensors held as the kernels hold them, fp16 times 2^12 with X in two halves (in
+the last step the high one) and the diagonals of A and b A + c A A apart, and
+sums without rounding: what that choice of types alone costs on a given matrix.
 """
 from __future__ import annotations
 
@@ -48,9 +48,9 @@ def orthogonalize_halves(u, steps=5, coef=ORTH_COEF, eps=1e-7):
     if x.shape[0] > x.shape[1]:
         return orthogonalize_halves(x.T, steps, coef, eps).T
     x = x / (np.sqrt(np.sum(x * x)) + eps)
-    for _ in range(steps):
+    for k in range(steps):
         hi = _half(x)
-        lo = _half(x - hi)
+        lo = _half(x - hi) if k + 1 < steps else 0.0
         A = hi @ hi.T
         d = np.diag(A).copy()
         np.fill_diagonal(A, 0.0)

@@ -5,8 +5,8 @@
 //   prep    X0 = U / (|U| + eps) to two fp16 halves, short side first, padded
 //           with zeros; the step also writes the momentum and clears the
 //           gradient here
-//   5 x     gram, poly, step
-//   finish  O, or w = w (1 - lr wd) - lr scale O and its bf16 copy
+//   5 x     gram, poly, step; the last step's epilogue writes O, or w = w (1 -
+//           lr wd) - lr scale O and its bf16 copy
 //
 // U is the matrix given, or  buf = mu buf + g,  U = g + mu buf (Nesterov) or
 // buf; it is formed twice, in norm and in prep, from the same inputs.
@@ -27,12 +27,8 @@ struct OrthIo {
   double *partial;        // [batch, parts]
   float eps;
   int tall;               // rows > cols: X is the transpose
-  half_t *hi, *lo;        // X [S, L] per matrix
+  half_t *hi, *lo;        // X [S, L] per matrix; lo may be NULL
   int64_t ldx, stride_x;
-  void *o;                // bf16
-  float *param;
-  bf16_t *param_bf16;     // or NULL
-  float decay, step_size;
 };
 
 enum { SRC_F32 = 0, SRC_BF16 = 1, SRC_MUON = 2 };
@@ -137,10 +133,11 @@ __global__ __launch_bounds__(kOrthThreads) void orth_prep_kernel(OrthIo p) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int64_t base = mat * p.rows * p.cols;
   auto put = [&](int64_t o, const float (&v)[4]) {
+    *reinterpret_cast<uint2 *>(p.hi + mat * p.stride_x + o) = make_uint2(pack_h2(v[0], v[1]), pack_h2(v[2], v[3]));
+    if (!p.lo) return;
     float l[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) l[q] = v[q] - h2f(f2h(v[q]));
-    *reinterpret_cast<uint2 *>(p.hi + mat * p.stride_x + o) = make_uint2(pack_h2(v[0], v[1]), pack_h2(v[2], v[3]));
     *reinterpret_cast<uint2 *>(p.lo + mat * p.stride_x + o) = make_uint2(pack_h2(l[0], l[1]), pack_h2(l[2], l[3]));
   };
   const bool vec = (p.cols & 3) == 0;
@@ -188,75 +185,6 @@ __global__ __launch_bounds__(kOrthThreads) void orth_prep_kernel(OrthIo p) {
   }
 }
 
-// A 64 x 64 tile of X back into the matrices given.
-template <bool MUON>
-__global__ __launch_bounds__(kOrthThreads) void orth_finish_kernel(OrthIo p) {
-  __shared__ float tile[64][65];
-  const int rt = (p.rows + 63) / 64, ct = (p.cols + 63) / 64;
-  const int64_t mat = blockIdx.x / ((int64_t)rt * ct);
-  const int t = (int)(blockIdx.x - mat * rt * ct);
-  const int r0 = t / ct * 64, c0 = t % ct * 64;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int64_t base = mat * p.rows * p.cols;
-  auto get = [&](int64_t o, float (&v)[4]) {
-    const uint2 h = *reinterpret_cast<const uint2 *>(p.hi + mat * p.stride_x + o);
-    const uint2 l = *reinterpret_cast<const uint2 *>(p.lo + mat * p.stride_x + o);
-    float a[4], b[4];
-    unpack_h2(h.x, a[0], a[1]);
-    unpack_h2(h.y, a[2], a[3]);
-    unpack_h2(l.x, b[0], b[1]);
-    unpack_h2(l.y, b[2], b[3]);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = (a[q] + b[q]) * kOrthUnscale;
-  };
-  if (p.tall) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float v[4];
-      get((int64_t)(c0 + ty + 16 * k) * p.ldx + r0 + tx * 4, v);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) tile[ty + 16 * k][tx * 4 + q] = v[q];
-    }
-    __syncthreads();
-  }
-  const bool vec = (p.cols & 3) == 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int r = r0 + ty + 16 * k, c = c0 + tx * 4;
-    const int left = r < p.rows ? min(4, p.cols - c) : 0;
-    if (left <= 0) continue;
-    float v[4];
-    if (p.tall) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] = tile[tx * 4 + q][ty + 16 * k];
-    } else {
-      get((int64_t)r * p.ldx + c, v);
-    }
-    const int64_t e = base + (int64_t)r * p.cols + c;
-    bf16_t *lowp = MUON ? p.param_bf16 : (bf16_t *)p.o;
-    if constexpr (MUON) {
-      if (vec) {
-        f32x4_t w = *reinterpret_cast<const f32x4_t *>(p.param + e);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) w[q] = v[q] = fmaf(-p.step_size, v[q], w[q] * p.decay);
-        *reinterpret_cast<f32x4_t *>(p.param + e) = w;
-      } else {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (q < left) p.param[e + q] = v[q] = fmaf(-p.step_size, v[q], p.param[e + q] * p.decay);
-      }
-      if (!lowp) continue;
-    }
-    if (vec) {
-      *reinterpret_cast<uint2 *>(lowp + e) = make_uint2(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]));
-    } else {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (q < left) lowp[e + q] = f2bf(v[q]);
-    }
-  }
-}
-
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
@@ -285,25 +213,31 @@ static hipError_t sym_product(const OrthTileParams &p, int64_t batch, bool gram,
       case kSmall: return run_orth_tile<64, 64, 32, 64, 4, 2, ORTH_GRAM>(p, batch, s);
       case kPair: return run_orth_tile<128, 128, 64, 64, 2, 2, ORTH_GRAM>(p, batch, s);
       case kSquare: return run_orth_tile<128, 128, 64, 64, 1, 2, ORTH_GRAM>(p, batch, s);
-      default: return run_orth_tile<256, 256, 128, 64, 1, 2, ORTH_GRAM>(p, batch, s);
+      default: return run_orth_wide<ORTH_GRAM>(p, batch, s);
     }
   }
   switch (t) {
     case kSmall: return run_orth_tile<64, 64, 32, 64, 4, 2, ORTH_POLY>(p, batch, s);
     case kPair: return run_orth_tile<128, 128, 64, 64, 2, 2, ORTH_POLY>(p, batch, s);
     case kSquare: return run_orth_tile<128, 128, 64, 64, 1, 2, ORTH_POLY>(p, batch, s);
-    default: return run_orth_tile<256, 256, 128, 64, 1, 2, ORTH_POLY>(p, batch, s);
+    default: return run_orth_wide<ORTH_POLY>(p, batch, s);
   }
 }
 
-static hipError_t step_product(const OrthTileParams &p, int64_t batch, hipStream_t s) {
-  LaunchScope scope("orth_step", s);
+template <int MODE>
+static hipError_t step_tiles(const OrthTileParams &p, int64_t batch, hipStream_t s) {
   switch (choose(p.M, p.N, batch, false)) {
-    case kSmall: return run_orth_tile<64, 128, 32, 64, 2, 2, ORTH_STEP>(p, batch, s);
-    case kPair: return run_orth_tile<128, 128, 64, 64, 2, 2, ORTH_STEP>(p, batch, s);
-    case kSquare: return run_orth_tile<128, 128, 64, 64, 1, 2, ORTH_STEP>(p, batch, s);
-    default: return run_orth_tile<256, 256, 128, 64, 1, 2, ORTH_STEP>(p, batch, s);
+    case kSmall: return run_orth_tile<64, 128, 32, 64, 2, 2, MODE>(p, batch, s);
+    case kPair: return run_orth_tile<128, 128, 64, 64, 2, 2, MODE>(p, batch, s);
+    case kSquare: return run_orth_tile<128, 128, 64, 64, 1, 2, MODE>(p, batch, s);
+    default: return run_orth_wide<MODE>(p, batch, s);
   }
+}
+
+static hipError_t step_product(const OrthTileParams &p, int64_t batch, bool last, hipStream_t s) {
+  LaunchScope scope(last ? "orth_last" : "orth_step", s);
+  if (!last) return step_tiles<ORTH_STEP>(p, batch, s);
+  return p.out.param ? step_tiles<ORTH_LAST_MUON>(p, batch, s) : step_tiles<ORTH_LAST>(p, batch, s);
 }
 
 template <int SRC>
@@ -345,11 +279,14 @@ hipError_t launch_orth(const OrthArgs &a, hipStream_t s) {
   io.lo = lo[0];
   io.ldx = w.L;
   io.stride_x = (int64_t)w.S * w.L;
-  io.o = a.o;
-  io.param = a.param;
-  io.param_bf16 = (bf16_t *)a.param_bf16;
-  io.decay = a.decay;
-  io.step_size = a.step_size;
+  OrthOut out{};
+  out.param = a.param;
+  out.lowp = (bf16_t *)(a.param ? a.param_bf16 : a.o);
+  out.rows = a.rows;
+  out.cols = a.cols;
+  out.tall = a.rows > a.cols ? 1 : 0;
+  out.decay = a.decay;
+  out.step_size = a.step_size;
   const bool muon = a.param != nullptr;
   hipError_t err = muon      ? enter<SRC_MUON>(io, a.batch, s)
                    : a.bf16 ? enter<SRC_BF16>(io, a.batch, s)
@@ -385,22 +322,16 @@ hipError_t launch_orth(const OrthArgs &a, hipStream_t s) {
     p.B = hi[cur];
     p.Xlo = lo[cur];
     p.C = hi[cur ^ 1];
-    p.Clo = lo[cur ^ 1];
+    p.Clo = k + 2 < a.steps ? lo[cur ^ 1] : nullptr;
+    p.out = out;
     p.diag = db;
     p.N = w.L;
     p.ldb = p.ldc = w.L;
     p.strideB = p.strideC = io.stride_x;
-    err = step_product(p, a.batch, s);
+    err = step_product(p, a.batch, k + 1 == a.steps, s);
     cur ^= 1;
   }
-  if (err != hipSuccess) return err;
-  io.hi = hi[cur];
-  io.lo = lo[cur];
-  LaunchScope scope("orth_finish", s);
-  const int64_t blocks = a.batch * ceil_div(io.rows, 64) * ceil_div(io.cols, 64);
-  if (muon) orth_finish_kernel<true><<<(unsigned)blocks, kOrthThreads, 0, s>>>(io);
-  else orth_finish_kernel<false><<<(unsigned)blocks, kOrthThreads, 0, s>>>(io);
-  return hipGetLastError();
+  return err;
 }
 
 }  // namespace moe

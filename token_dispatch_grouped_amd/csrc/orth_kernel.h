@@ -11,14 +11,15 @@
 // coefficients): each is stored times 2^12, so that elements from 2^-26 to 8
 // are normal numbers. Three roundings that would still show are avoided:
 //   X is held as a high and a low half (22 bits). The products read the high
-//     one; the term a X, which carries X while B X is small, reads both.
+//     one; the term a X, which carries X while B X is small, reads both (the
+//     last step, where little is left to carry, the high one).
 //   The diagonals of A and B, where nearly orthogonal rows put all their
 //     weight, are held apart in fp32 (DA, DB), the matrices' own diagonals
 //     being zero:  A A = A'A' + (DA_i + DA_j) A'_ij + DA_i^2 [i = j]  and
 //     a X + B X = (a + DB_i) X + B'X.
-// Measured on a 704 x 1024 matrix against fp64: 5e-4 of the norm, 1.4e-3
-// without, 1e-2 with everything in bf16; where a few directions hold all the
-// weight, 4e-4, 3e-2 and 2e-1.
+// Measured on a 704 x 1024 matrix against fp64: 5e-4 of the norm, 1.3e-3
+// without, 1e-2 with everything in bf16; where a few directions hold nearly
+// all the weight, 8e-4, 3e-2 and 2e-1.
 //
 // The kernel is the dense block's tile (ffn_kernel.h): a ring of 64-deep
 // stages filled by the LDS DMA, 32 x 32 x 16 MFMAs with swapped operands, KG
@@ -27,23 +28,34 @@
 // each twice.
 #pragma once
 
-#include "gemm_bf16_kernel.h"
+#include "mx8.h"
+#include "pingpong.h"
 
 namespace moe {
 
-enum { ORTH_GRAM = 0, ORTH_POLY = 1, ORTH_STEP = 2 };
+// LAST: the step whose result goes out, as o or into the weights (MUON)
+enum { ORTH_GRAM = 0, ORTH_POLY = 1, ORTH_STEP = 2, ORTH_LAST = 3, ORTH_LAST_MUON = 4 };
+constexpr bool orth_step(int mode) { return mode >= ORTH_STEP; }
 
 typedef uint16_t half_t;  // fp16 storage (bit pattern)
-typedef __attribute__((__vector_size__(8 * sizeof(_Float16)))) _Float16 f16x8_t;
 
 constexpr float kOrthScale = 4096.f;           // what every fp16 tensor is multiplied with
 constexpr float kOrthUnscale = 1.f / 4096.f;
 
+// Where the last step's result goes: [batch, rows, cols], X itself or, tall, its
+// transpose.
+struct OrthOut {
+  float *param;      // MUON: param = param * decay - step_size * X
+  uint16_t *lowp;    // bf16: X, or MUON: the new param, or NULL
+  int rows, cols, tall;
+  float decay, step_size;
+};
+
 struct OrthTileParams {
   const half_t *A, *B;      // operands, per matrix
   half_t *C;                // GRAM: A', POLY: B', STEP: high half of X'
-  half_t *Clo;              // STEP: low half of X'
-  const half_t *Xlo;        // STEP: low half of X (its high half is B)
+  half_t *Clo;              // STEP: low half of X', or NULL (the last X)
+  const half_t *Xlo;        // STEP: low half of X (its high half is B), or NULL
   const float *diag;        // POLY: DA, STEP: DB (with a added)
   float *diag_out;          // GRAM: DA, POLY: DB + a
   float ca, cb, cc;         // coefficients a, b, c
@@ -53,12 +65,14 @@ struct OrthTileParams {
   int S;                    // stride of the diagonals
   int m_tiles, n_tiles, tiles;        // tiles: of one matrix
   int64_t total;            // tiles of all matrices
+  OrthOut out;              // LAST
 };
 
 MOE_DEVICE uint32_t pack_h2(float a, float b) {  // nearest-even
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
   typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
-  const f16x2_t v = {(_Float16)a, (_Float16)b};
-  return __builtin_bit_cast(uint32_t, v);
+  const f32x2_t v = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2_t));
 }
 MOE_DEVICE half_t f2h(float a) { return __builtin_bit_cast(half_t, (_Float16)a); }
 MOE_DEVICE float h2f(half_t a) { return (float)__builtin_bit_cast(_Float16, a); }
@@ -74,10 +88,342 @@ MOE_DEVICE void orth_swap32(uint32_t &a, uint32_t &b) {
   b = r[1];
 }
 
+// A 4 x 4 transpose over lanes 4n .. 4n + 3: d0, d1 hold a lane's columns 0 .. 3 of
+// fp16 as pairs; after it lane k of the four holds column k, its pairs the
+// lanes' rows.
+MOE_DEVICE void orth_quad_transpose(uint32_t &d0, uint32_t &d1, int lane) {
+  const uint32_t t0 = dpp_u<kDppXor1>(d0), t1 = dpp_u<kDppXor1>(d1);
+  const bool odd = lane & 1, upper = lane & 2;
+  // even lanes: (own low, other's low); odd ones: (other's high, own high)
+  const uint32_t p0 = odd ? __builtin_amdgcn_perm(d0, t0, 0x07060302u) : __builtin_amdgcn_perm(t0, d0, 0x05040100u);
+  const uint32_t p1 = odd ? __builtin_amdgcn_perm(d1, t1, 0x07060302u) : __builtin_amdgcn_perm(t1, d1, 0x05040100u);
+  const uint32_t r = dpp_u<kDppXor2>(upper ? p0 : p1);
+  d0 = upper ? r : p0;
+  d1 = upper ? p1 : r;
+}
+
+// The same for fp32: v[e] becomes row e of column `lane & 3`.
+MOE_DEVICE void orth_quad_transpose(float (&v)[4], int lane) {
+  const bool odd = lane & 1, upper = lane & 2;
+  auto dpp = [](float x, auto ctrl) { return __uint_as_float(dpp_u<decltype(ctrl)::value>(__float_as_uint(x))); };
+  constexpr std::integral_constant<int, kDppXor1> x1{};
+  constexpr std::integral_constant<int, kDppXor2> x2{};
+  const float r0 = dpp(odd ? v[0] : v[1], x1), r1 = dpp(odd ? v[2] : v[3], x1);
+  // p: columns (0 or 1), s: columns (2 or 3), rows of the lane pair
+  const float p0 = odd ? r0 : v[0], p1 = odd ? v[1] : r0, s0 = odd ? r1 : v[2], s1 = odd ? v[3] : r1;
+  const float t0 = dpp(upper ? p0 : s0, x2), t1 = dpp(upper ? p1 : s1, x2);
+  v[0] = upper ? t0 : p0;
+  v[1] = upper ? t1 : p1;
+  v[2] = upper ? s0 : t0;
+  v[3] = upper ? s1 : t1;
+}
+
+// Epilogue of a wavefront's sub-tile of FM x FN blocks of 32 x 32, from row m0 +
+// row0 and column col0 on; m_valid: rows of the tile that exist, mirror: store
+// the transpose as well. acc[i][j][4g + q] is row i*32 + (lane & 31), column j*32
+// + 8g + 4*(lane >> 5) + q.
+//
+// Global memory is read and written in whole rows of a block (8 lanes of 16
+// bytes); a wavefront's own 4 KB of LDS, scr, turns them into the accumulators'
+// order and back. (Straight from registers an instruction touches 32 rows, 32
+// bytes of each, and the step's epilogue took 400 of 730 us.) All loads of a row
+// block are in flight together; their addresses are clamped, not masked, since
+// a branch around each would keep them apart.
+constexpr int kOrthScratch = 4096;  // bytes of a wavefront
+
+template <int FM, int FN, int MODE>
+MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x16_t (&acc)[FM][FN], char *scr, int mat, int m0, int m_valid,
+                              int row0, int col0, bool mirror) {
+  static_assert(FN == 2, "a row of a block is 64 columns");
+  constexpr bool STEP = orth_step(MODE);
+  constexpr bool LAST = MODE == ORTH_LAST || MODE == ORTH_LAST_MUON;
+  int lane = threadIdx.x & 63;
+  // opaque: no address below is formed above the main loop and held there
+  asm volatile("" : "+v"(lane));
+  const int l32 = lane & 31, lhi = lane >> 5;
+  const int rr = lane >> 3, rc = lane & 7;  // row (of 8) and 16-byte chunk of a row-wise access
+  // 16 bytes of row r (128 bytes), chunk c, of the scratch
+  auto at = [&](int r, int c) -> u32x4_t & { return *reinterpret_cast<u32x4_t *>(scr + r * 128 + ((c ^ (r & 7)) * 16)); };
+  auto pack_chunk = [&](const float *v) -> u32x4_t {  // v: groups 2gp (4 values) and 2gp + 1 of a row
+    uint32_t e0 = pack_h2(v[0], v[1]), e1 = pack_h2(v[2], v[3]);
+    uint32_t o0 = pack_h2(v[4], v[5]), o1 = pack_h2(v[6], v[7]);
+    orth_swap32(e0, o0);
+    orth_swap32(e1, o1);
+    return u32x4_t{e0, e1, o0, o1};  // the 8 columns from 16 gp + 8 lhi on
+  };
+  auto unpack_chunk = [&](const u32x4_t &c, float *v) {  // the inverse
+    uint32_t e0 = c[0], e1 = c[1], o0 = c[2], o1 = c[3];
+    orth_swap32(e0, o0);
+    orth_swap32(e1, o1);
+    unpack_h2(e0, v[0], v[1]);
+    unpack_h2(e1, v[2], v[3]);
+    unpack_h2(o0, v[4], v[5]);
+    unpack_h2(o1, v[6], v[7]);
+  };
+  half_t *C = p.C + mat * p.strideC;
+  half_t *Clo = p.Clo ? p.Clo + mat * p.strideC : nullptr;
+  const half_t *src = (STEP ? p.B + mat * p.strideB : p.A + mat * p.strideA);  // X, or POLY: A
+  const half_t *srclo = STEP && !LAST && p.Xlo ? p.Xlo + mat * p.strideC : nullptr;
+  const float *diag = p.diag + (int64_t)mat * p.S;
+  const OrthOut &out = p.out;
+  const int64_t obase = mat * (int64_t)out.rows * out.cols;
+  const bool ovec = (out.cols & 3) == 0;
+  const bool cok = col0 < p.N;  // 64 columns exist or none
+  u32x4_t gh[4], gl[4];
+  f32x4_t pv[2][4];
+  (void)gh;
+  (void)gl;
+  (void)pv;
+  // row block i: its first row, 0 where it does not exist (32 rows do or none)
+  auto block_ok = [&](int i) { return row0 + i * 32 < m_valid && cok; };
+  auto block_row = [&](int i) { return m0 + (block_ok(i) ? row0 + i * 32 : 0); };
+  // the lane's row-wise access
+  auto row_wise = [&](int i) { return (int64_t)(block_row(i) + rr) * p.ldc + (cok ? col0 : 0) + rc * 8; };
+  // fp32 output block j of row block i: row k * 8 + rr, 4 columns from rc * 4 on
+  auto out_at = [&](int i, int j, int k, bool &in) -> int64_t {
+    const int cb = col0 + j * 32, br = block_row(i);
+    const int orow = (out.tall ? cb : br) + k * 8 + rr, ocol = (out.tall ? br : cb) + rc * 4;
+    in = block_ok(i) && orow < out.rows && ocol < out.cols;
+    return obase + (in ? (int64_t)orow * out.cols + ocol : 0);
+  };
+  auto load_rows = [&](int i) {
+    if constexpr (MODE != ORTH_GRAM) {
+      const int64_t o = row_wise(i);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) gh[k] = ld16(src + o + (int64_t)(k * 8) * p.ldc);
+      if (srclo) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) gl[k] = ld16_nt(srclo + o + (int64_t)(k * 8) * p.ldc);
+      }
+    }
+  };
+  auto load_param = [&](int i, int j) {
+    if constexpr (MODE == ORTH_LAST_MUON) {
+      if (!ovec) return;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        bool in;
+        pv[j][k] = *reinterpret_cast<const f32x4_t *>(out.param + out_at(i, j, k, in));
+      }
+    }
+  };
+  load_rows(0);
+  load_param(0, 0);
+  load_param(0, 1);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const bool rok = block_ok(i);
+    const int br = block_row(i);
+    const int gr = br + l32;
+    const int64_t o0 = row_wise(i);
+    if (i > 0) load_rows(i);
+    __builtin_amdgcn_sched_barrier(0);
+    const float dr = MODE == ORTH_GRAM ? 0.f : diag[gr];
+    // acc -> the new values, in place
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][j][q] *= kOrthUnscale;
+    auto col = [&](int j, int q) { return col0 + j * 32 + 8 * (q >> 2) + 4 * lhi + (q & 3); };
+    // rows of the block to the accumulators' order: f(j, first of 8 accumulators, values)
+    auto in_order = [&](const u32x4_t (&g)[4], auto f) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) at(k * 8 + rr, rc) = g[k];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int gp = 0; gp < 2; ++gp) {
+          float v[8];
+          unpack_chunk(at(l32, j * 4 + gp * 2 + lhi), v);
+          f(j, gp * 8, v);
+        }
+    };
+    if constexpr (STEP) {
+      in_order(gh, [&](int j, int q0, const float *v) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) acc[i][j][q0 + q] = fmaf(dr, v[q], acc[i][j][q0 + q]);
+      });
+      if (srclo)
+        in_order(gl, [&](int j, int q0, const float *v) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) acc[i][j][q0 + q] = fmaf(dr, v[q], acc[i][j][q0 + q]);
+        });
+    } else if constexpr (MODE == ORTH_POLY) {
+      in_order(gh, [&](int j, int q0, const float *v) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int c4 = col(j, q0 + 4 * h);
+          const f32x4_t dc = *reinterpret_cast<const f32x4_t *>(diag + (cok ? c4 : 0));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int q = q0 + 4 * h + e;
+            const float a = v[4 * h + e];
+            acc[i][j][q] = fmaf(p.cb, a, p.cc * fmaf((dr + dc[e]) * kOrthUnscale, a, acc[i][j][q]));
+          }
+        }
+      });
+    }
+    if constexpr (!STEP) {
+      if (br < col0 + 64 && col0 < br + 32) {  // a block on the diagonal
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int q = 0; q < 16; ++q)
+            if (col(j, q) == gr) {
+              float x = acc[i][j][q];
+              // A' is zero there: b DA_i + c DA_i^2 is still to come
+              if (MODE == ORTH_POLY)
+                x = fmaf(fmaf(p.cc * dr * kOrthUnscale + p.cb, dr, x), kOrthUnscale, p.ca);
+              if (rok) p.diag_out[(int64_t)mat * p.S + gr] = x;
+              acc[i][j][q] = 0.f;
+            }
+      }
+      if (mirror && rok) {  // transposed, 4 rows of a column to a lane
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            uint32_t d0 = pack_h2(acc[i][j][4 * g], acc[i][j][4 * g + 1]);
+            uint32_t d1 = pack_h2(acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]);
+            orth_quad_transpose(d0, d1, lane);
+            const int cc = col(j, 4 * g) + (lane & 3);
+            *reinterpret_cast<uint2 *>(C + (int64_t)cc * p.ldc + (gr & ~3)) = make_uint2(d0, d1);
+          }
+      }
+    }
+    if constexpr (!LAST) {
+      auto rows_out = [&](half_t *dst) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int gp = 0; gp < 2; ++gp) {
+            float v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = acc[i][j][gp * 8 + q];
+            at(l32, j * 4 + gp * 2 + lhi) = pack_chunk(v);
+          }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const u32x4_t v = at(k * 8 + rr, rc);
+          if (rok) st16_nt(dst + o0 + (int64_t)(k * 8) * p.ldc, v);
+        }
+      };
+      rows_out(C);
+      if (STEP && Clo) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int q = 0; q < 16; ++q) acc[i][j][q] -= h2f(f2h(acc[i][j][q]));
+        rows_out(Clo);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * g + e] * kOrthUnscale;
+          if (out.tall) orth_quad_transpose(v, lane);
+          const u32x4_t w = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+          if (out.tall) at(8 * g + 4 * lhi + (lane & 3), l32 >> 2) = w;
+          else at(l32, 2 * g + lhi) = w;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const u32x4_t w = at(k * 8 + rr, rc);
+          float x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(w[e]);
+          bool in;
+          const int64_t o = out_at(i, j, k, in);
+          if (ovec) {
+            if constexpr (MODE == ORTH_LAST_MUON) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[e] = fmaf(-out.step_size, x[e], pv[j][k][e] * out.decay);
+              if (in) *reinterpret_cast<f32x4_t *>(out.param + o) = f32x4_t{x[0], x[1], x[2], x[3]};
+            }
+            if (out.lowp && in)
+              *reinterpret_cast<uint2 *>(out.lowp + o) = make_uint2(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]));
+          } else if (in) {
+            const int left = out.cols - ((out.tall ? br : col0 + j * 32) + rc * 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (e >= left) break;
+              if constexpr (MODE == ORTH_LAST_MUON) {
+                x[e] = fmaf(-out.step_size, x[e], out.param[o + e] * out.decay);
+                out.param[o + e] = x[e];
+              }
+              if (out.lowp) out.lowp[o + e] = f2bf(x[e]);
+            }
+          }
+        }
+        if (i + 1 < FM) load_param(i + 1, j);
+      }
+    }
+  }
+}
+
+// A place in the order of the tiles: matrix by matrix; of a symmetric product
+// the tiles on and below the diagonal, row by row, of the step groups of
+// kGroupM row tiles, column tile outer.
+template <bool SYM>
+struct OrthCursor {
+  int mat, mt, nt;
+  int base, rows;  // step: the group's first row tile, its row tiles
+
+  MOE_DEVICE void start(const OrthTileParams &p, int64_t id) {
+    mat = __builtin_amdgcn_readfirstlane((int)(id / p.tiles));
+    const int t = __builtin_amdgcn_readfirstlane((int)(id - (int64_t)mat * p.tiles));
+    if (SYM) {  // t = mt (mt + 1) / 2 + nt, nt <= mt
+      mt = (int)((sqrtf(8.f * (float)t + 1.f) - 1.f) * 0.5f);
+      while ((mt + 1) * (mt + 2) / 2 <= t) ++mt;
+      while (mt * (mt + 1) / 2 > t) --mt;
+      mt = __builtin_amdgcn_readfirstlane(mt);
+      nt = t - mt * (mt + 1) / 2;
+    } else {
+      const int per = kGroupM * p.n_tiles;
+      base = __builtin_amdgcn_readfirstlane(t / per * kGroupM);
+      rows = min(kGroupM, p.m_tiles - base);
+      const int rem = t - base * p.n_tiles;
+      nt = __builtin_amdgcn_readfirstlane(rem / rows);
+      mt = base + rem - nt * rows;
+    }
+  }
+  MOE_DEVICE void step(const OrthTileParams &p, int n) {
+    if (SYM) {
+      nt += n;
+      while (nt > mt) {
+        nt -= mt + 1;
+        if (++mt == p.m_tiles) {
+          mt = 0;
+          ++mat;
+        }
+      }
+    } else {
+      mt += n;
+      while (mt >= base + rows) {
+        mt -= rows;
+        if (++nt < p.n_tiles) continue;
+        nt = 0;
+        mt += rows;  // into the next group
+        base += rows;
+        if (base == p.m_tiles) {
+          mt -= base;
+          base = 0;
+          ++mat;
+        }
+        rows = min(kGroupM, p.m_tiles - base);
+      }
+    }
+  }
+};
+
 template <int BM, int BN, int WM, int WN, int KG, int STAGES, int MODE>
 __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void orth_tile_kernel(OrthTileParams p) {
-  constexpr bool BKM = MODE == ORTH_STEP;  // X is [k, n] there
-  constexpr bool SYM = MODE != ORTH_STEP;
+  constexpr bool BKM = orth_step(MODE);  // X is [k, n] there
+  constexpr bool SYM = !orth_step(MODE);
   static_assert(!SYM || BM == BN, "symmetric products have square tiles");
   constexpr int WAVES_M = BM / WM, WAVES_N = BN / WN, NW = WAVES_M * WAVES_N, NT = NW * 64;  // of a k group
   constexpr int FM = WM / 32, FN = WN / 32;
@@ -88,28 +434,17 @@ __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void orth_tile_
   constexpr int STAGE_BYTES = OpA::BYTES + OpB::BYTES;
   constexpr int PER_STAGE = OpA::NDMA + OpB::NDMA;
   static_assert(KG * STAGES * STAGE_BYTES <= 160 * 1024, "LDS budget of one workgroup");
-  static_assert((KG - 1) * BM * BN * 4 <= KG * STAGES * STAGE_BYTES, "the groups' sums meet in the rings");
+  static_assert((KG - 1) * BM * BN * 4 + NW * kOrthScratch <= KG * STAGES * STAGE_BYTES,
+                "the groups' sums meet in the rings, the epilogue's scratch behind them");
   __shared__ u32x4_t lds[KG * STAGES * STAGE_BYTES / 16];
 
   // each XCD takes a contiguous share of the tiles, matrix by matrix
   const int64_t lo = (int64_t)(blockIdx.x & 7) * p.total >> 3, hi = (int64_t)((blockIdx.x & 7) + 1) * p.total >> 3;
   const int64_t id = lo + (int64_t)(blockIdx.x >> 3);
   if (id >= hi) return;
-  const int mat = (int)(id / p.tiles);
-  const int t = (int)(id - (int64_t)mat * p.tiles);
-  int mt, nt;
-  if (SYM) {  // t = mt (mt + 1) / 2 + nt, nt <= mt
-    mt = (int)((sqrtf(8.f * (float)t + 1.f) - 1.f) * 0.5f);
-    while ((mt + 1) * (mt + 2) / 2 <= t) ++mt;
-    while (mt * (mt + 1) / 2 > t) --mt;
-    nt = t - mt * (mt + 1) / 2;
-  } else {  // groups of row tiles, column tile outer
-    const int per = kGroupM * p.n_tiles;
-    const int grp = t / per, rem = t - grp * per;
-    const int rows = min(kGroupM, p.m_tiles - grp * kGroupM);
-    nt = rem / rows;
-    mt = grp * kGroupM + (rem - nt * rows);
-  }
+  OrthCursor<SYM> at;
+  at.start(p, id);
+  const int mat = at.mat, mt = at.mt, nt = at.nt;
   const int m0 = mt * BM, n0 = nt * BN;
   const int m_valid = min(BM, p.M - m0), n_valid = min(BN, p.N - n0);
 
@@ -118,7 +453,6 @@ __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void orth_tile_
   const int tid = KG == 1 ? threadIdx.x : threadIdx.x % NT;
   const int lane = tid & 63, wave = tid >> 6;
   const int wm = wave / WAVES_N, wn = wave % WAVES_N;
-  const int l32 = lane & 31, lhi = lane >> 5;
   const int wave_u = __builtin_amdgcn_readfirstlane(wave);
 
   const half_t *Ab = p.A + mat * p.strideA + (int64_t)m0 * p.lda;
@@ -234,96 +568,10 @@ __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void orth_tile_
         }
   }
 
-  // Epilogue. acc[i][j][4g + q] is row i*32 + l32, column j*32 + 8g + 4*lhi + q
-  // of the wavefront's sub-tile; chunk (j, gp) of a lane is the 8 columns from
-  // j*32 + 16*gp + 8*lhi.
-  auto pack_chunk = [&](const float *v) -> u32x4_t {  // v: groups 2gp (4 values) and 2gp + 1
-    uint32_t e0 = pack_h2(v[0], v[1]), e1 = pack_h2(v[2], v[3]);
-    uint32_t o0 = pack_h2(v[4], v[5]), o1 = pack_h2(v[6], v[7]);
-    orth_swap32(e0, o0);
-    orth_swap32(e1, o1);
-    return u32x4_t{e0, e1, o0, o1};
-  };
-  auto unpack_chunk = [&](const u32x4_t &c, float *v) {  // the inverse
-    uint32_t e0 = c[0], e1 = c[1], o0 = c[2], o1 = c[3];
-    orth_swap32(e0, o0);
-    orth_swap32(e1, o1);
-    unpack_h2(e0, v[0], v[1]);
-    unpack_h2(e1, v[2], v[3]);
-    unpack_h2(o0, v[4], v[5]);
-    unpack_h2(o1, v[6], v[7]);
-  };
-  int el32 = l32, ehi = lhi;
-  // opaque: no address below is formed above the main loop and held there
-  asm volatile("" : "+v"(el32), "+v"(ehi));
-  const int row_l = wm * WM + el32;
-  half_t *C = p.C + mat * p.strideC;
-  const u32x4_t zero = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const int r = row_l + i * 32;
-    const bool rok = r < m_valid;
-    const int gr = m0 + (rok ? r : 0);
-    const int64_t ro = (int64_t)gr * p.ldc;
-    const float dr = MODE == ORTH_GRAM ? 0.f : p.diag[(int64_t)mat * p.S + gr];
-#pragma unroll
-    for (int j = 0; j < FN; ++j)
-#pragma unroll
-      for (int gp = 0; gp < 2; ++gp) {
-        const int cb = n0 + wn * WN + j * 32 + 16 * gp;  // of the chunk pair
-        const int c = cb + 8 * ehi;
-        const bool ok = rok && c < p.N;
-        float v[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = acc[i][j][8 * gp + q] * kOrthUnscale;
-        if constexpr (MODE == ORTH_STEP) {
-          const half_t *xh = p.B + mat * p.strideB;
-          float h[8], l[8];
-          unpack_chunk(ok ? ld16(xh + ro + c) : zero, h);
-          unpack_chunk(ok ? ld16(p.Xlo + mat * p.strideC + ro + c) : zero, l);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) v[q] = fmaf(dr, h[q] + l[q], v[q]);
-          const u32x4_t o = pack_chunk(v);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) l[q] = v[q] - h2f(f2h(v[q]));
-          const u32x4_t ol = pack_chunk(l);
-          if (ok) {
-            st16(C + ro + c, o);
-            st16(p.Clo + mat * p.strideC + ro + c, ol);
-          }
-        } else {
-          // column of v[q]: groups 2gp (q < 4) and 2gp + 1, 8 apart
-          auto col = [&](int q) { return cb + 8 * (q >> 2) + 4 * ehi + (q & 3); };
-          if constexpr (MODE == ORTH_POLY) {
-            float a[8];
-            unpack_chunk(ok ? ld16(p.A + mat * p.strideA + ro + c) : zero, a);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const int cc = col(q);
-              const float dc = p.diag[(int64_t)mat * p.S + (cc < p.N ? cc : 0)];
-              if (cc == m0 + r) a[q] = 0.5f * dr;  // (DA_i + DA_j) a = DA_i^2 on the diagonal, and b a below
-              const float bb = cc == m0 + r ? 2.f * p.cb : p.cb;
-              v[q] = fmaf(bb, a[q], p.cc * fmaf((dr + dc) * kOrthUnscale, a[q], v[q]));
-            }
-          }
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            if (col(q) == m0 + r) {
-              if (rok) p.diag_out[(int64_t)mat * p.S + gr] = MODE == ORTH_GRAM ? v[q] : fmaf(v[q], kOrthUnscale, p.ca);
-              v[q] = 0.f;
-            }
-          const u32x4_t o = pack_chunk(v);
-          if (ok) st16(C + ro + c, o);
-          if (mt != nt && rok) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const int cc = col(q);
-              if (cc < p.N) C[(int64_t)cc * p.ldc + gr] = f2h(v[q]);
-            }
-          }
-        }
-      }
-  }
+  // scratch: behind the groups' sums, in rings that every wavefront is done with
+  if (KG == 1) __syncthreads();
+  char *scr = reinterpret_cast<char *>(lds) + (KG - 1) * BM * BN * 4 + wave * kOrthScratch;
+  orth_epilogue<FM, FN, MODE>(p, acc, scr, mat, m0, m_valid, wm * WM, n0 + wn * WN, mt != nt);
 }
 
 template <int BM, int BN, int WM, int WN, int KG, int STAGES, int MODE>
@@ -331,10 +579,55 @@ hipError_t run_orth_tile(OrthTileParams p, int64_t batch, hipStream_t s) {
   constexpr int NT = KG * (BM / WM) * (BN / WN) * 64;
   p.m_tiles = (p.M + BM - 1) / BM;
   p.n_tiles = (p.N + BN - 1) / BN;
-  p.tiles = MODE == ORTH_STEP ? p.m_tiles * p.n_tiles : p.m_tiles * (p.m_tiles + 1) / 2;
+  p.tiles = orth_step(MODE) ? p.m_tiles * p.n_tiles : p.m_tiles * (p.m_tiles + 1) / 2;
   p.total = batch * p.tiles;
   const unsigned grid = (unsigned)(ceil_div(p.total, 8) * 8);
   orth_tile_kernel<BM, BN, WM, WN, KG, STAGES, MODE><<<dim3(grid), NT, 0, s>>>(p);
+  return hipGetLastError();
+}
+
+// Large products: 256 x 256 tiles on the main loop of pingpong.h, persistent,
+// each XCD walking a contiguous share of the tiles.
+template <int MODE>
+__global__ __launch_bounds__(kPpThreads, 2) void orth_wide_kernel(OrthTileParams p) {
+  __shared__ u32x4_t lds[(kPpLdsBytes + 8 * kOrthScratch) / 16];  // all 160 KB
+  const int64_t lo = (int64_t)(blockIdx.x & 7) * p.total >> 3, hi = (int64_t)((blockIdx.x & 7) + 1) * p.total >> 3;
+  const int step = gridDim.x >> 3;
+  const int64_t first = lo + (blockIdx.x >> 3);
+  if (first >= hi) return;
+  const int count = (int)((hi - first + step - 1) / step);
+  OrthCursor<!orth_step(MODE)> load, put;
+  load.start(p, first);
+  put = load;
+  auto get = [&]() {
+    const int m0 = load.mt * kPpTile, n0 = load.nt * kPpTile;
+    PpTile t;
+    t.A = p.A + load.mat * p.strideA + (int64_t)m0 * p.lda;
+    t.B = p.B + load.mat * p.strideB + (orth_step(MODE) ? (int64_t)n0 : (int64_t)n0 * p.ldb);
+    t.m_valid = min(kPpTile, p.M - m0);
+    t.n_valid = min(kPpTile, p.N - n0);
+    load.step(p, step);
+    return t;
+  };
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  char *scr = reinterpret_cast<char *>(lds) + kPpLdsBytes + wave * kOrthScratch;
+  auto done = [&](f32x16_t (&acc)[4][2]) {
+    const int m0 = put.mt * kPpTile;
+    orth_epilogue<4, 2, MODE>(p, acc, scr, put.mat, m0, min(kPpTile, p.M - m0), (wave >> 2) * 128,
+                              put.nt * kPpTile + (wave & 3) * 64, put.mt != put.nt);
+    put.step(p, step);
+  };
+  pp_tiles<true, orth_step(MODE)>(lds, p.lda, p.ldb, p.K / 64, count, get, done);
+}
+
+template <int MODE>
+hipError_t run_orth_wide(OrthTileParams p, int64_t batch, hipStream_t s) {
+  p.m_tiles = (p.M + kPpTile - 1) / kPpTile;
+  p.n_tiles = (p.N + kPpTile - 1) / kPpTile;
+  p.tiles = orth_step(MODE) ? p.m_tiles * p.n_tiles : p.m_tiles * (p.m_tiles + 1) / 2;
+  p.total = batch * p.tiles;
+  const int64_t grid = std::min<int64_t>(persistent_grid(), ceil_div(p.total, 8) * 8);
+  orth_wide_kernel<MODE><<<dim3((unsigned)grid), kPpThreads, 0, s>>>(p);
   return hipGetLastError();
 }
 

@@ -1,0 +1,274 @@
+// The main loop of the large products (256 x 256 tiles of C[m, n] = sum_k
+// A(m, k) B(n, k)) in bf16 or fp16: two groups of four wavefronts take turns on
+// the matrix cores.
+//
+// A SIMD holds one wavefront of each group. A group's phase is a memory part
+// (DMA and LDS reads) and a compute part (8 MFMAs of 32 x 32 x 16, 256 cycles),
+// each ended by the workgroup's barrier; the second group runs one barrier
+// behind the first, so that one group computes while the other moves data, and
+// the matrix cores change hands instead of waiting for either.
+//
+// A wavefront owns 128 x 64 of the tile, in four quadrants of 64 x 32; a stage of
+// 64 k is four phases:
+//   phase   computes   reads from LDS        issues (tile rows by DMA)
+//   0       A0 B0      B0 of stage t         A1 of stage t + 1
+//   1       A0 B1      B1 of stage t         A0 of stage t + 2
+//   2       A1 B1      A1 of stage t         B0 of stage t + 2   (k-major: -)
+//   3       A1 B0      A0 of stage t + 1     B1 of stage t + 2   (k-major: B)
+// A part of a ring slot is read in a phase and refilled from the second phase
+// after it on: by then both groups have waited for those reads (at the start of
+// their compute parts) and passed a barrier. A part is waited for (vmcnt, every
+// wavefront its own) in the memory part before the one that reads it, five
+// phases after its issue: 80 KB of a workgroup's loads stay in flight.
+//
+// Persistent: the stages of a workgroup's tiles form one stream, the first two of
+// the next tile being loaded under the last two of this one. The epilogue
+// works from registers and leaves the ring alone; both groups meet in front of
+// it and fall apart again behind it.
+#pragma once
+
+#include "gemm_bf16_kernel.h"
+
+namespace moe {
+
+typedef __attribute__((__vector_size__(8 * sizeof(_Float16)))) _Float16 f16x8_t;
+
+constexpr int kPpThreads = 512;
+constexpr int kPpTile = 256;
+constexpr int kPpLdsBytes = 4 * 32768;  // A slots, then B slots
+// Rows and columns that do not exist read zeros, by the buffer's range check:
+// no traffic, and matrix cores that multiply zeros draw less of the power that
+// bounds the clock. A tile's own offsets stay below 2^27.
+constexpr uint32_t kPpRecords = 0x40000000u, kPpOutside = 0x80000000u;
+
+// 16 bytes per lane from rsrc + voff + soff into LDS at lds_addr + 16 lane.
+MOE_DEVICE void bdma16s(rsrc_t rsrc, uint32_t voff, uint32_t soff, uint32_t lds_addr) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds_addr), "v"(voff), "s"(rsrc),
+               "s"(soff)
+               : "memory", "m0");
+}
+
+// Operands of one output tile. A: first row of the tile (k-contiguous); B: first
+// row (k-contiguous) or column (k-major) of the tile.
+struct PpTile {
+  const uint16_t *A, *B;
+  int m_valid, n_valid;
+};
+
+// count: the workgroup's tiles; nk: stages of 64 k, the same for all of them.
+// get(): the next tile to load, asked for once each; done(acc): the epilogue of
+// the next tile, in the same order. acc[a][b][4g + q] is row 128 group + 32 a +
+// (lane & 31), column 64 (wave & 3) + 32 b + 8 g + 4 (lane >> 5) + q of the tile.
+template <bool F16, bool BKM, typename Get, typename Done>
+MOE_DEVICE void pp_tiles(u32x4_t *lds, int64_t lda, int64_t ldb, int nk, int count, Get get, Done done) {
+  if (count <= 0) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int grp = wave >> 2, wn = wave & 3;
+  const int l32 = lane & 31, lhi = lane >> 5;
+  const char *ldsc = reinterpret_cast<const char *>(lds);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)ldsc;
+
+  // Fragment addresses, without slot (bit 15) and row block. Chunk c of a
+  // k-contiguous row r sits at c ^ swz(r); row blocks of odd 32 flip bit 2 of it,
+  // which is bit 1 of ks.
+  uint32_t la[4], lb[4];
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks) {
+    const uint32_t a = (uint32_t)(l32 * 128 + (((ks * 2 + lhi) ^ swz(l32)) * 16));
+    la[ks] = a + (uint32_t)grp * 16384u;
+    lb[ks] = a + 65536u + (uint32_t)wn * 8192u;
+  }
+  if constexpr (BKM) {  // lb[j]: column block j, as Operand's transposing reads
+    const int b = lane & 15, q = lane >> 4;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int col = wn * 64 + j * 32 + 16 * (q & 1) + 4 * (b & 3);
+      const int k_lo = 8 * (q >> 1) + (b >> 2);
+      lb[j] = 65536u + (uint32_t)(k_lo * 512 + ((col >> 3) ^ (4 * (b >> 2))) * 16 + ((col >> 2) & 1) * 8);
+    }
+  }
+  typedef typename std::conditional<F16, f16x8_t, bf16x8_t>::type frag_t;
+  frag_t fa[2][2][4], fb[2][4];  // [half][row block][k step], [half][k step]
+  auto read_a = [&](int h) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+        fa[h][i][ks] = __builtin_bit_cast(
+            frag_t, *reinterpret_cast<const u32x4_t *>(ldsc + la[ks ^ (2 * i)] + (h * 64 + i * 32) * 128));
+  };
+  auto read_b = [&](int j) {
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      if constexpr (BKM) {
+        typedef __attribute__((__vector_size__(8 * sizeof(short)))) short i16x8_t;
+        const i16x4_t lo = lds_read_tr16(ldsc + lb[j] + ks * 8192), hi = lds_read_tr16(ldsc + lb[j] + ks * 8192 + 2048);
+        const i16x8_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        fb[j][ks] = __builtin_bit_cast(frag_t, v);
+      } else {
+        fb[j][ks] = __builtin_bit_cast(
+            frag_t, *reinterpret_cast<const u32x4_t *>(ldsc + lb[ks ^ (2 * j)] + j * 32 * 128));
+      }
+    }
+  };
+
+  // The loading side: stage lk of tile lt into slot ls (a byte offset). Row
+  // groups of 8 rows go to wavefronts so that every group of a wavefront's has
+  // the same swizzle (up to bit 2 of the chunk for B1).
+  uint32_t va[4], vb[4];  // byte offsets: A0 of either group, A1; B0, B0, B1, B1 (k-major: one)
+  rsrc_t ra, rb;
+  const uint16_t *bptr = nullptr;
+  const int qb = (wave & 3) + 8 * (wave >> 2);
+  auto aim = [&](const PpTile &t) {
+    const int l8 = lane >> 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = wave * 8 + l8 + (i & 1) * 128 + (i >> 1) * 64;
+      va[i] = r < t.m_valid ? (uint32_t)((int64_t)r * lda * 2) + (uint32_t)(((lane & 7) ^ swz(r)) * 16) : kPpOutside;
+      if constexpr (!BKM) {
+        const int s = (qb + (i & 1) * 16 + (i >> 1) * 4) * 8 + l8;
+        vb[i] = s < t.n_valid ? (uint32_t)((int64_t)s * ldb * 2) + (uint32_t)(((lane & 7) ^ swz(s)) * 16) : kPpOutside;
+      }
+    }
+    if constexpr (BKM) {
+      const int r = wave * 2 + lhi;
+      const int col = (l32 ^ (4 * (r & 3))) * 8;
+      vb[0] = col < t.n_valid ? (uint32_t)(((int64_t)r * ldb + col) * 2) : kPpOutside;
+    }
+    ra = make_rsrc(t.A, kPpRecords);
+    bptr = t.B;
+    if constexpr (!BKM) rb = make_rsrc(t.B, kPpRecords);
+  };
+  int left = count - 1, lk = 0;  // tiles not asked for yet; the stage
+  uint32_t ls = 0;
+  auto issue_a = [&](int h) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      bdma16s(ra, va[h * 2 + i], (uint32_t)lk * 128u, lds0 + ls + (uint32_t)((wave * 8 + i * 128 + h * 64) * 128));
+  };
+  auto issue_b = [&](int j) {  // k-contiguous
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      bdma16s(rb, vb[j * 2 + i], (uint32_t)lk * 128u, lds0 + 65536u + ls + (uint32_t)((qb + i * 16 + j * 4) * 1024));
+  };
+  auto issue_bk = [&]() {  // k-major
+    rb = make_rsrc(bptr + (int64_t)lk * 64 * ldb, kPpRecords);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      bdma16s(rb, vb[0], (uint32_t)(i * 32 * ldb), lds0 + 65536u + ls + (uint32_t)((i * 8 + wave) * 1024));
+  };
+  auto advance = [&]() {
+    ls ^= 32768u;
+    if (++lk < nk) return;
+    if (left > 0) {
+      --left;
+      lk = 0;
+      aim(get());
+    } else {
+      lk = nk - 1;  // past the last stage: any valid load keeps the counts
+    }
+  };
+
+  f32x16_t acc[4][2];
+  auto mma = [&](int h, int j) {
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if constexpr (F16)
+          acc[h * 2 + i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb[j][ks], fa[h][i][ks], acc[h * 2 + i][j], 0, 0, 0);
+        else
+          acc[h * 2 + i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[j][ks], fa[h][i][ks], acc[h * 2 + i][j], 0, 0, 0);
+      }
+    __builtin_amdgcn_s_setprio(0);
+  };
+  auto turn = [&]() {  // memory part -> compute part
+    __builtin_amdgcn_sched_barrier(0);
+    barrier();
+    wait_lds();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto end = [&]() {  // compute part -> memory part
+    __builtin_amdgcn_sched_barrier(0);
+    barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  aim(get());
+  issue_a(0);
+  if constexpr (BKM) {
+    issue_bk();
+  } else {
+    issue_b(0);
+    issue_b(1);
+  }
+  issue_a(1);
+  advance();
+  issue_a(0);
+  if constexpr (BKM) {
+    issue_bk();
+    wait_vm<8>();  // A0 and B of the first stage
+  } else {
+    issue_b(0);
+    issue_b(1);
+    wait_vm<10>();  // A0 and B0 of the first stage
+  }
+  barrier();
+  read_a(0);
+
+  for (int ti = 0; ti < count; ++ti) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+    if (grp == 1) barrier();
+    for (int kt = 0; kt < nk; ++kt) {
+      read_b(0);
+      issue_a(1);
+      if (!BKM) wait_vm<10>();  // B1 of this stage
+      turn();
+      mma(0, 0);
+      end();
+
+      read_b(1);
+      advance();
+      issue_a(0);
+      wait_vm<10>();  // A1 of this stage
+      turn();
+      mma(0, 1);
+      end();
+
+      read_a(1);
+      if (!BKM) issue_b(0);
+      wait_vm<BKM ? 8 : 10>();  // A0 of the next stage
+      turn();
+      mma(1, 1);
+      end();
+
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) la[ks] ^= 32768u;
+      read_a(0);
+      if constexpr (BKM) {
+        issue_bk();
+        wait_vm<8>();  // B of the next stage
+      } else {
+        issue_b(1);
+        wait_vm<10>();  // B0 of the next stage
+      }
+      turn();
+      mma(1, 0);
+#pragma unroll
+      for (int ks = 0; ks < (BKM ? 2 : 4); ++ks) lb[ks] ^= 32768u;
+      end();
+    }
+    if (grp == 0) barrier();
+    done(acc);
+  }
+  wait_vm<0>();  // no load may land in the next workgroup's LDS
+}
+
+}  // namespace moe
