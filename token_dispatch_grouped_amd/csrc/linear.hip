@@ -3,7 +3,8 @@
 //   dz = dy act'(z)                                  (linear_dact)
 //   dx = (dz W) act_in'(z_in) + add                  (linear_dgrad)
 //   dW (+)= dz^T x, db (+)= sum over tokens of dz    (linear_wgrad)
-// on the dense block's kernels (ffn_kernel.h, ffn_few.h; the weight
+// on the dense block's kernels (ffn_kernel.h, ffn_few.h) and on large
+// tiles of its own (linear_wide.h; the weight
 // gradient's in ffn_ilp.hip), with epilogues of its own: bias, activation and
 // residual are applied to the fp32 sums, so that z and y are each rounded once.
 // The input gradient's epilogue applies the derivative of the activation that
@@ -12,6 +13,7 @@
 #include "ffn_few.h"
 #include "ffn_kernel.h"
 #include "ffn_plan.h"
+#include "linear_wide.h"
 
 namespace moe {
 
@@ -23,7 +25,7 @@ static hipError_t forward(const FfnTileParams &p, hipStream_t s) {
     case kNarrow: return run_ffn_tile<false, 64, 128, 32, 64, 2, 3, false, FFN_LINEAR>(p, s);
     case kPair: return run_ffn_tile<false, 128, 128, 64, 64, 2, 2, false, FFN_LINEAR>(p, s);
     case kHalf: return run_ffn_tile<false, 64, 128, 32, 64, 1, 3, false, FFN_LINEAR>(p, s);
-    case kLarge: return run_ffn_tile<false, 256, 256, 128, 64, 1, 2, false, FFN_LINEAR>(p, s);
+    case kLarge: return run_linear_wide<false>(p, s);
     default: return run_ffn_tile<false, 128, 128, 64, 64, 1, 2, false, FFN_LINEAR>(p, s);
   }
 }
@@ -50,7 +52,7 @@ static hipError_t dgrad(const FfnTileParams &p, hipStream_t s) {
   switch (choose(p.M, p.N, false, false, true)) {
     case kNarrow: return run_ffn_tile<false, 64, 128, 32, 64, 2, 2, true, FFN_LINEAR_DX>(p, s);
     case kPair: return run_ffn_tile<false, 128, 128, 64, 64, 2, 2, true, FFN_LINEAR_DX>(p, s);
-    case kLarge: return run_ffn_tile<false, 256, 256, 128, 64, 1, 2, true, FFN_LINEAR_DX>(p, s);
+    case kLarge: return run_linear_wide<true>(p, s);
     default: return run_ffn_tile<false, 128, 128, 64, 64, 1, 2, true, FFN_LINEAR_DX>(p, s);
   }
 }

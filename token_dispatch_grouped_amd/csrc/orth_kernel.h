@@ -22,7 +22,7 @@
 // all the weight, 8e-4, 3e-2 and 2e-1.
 //
 // The kernel is the dense block's tile (ffn_kernel.h): a ring of 64-deep
-// stages filled by the LDS DMA, 32 x 32 x 16 MFMAs with swapped operands, KG
+// stages filled by the LDS DMA, MFMAs with swapped operands, KG
 // groups of wavefronts sharing a tile's stages where tiles are few. The two
 // symmetric products compute the tiles on and below the diagonal and store
 // each twice.
@@ -81,13 +81,6 @@ MOE_DEVICE void unpack_h2(uint32_t v, float &a, float &b) {
   b = h2f((half_t)(v >> 16));
 }
 
-// vdst's upper lanes trade places with vsrc's lower ones.
-MOE_DEVICE void orth_swap32(uint32_t &a, uint32_t &b) {
-  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-  a = r[0];
-  b = r[1];
-}
-
 // A 4 x 4 transpose over lanes 4n .. 4n + 3: d0, d1 hold a lane's columns 0 .. 3 of
 // fp16 as pairs; after it lane k of the four holds column k, its pairs the
 // lanes' rows.
@@ -118,48 +111,38 @@ MOE_DEVICE void orth_quad_transpose(float (&v)[4], int lane) {
   v[3] = upper ? s1 : t1;
 }
 
-// Epilogue of a wavefront's sub-tile of FM x FN blocks of 32 x 32, from row m0 +
+// Epilogue of a wavefront's sub-tile of FM x 4 blocks of 16 x 16, from row m0 +
 // row0 and column col0 on; m_valid: rows of the tile that exist, mirror: store
-// the transpose as well. acc[i][j][4g + q] is row i*32 + (lane & 31), column j*32
-// + 8g + 4*(lane >> 5) + q.
+// the transpose as well.
 //
-// Global memory is read and written in whole rows of a block (8 lanes of 16
-// bytes); a wavefront's own 4 KB of LDS, scr, turns them into the accumulators'
-// order and back. (Straight from registers an instruction touches 32 rows, 32
-// bytes of each, and the step's epilogue took 400 of 730 us.) All loads of a row
-// block are in flight together; their addresses are clamped, not masked, since
-// a branch around each would keep them apart.
-constexpr int kOrthScratch = 4096;  // bytes of a wavefront
-
-template <int FM, int FN, int MODE>
-MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x16_t (&acc)[FM][FN], char *scr, int mat, int m0, int m_valid,
+// Global memory is read and written in whole rows of a block of 32 rows, which the
+// wavefront's own LDS scr turns into the accumulators' order and back. (Straight
+// from registers an instruction touches 32 rows, 32 bytes of each, and the
+// step's epilogue took 400 of 730 us.) All loads of a row block are in flight
+// together; their addresses are clamped, not masked, since a branch around each
+// would keep them apart.
+template <int FM, int MODE>
+MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x4_t (&acc)[FM][4], char *scr, int mat, int m0, int m_valid,
                               int row0, int col0, bool mirror) {
-  static_assert(FN == 2, "a row of a block is 64 columns");
   constexpr bool STEP = orth_step(MODE);
   constexpr bool LAST = MODE == ORTH_LAST || MODE == ORTH_LAST_MUON;
   int lane = threadIdx.x & 63;
   // opaque: no address below is formed above the main loop and held there
   asm volatile("" : "+v"(lane));
-  const int l32 = lane & 31, lhi = lane >> 5;
-  const int rr = lane >> 3, rc = lane & 7;  // row (of 8) and 16-byte chunk of a row-wise access
-  // 16 bytes of row r (128 bytes), chunk c, of the scratch
-  auto at = [&](int r, int c) -> u32x4_t & { return *reinterpret_cast<u32x4_t *>(scr + r * 128 + ((c ^ (r & 7)) * 16)); };
-  auto pack_chunk = [&](const float *v) -> u32x4_t {  // v: groups 2gp (4 values) and 2gp + 1 of a row
-    uint32_t e0 = pack_h2(v[0], v[1]), e1 = pack_h2(v[2], v[3]);
-    uint32_t o0 = pack_h2(v[4], v[5]), o1 = pack_h2(v[6], v[7]);
-    orth_swap32(e0, o0);
-    orth_swap32(e1, o1);
-    return u32x4_t{e0, e1, o0, o1};  // the 8 columns from 16 gp + 8 lhi on
+  const RowBlock blk(scr, lane);
+  const int l16 = blk.l16, l4 = blk.l4, rr = blk.rr, rc = blk.rc;
+  auto unpack = [](const uint2 &v) {
+    f32x4_t x;
+    float a, b;
+    unpack_h2(v.x, a, b);
+    x[0] = a;
+    x[1] = b;
+    unpack_h2(v.y, a, b);
+    x[2] = a;
+    x[3] = b;
+    return x;
   };
-  auto unpack_chunk = [&](const u32x4_t &c, float *v) {  // the inverse
-    uint32_t e0 = c[0], e1 = c[1], o0 = c[2], o1 = c[3];
-    orth_swap32(e0, o0);
-    orth_swap32(e1, o1);
-    unpack_h2(e0, v[0], v[1]);
-    unpack_h2(e1, v[2], v[3]);
-    unpack_h2(o0, v[4], v[5]);
-    unpack_h2(o1, v[6], v[7]);
-  };
+  auto pack = [](const f32x4_t &a) { return make_uint2(pack_h2(a[0], a[1]), pack_h2(a[2], a[3])); };
   half_t *C = p.C + mat * p.strideC;
   half_t *Clo = p.Clo ? p.Clo + mat * p.strideC : nullptr;
   const half_t *src = (STEP ? p.B + mat * p.strideB : p.A + mat * p.strideA);  // X, or POLY: A
@@ -179,23 +162,12 @@ MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x16_t (&acc)[FM][FN], 
   auto block_row = [&](int i) { return m0 + (block_ok(i) ? row0 + i * 32 : 0); };
   // the lane's row-wise access
   auto row_wise = [&](int i) { return (int64_t)(block_row(i) + rr) * p.ldc + (cok ? col0 : 0) + rc * 8; };
-  // fp32 output block j of row block i: row k * 8 + rr, 4 columns from rc * 4 on
+  // fp32 output block j (32 columns) of row block i: row k * 8 + rr, 4 columns from rc * 4 on
   auto out_at = [&](int i, int j, int k, bool &in) -> int64_t {
     const int cb = col0 + j * 32, br = block_row(i);
     const int orow = (out.tall ? cb : br) + k * 8 + rr, ocol = (out.tall ? br : cb) + rc * 4;
     in = block_ok(i) && orow < out.rows && ocol < out.cols;
     return obase + (in ? (int64_t)orow * out.cols + ocol : 0);
-  };
-  auto load_rows = [&](int i) {
-    if constexpr (MODE != ORTH_GRAM) {
-      const int64_t o = row_wise(i);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) gh[k] = ld16(src + o + (int64_t)(k * 8) * p.ldc);
-      if (srclo) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) gl[k] = ld16_nt(srclo + o + (int64_t)(k * 8) * p.ldc);
-      }
-    }
   };
   auto load_param = [&](int i, int j) {
     if constexpr (MODE == ORTH_LAST_MUON) {
@@ -207,147 +179,144 @@ MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x16_t (&acc)[FM][FN], 
       }
     }
   };
-  load_rows(0);
   load_param(0, 0);
   load_param(0, 1);
-  __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
+  for (int i = 0; i < FM / 2; ++i) {
     const bool rok = block_ok(i);
     const int br = block_row(i);
-    const int gr = br + l32;
     const int64_t o0 = row_wise(i);
-    if (i > 0) load_rows(i);
+    if constexpr (MODE != ORTH_GRAM) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) gh[k] = ld16(src + o0 + (int64_t)(k * 8) * p.ldc);
+      if (srclo) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) gl[k] = ld16_nt(srclo + o0 + (int64_t)(k * 8) * p.ldc);
+      }
+    }
+    float dr[2] = {0.f, 0.f};
+    if constexpr (MODE != ORTH_GRAM) {
+      dr[0] = diag[br + l16];
+      dr[1] = diag[br + 16 + l16];
+    }
     __builtin_amdgcn_sched_barrier(0);
-    const float dr = MODE == ORTH_GRAM ? 0.f : diag[gr];
     // acc -> the new values, in place
+    auto acc_at = [&](int h, int j) -> f32x4_t & { return acc[i * 2 + h][j]; };
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int q = 0; q < 16; ++q) acc[i][j][q] *= kOrthUnscale;
-    auto col = [&](int j, int q) { return col0 + j * 32 + 8 * (q >> 2) + 4 * lhi + (q & 3); };
-    // rows of the block to the accumulators' order: f(j, first of 8 accumulators, values)
-    auto in_order = [&](const u32x4_t (&g)[4], auto f) {
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) at(k * 8 + rr, rc) = g[k];
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int gp = 0; gp < 2; ++gp) {
-          float v[8];
-          unpack_chunk(at(l32, j * 4 + gp * 2 + lhi), v);
-          f(j, gp * 8, v);
-        }
-    };
+        for (int e = 0; e < 4; ++e) acc_at(h, j)[e] *= kOrthUnscale;
+    auto col = [&](int j) { return col0 + j * 16 + 4 * l4; };  // of acc_at(., j)[0]
     if constexpr (STEP) {
-      in_order(gh, [&](int j, int q0, const float *v) {
+      auto add = [&](int h, int j, const uint2 &g) {
+        const f32x4_t v = unpack(g);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) acc[i][j][q0 + q] = fmaf(dr, v[q], acc[i][j][q0 + q]);
-      });
-      if (srclo)
-        in_order(gl, [&](int j, int q0, const float *v) {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) acc[i][j][q0 + q] = fmaf(dr, v[q], acc[i][j][q0 + q]);
-        });
+        for (int e = 0; e < 4; ++e) acc_at(h, j)[e] = fmaf(dr[h], v[e], acc_at(h, j)[e]);
+      };
+      blk.in_order(gh, add);
+      if (srclo) blk.in_order(gl, add);
     } else if constexpr (MODE == ORTH_POLY) {
-      in_order(gh, [&](int j, int q0, const float *v) {
+      blk.in_order(gh, [&](int h, int j, const uint2 &g) {
+        const f32x4_t v = unpack(g);
+        const f32x4_t dc = *reinterpret_cast<const f32x4_t *>(diag + (cok ? col(j) : 0));
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int c4 = col(j, q0 + 4 * h);
-          const f32x4_t dc = *reinterpret_cast<const f32x4_t *>(diag + (cok ? c4 : 0));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int q = q0 + 4 * h + e;
-            const float a = v[4 * h + e];
-            acc[i][j][q] = fmaf(p.cb, a, p.cc * fmaf((dr + dc[e]) * kOrthUnscale, a, acc[i][j][q]));
-          }
-        }
+        for (int e = 0; e < 4; ++e)
+          acc_at(h, j)[e] =
+              fmaf(p.cb, v[e], p.cc * fmaf((dr[h] + dc[e]) * kOrthUnscale, v[e], acc_at(h, j)[e]));
       });
     }
     if constexpr (!STEP) {
       if (br < col0 + 64 && col0 < br + 32) {  // a block on the diagonal
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int q = 0; q < 16; ++q)
-            if (col(j, q) == gr) {
-              float x = acc[i][j][q];
-              // A' is zero there: b DA_i + c DA_i^2 is still to come
-              if (MODE == ORTH_POLY)
-                x = fmaf(fmaf(p.cc * dr * kOrthUnscale + p.cb, dr, x), kOrthUnscale, p.ca);
-              if (rok) p.diag_out[(int64_t)mat * p.S + gr] = x;
-              acc[i][j][q] = 0.f;
-            }
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (col(j) + e == br + h * 16 + l16) {
+                float x = acc_at(h, j)[e];
+                // A' is zero there: b DA_i + c DA_i^2 is still to come
+                if (MODE == ORTH_POLY)
+                  x = fmaf(fmaf(p.cc * dr[h] * kOrthUnscale + p.cb, dr[h], x), kOrthUnscale, p.ca);
+                if (rok) p.diag_out[(int64_t)mat * p.S + br + h * 16 + l16] = x;
+                acc_at(h, j)[e] = 0.f;
+              }
       }
-      if (mirror && rok) {  // transposed, 4 rows of a column to a lane
+      if (mirror) {
+        // transposed: 64 columns of 32 rows (64 bytes) in scr, 16-byte chunks
+        // swizzled by bits 1 and 2 of the column
+        auto at = [&](int c, int ch) { return scr + c * 64 + ((ch ^ ((c >> 1) & 3)) * 16); };
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            uint32_t d0 = pack_h2(acc[i][j][4 * g], acc[i][j][4 * g + 1]);
-            uint32_t d1 = pack_h2(acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]);
-            orth_quad_transpose(d0, d1, lane);
-            const int cc = col(j, 4 * g) + (lane & 3);
-            *reinterpret_cast<uint2 *>(C + (int64_t)cc * p.ldc + (gr & ~3)) = make_uint2(d0, d1);
+          for (int j = 0; j < 4; ++j) {
+            uint2 d = pack(acc_at(h, j));
+            orth_quad_transpose(d.x, d.y, lane);
+            const int r4 = h * 4 + (l16 >> 2);  // rows 4 r4 .. of column 16 j + 4 l4 + (lane & 3)
+            *reinterpret_cast<uint2 *>(at(j * 16 + 4 * l4 + (lane & 3), r4 >> 1) + (r4 & 1) * 8) = d;
           }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int c = k * 16 + (lane >> 2), ch = lane & 3;
+          const u32x4_t v = *reinterpret_cast<const u32x4_t *>(at(c, ch));
+          if (rok) st16(C + (int64_t)(col0 + c) * p.ldc + br + ch * 8, v);
+        }
       }
     }
     if constexpr (!LAST) {
       auto rows_out = [&](half_t *dst) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int gp = 0; gp < 2; ++gp) {
-            float v[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] = acc[i][j][gp * 8 + q];
-            at(l32, j * 4 + gp * 2 + lhi) = pack_chunk(v);
-          }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const u32x4_t v = at(k * 8 + rr, rc);
-          if (rok) st16_nt(dst + o0 + (int64_t)(k * 8) * p.ldc, v);
-        }
+        blk.rows_out([&](int h, int j) { return pack(acc_at(h, j)); },
+                     [&](int k, const u32x4_t &v) {
+                       if (rok) st16_nt(dst + o0 + (int64_t)(k * 8) * p.ldc, v);
+                     });
       };
       rows_out(C);
       if (STEP && Clo) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int q = 0; q < 16; ++q) acc[i][j][q] -= h2f(f2h(acc[i][j][q]));
+          for (int j = 0; j < 4; ++j) {
+            const f32x4_t hi = unpack(pack(acc_at(h, j)));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc_at(h, j)[e] -= hi[e];
+          }
         rows_out(Clo);
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j2 = 0; j2 < 2; ++j2) {
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          float v[4];
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * g + e] * kOrthUnscale;
-          if (out.tall) orth_quad_transpose(v, lane);
-          const u32x4_t w = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
-          if (out.tall) at(8 * g + 4 * lhi + (lane & 3), l32 >> 2) = w;
-          else at(l32, 2 * g + lhi) = w;
-        }
+          for (int x = 0; x < 2; ++x) {
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = acc_at(h, j2 * 2 + x)[e] * kOrthUnscale;
+            if (out.tall) orth_quad_transpose(v, lane);
+            const u32x4_t w = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+            if (out.tall) blk.at16(x * 16 + 4 * l4 + (lane & 3), h * 4 + (l16 >> 2)) = w;
+            else blk.at16(h * 16 + l16, x * 4 + l4) = w;
+          }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const u32x4_t w = at(k * 8 + rr, rc);
+          const u32x4_t w = blk.at16(k * 8 + rr, rc);
           float x[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(w[e]);
           bool in;
-          const int64_t o = out_at(i, j, k, in);
+          const int64_t o = out_at(i, j2, k, in);
           if (ovec) {
             if constexpr (MODE == ORTH_LAST_MUON) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) x[e] = fmaf(-out.step_size, x[e], pv[j][k][e] * out.decay);
+              for (int e = 0; e < 4; ++e) x[e] = fmaf(-out.step_size, x[e], pv[j2][k][e] * out.decay);
               if (in) *reinterpret_cast<f32x4_t *>(out.param + o) = f32x4_t{x[0], x[1], x[2], x[3]};
             }
             if (out.lowp && in)
               *reinterpret_cast<uint2 *>(out.lowp + o) = make_uint2(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]));
           } else if (in) {
-            const int left = out.cols - ((out.tall ? br : col0 + j * 32) + rc * 4);
+            const int left = out.cols - ((out.tall ? br : col0 + j2 * 32) + rc * 4);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               if (e >= left) break;
@@ -359,19 +328,18 @@ MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x16_t (&acc)[FM][FN], 
             }
           }
         }
-        if (i + 1 < FM) load_param(i + 1, j);
+        if (i + 1 < FM / 2) load_param(i + 1, j2);
       }
     }
   }
 }
 
 // A place in the order of the tiles: matrix by matrix; of a symmetric product
-// the tiles on and below the diagonal, row by row, of the step groups of
-// kGroupM row tiles, column tile outer.
+// the tiles on and below the diagonal, row by row.
 template <bool SYM>
 struct OrthCursor {
   int mat, mt, nt;
-  int base, rows;  // step: the group's first row tile, its row tiles
+  PpCursor c;  // step
 
   MOE_DEVICE void start(const OrthTileParams &p, int64_t id) {
     mat = __builtin_amdgcn_readfirstlane((int)(id / p.tiles));
@@ -383,12 +351,9 @@ struct OrthCursor {
       mt = __builtin_amdgcn_readfirstlane(mt);
       nt = t - mt * (mt + 1) / 2;
     } else {
-      const int per = kGroupM * p.n_tiles;
-      base = __builtin_amdgcn_readfirstlane(t / per * kGroupM);
-      rows = min(kGroupM, p.m_tiles - base);
-      const int rem = t - base * p.n_tiles;
-      nt = __builtin_amdgcn_readfirstlane(rem / rows);
-      mt = base + rem - nt * rows;
+      c.start(p.m_tiles, p.n_tiles, t);
+      mt = c.mt;
+      nt = c.nt;
     }
   }
   MOE_DEVICE void step(const OrthTileParams &p, int n) {
@@ -402,20 +367,9 @@ struct OrthCursor {
         }
       }
     } else {
-      mt += n;
-      while (mt >= base + rows) {
-        mt -= rows;
-        if (++nt < p.n_tiles) continue;
-        nt = 0;
-        mt += rows;  // into the next group
-        base += rows;
-        if (base == p.m_tiles) {
-          mt -= base;
-          base = 0;
-          ++mat;
-        }
-        rows = min(kGroupM, p.m_tiles - base);
-      }
+      mat += c.step(p.m_tiles, p.n_tiles, n);
+      mt = c.mt;
+      nt = c.nt;
     }
   }
 };
@@ -426,15 +380,16 @@ __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void orth_tile_
   constexpr bool SYM = !orth_step(MODE);
   static_assert(!SYM || BM == BN, "symmetric products have square tiles");
   constexpr int WAVES_M = BM / WM, WAVES_N = BN / WN, NW = WAVES_M * WAVES_N, NT = NW * 64;  // of a k group
-  constexpr int FM = WM / 32, FN = WN / 32;
-  constexpr int BK = 64, KS = 4;
+  constexpr int FM = WM / 16, FN = WN / 16;
+  constexpr int BK = 64, KS = 2;
+  static_assert(FN == 4, "the epilogue's rows are 64 columns");
   static_assert((KS * FM) % 2 == 0, "the A fragments alternate between two sets across stages");
   using OpA = Operand<BM, false, NW, BK>;
   using OpB = Operand<BN, BKM, NW, BK>;
   constexpr int STAGE_BYTES = OpA::BYTES + OpB::BYTES;
   constexpr int PER_STAGE = OpA::NDMA + OpB::NDMA;
   static_assert(KG * STAGES * STAGE_BYTES <= 160 * 1024, "LDS budget of one workgroup");
-  static_assert((KG - 1) * BM * BN * 4 + NW * kOrthScratch <= KG * STAGES * STAGE_BYTES,
+  static_assert((KG - 1) * BM * BN * 4 + NW * RowBlock::kBytes <= KG * STAGES * STAGE_BYTES,
                 "the groups' sums meet in the rings, the epilogue's scratch behind them");
   __shared__ u32x4_t lds[KG * STAGES * STAGE_BYTES / 16];
 
@@ -469,20 +424,32 @@ __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void orth_tile_
     opa.issue(ks * BK, p.lda, p.K, sb, wave_u);
     opb.issue(ks * BK, p.ldb, p.K, sb + OpA::BYTES, wave_u);
   };
-  auto load_a = [&](int slot, int ks, int i) {
-    return __builtin_bit_cast(f16x8_t, opa.frag(ldsc + slot * STAGE_BYTES, wm * WM + i * 32, ks, lane));
+  // 8 consecutive k of row lane & 15 from 8 (lane >> 4) on
+  auto rows16 = [&](const char *tile, int rb, int ks) {
+    const int r = rb + (lane & 15), c = ks * 4 + (lane >> 4);
+    return __builtin_bit_cast(f16x8_t, *reinterpret_cast<const u32x4_t *>(tile + (r * 8 + (c ^ swz(r))) * 16));
   };
+  auto cols16 = [&](const char *tile, int cb, int ks) {  // of column lane & 15, k-major (Operand's layout)
+    typedef __attribute__((__vector_size__(8 * sizeof(short)))) short i16x8_t;
+    const int b = lane & 15, col = cb + 4 * (b & 3);
+    const char *a = tile + (ks * 32 + 8 * (lane >> 4) + (b >> 2)) * OpB::ROWB + ((col >> 3) ^ (4 * (b >> 2))) * 16 +
+                    ((col >> 2) & 1) * 8;
+    const i16x4_t lo = lds_read_tr16(a), hi = lds_read_tr16(a + 4 * OpB::ROWB);
+    const i16x8_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    return __builtin_bit_cast(f16x8_t, v);
+  };
+  auto load_a = [&](int slot, int ks, int i) { return rows16(ldsc + slot * STAGE_BYTES, wm * WM + i * 16, ks); };
   auto load_b = [&](int slot, int ks, int j) {
-    return __builtin_bit_cast(f16x8_t, opb.frag(ldsc + slot * STAGE_BYTES + OpA::BYTES, wn * WN + j * 32, ks, lane));
+    const char *tile = ldsc + slot * STAGE_BYTES + OpA::BYTES;
+    if constexpr (BKM) return cols16(tile, wn * WN + j * 16, ks);
+    else return rows16(tile, wn * WN + j * 16, ks);
   };
 
-  f32x16_t acc[FM][FN];
+  f32x4_t acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
   const int stages = p.K / BK;
   const int nk = (stages - kg + KG - 1) / KG;  // the group's own
@@ -490,8 +457,7 @@ __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void orth_tile_
   f16x8_t fa[2], fb[2][FN];
   auto mma = [&](int i, int set_a, int set_b) {
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
-      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb[set_b][j], fa[set_a], acc[i][j], 0, 0, 0);
+    for (int j = 0; j < FN; ++j) acc[i][j] = mfma16(fb[set_b][j], fa[set_a], acc[i][j]);
   };
   // wait until at most `younger` whole stages are still in flight
   auto wait_stages = [&](int younger) {
@@ -544,34 +510,27 @@ __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void orth_tile_
     // the groups' sums, added in the order of the groups by the first one
     __syncthreads();  // every ring is done with
     f32x4_t *sum = reinterpret_cast<f32x4_t *>(lds);
-    auto at = [&](int g, int f, int q) -> f32x4_t & { return sum[((g * FM * FN + f) * 4 + q) * NT + tid]; };
+    auto at = [&](int g, int f) -> f32x4_t & { return sum[(g * FM * FN + f) * NT + tid]; };
     if (kg > 0) {
 #pragma unroll
-      for (int f = 0; f < FM * FN; ++f)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x16_t &a = acc[f / FN][f % FN];
-          at(kg - 1, f, q) = f32x4_t{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
-        }
+      for (int f = 0; f < FM * FN; ++f) at(kg - 1, f) = acc[f / FN][f % FN];
     }
     __syncthreads();
     if (kg > 0) return;
 #pragma unroll
     for (int g = 0; g < KG - 1; ++g)
 #pragma unroll
-      for (int f = 0; f < FM * FN; ++f)
+      for (int f = 0; f < FM * FN; ++f) {
+        const f32x4_t v = at(g, f);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x4_t v = at(g, f, q);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[f / FN][f % FN][4 * q + e] += v[e];
-        }
+        for (int e = 0; e < 4; ++e) acc[f / FN][f % FN][e] += v[e];
+      }
   }
 
   // scratch: behind the groups' sums, in rings that every wavefront is done with
   if (KG == 1) __syncthreads();
-  char *scr = reinterpret_cast<char *>(lds) + (KG - 1) * BM * BN * 4 + wave * kOrthScratch;
-  orth_epilogue<FM, FN, MODE>(p, acc, scr, mat, m0, m_valid, wm * WM, n0 + wn * WN, mt != nt);
+  char *scr = reinterpret_cast<char *>(lds) + (KG - 1) * BM * BN * 4 + wave * RowBlock::kBytes;
+  orth_epilogue<FM, MODE>(p, acc, scr, mat, m0, m_valid, wm * WM, n0 + wn * WN, mt != nt);
 }
 
 template <int BM, int BN, int WM, int WN, int KG, int STAGES, int MODE>
@@ -590,7 +549,7 @@ hipError_t run_orth_tile(OrthTileParams p, int64_t batch, hipStream_t s) {
 // each XCD walking a contiguous share of the tiles.
 template <int MODE>
 __global__ __launch_bounds__(kPpThreads, 2) void orth_wide_kernel(OrthTileParams p) {
-  __shared__ u32x4_t lds[(kPpLdsBytes + 8 * kOrthScratch) / 16];  // all 160 KB
+  __shared__ u32x4_t lds[(kPpLdsBytes + 8 * RowBlock::kBytes) / 16];  // all 160 KB
   const int64_t lo = (int64_t)(blockIdx.x & 7) * p.total >> 3, hi = (int64_t)((blockIdx.x & 7) + 1) * p.total >> 3;
   const int step = gridDim.x >> 3;
   const int64_t first = lo + (blockIdx.x >> 3);
@@ -610,10 +569,10 @@ __global__ __launch_bounds__(kPpThreads, 2) void orth_wide_kernel(OrthTileParams
     return t;
   };
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  char *scr = reinterpret_cast<char *>(lds) + kPpLdsBytes + wave * kOrthScratch;
-  auto done = [&](f32x16_t (&acc)[4][2]) {
+  char *scr = reinterpret_cast<char *>(lds) + kPpLdsBytes + wave * RowBlock::kBytes;
+  auto done = [&](PpAcc &acc) {
     const int m0 = put.mt * kPpTile;
-    orth_epilogue<4, 2, MODE>(p, acc, scr, put.mat, m0, min(kPpTile, p.M - m0), (wave >> 2) * 128,
+    orth_epilogue<8, MODE>(p, acc, scr, put.mat, m0, min(kPpTile, p.M - m0), (wave >> 2) * 128,
                               put.nt * kPpTile + (wave & 3) * 64, put.mt != put.nt);
     put.step(p, step);
   };

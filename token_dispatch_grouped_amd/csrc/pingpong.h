@@ -3,7 +3,7 @@
 // the matrix cores.
 //
 // A SIMD holds one wavefront of each group. A group's phase is a memory part
-// (DMA and LDS reads) and a compute part (8 MFMAs of 32 x 32 x 16, 256 cycles),
+// (DMA and LDS reads) and a compute part (16 MFMAs of 16 x 16 x 32, 256 cycles),
 // each ended by the workgroup's barrier; the second group runs one barrier
 // behind the first, so that one group computes while the other moves data, and
 // the matrix cores change hands instead of waiting for either.
@@ -23,8 +23,12 @@
 //
 // Persistent: the stages of a workgroup's tiles form one stream, the first two of
 // the next tile being loaded under the last two of this one. The epilogue
-// works from registers and leaves the ring alone; both groups meet in front of
-// it and fall apart again behind it.
+// leaves the ring alone; both groups meet in front of it and fall apart again
+// behind it.
+//
+// Measured on 8192^3 bf16 (normal values): 1.54 PFLOP/s, and 1.38 with MFMAs of
+// 32 x 32 x 16, which read and write twice the accumulators for a product: the
+// power that they draw bounds the clock (on zeros the same loop reaches 1.7).
 #pragma once
 
 #include "gemm_bf16_kernel.h"
@@ -55,62 +59,157 @@ struct PpTile {
   int m_valid, n_valid;
 };
 
+// MFMA of 16 x 16 x 32 with swapped operands: a lane holds row (lane & 15) of the
+// block, 4 consecutive columns from 4 (lane >> 4) on; a fragment, 8 consecutive
+// k of row (lane & 15) from 8 (lane >> 4) on.
+MOE_DEVICE f32x4_t mfma16(bf16x8_t b, bf16x8_t a, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, a, c, 0, 0, 0);
+}
+MOE_DEVICE f32x4_t mfma16(f16x8_t b, f16x8_t a, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(b, a, c, 0, 0, 0);
+}
+// Accumulators of a wavefront's 128 x 64: [row block][column block].
+typedef f32x4_t PpAcc[8][4];
+
+// 32 rows of 64 16-bit values (or 32 of fp32) in a wavefront's own 4 KB of LDS,
+// between whole rows as global memory is read and written (8 lanes of 16 bytes)
+// and the accumulators' order.
+struct RowBlock {
+  static constexpr int kBytes = 4096;
+  char *scr;
+  int l16, l4;  // the lane's row and column group of an accumulator block
+  int rr, rc;   // row (of 8) and 16-byte chunk of a row-wise access
+  MOE_DEVICE RowBlock(char *s, int lane) : scr(s), l16(lane & 15), l4(lane >> 4), rr(lane >> 3), rc(lane & 7) {}
+  MOE_DEVICE u32x4_t &at16(int r, int c) const {
+    return *reinterpret_cast<u32x4_t *>(scr + r * 128 + ((c ^ (r & 7)) * 16));
+  }
+  // 4 16-bit values of accumulator block (i, j), i of 2 row blocks
+  MOE_DEVICE uint2 &at8(int i, int j) const {
+    const int r = i * 16 + l16;
+    return *reinterpret_cast<uint2 *>(scr + r * 128 + (((j * 2 + (l4 >> 1)) ^ (r & 7)) * 16) + (l4 & 1) * 8);
+  }
+  // rows g[k] = row k * 8 + rr, chunk rc to f(i, j, the 4 values of block (i, j))
+  template <typename F>
+  MOE_DEVICE void in_order(const u32x4_t (&g)[4], F f) const {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) at16(k * 8 + rr, rc) = g[k];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f(i, j, at8(i, j));
+  }
+  // f(i, j) of every block to rows, put(k, chunk rc of row k * 8 + rr)
+  template <typename F, typename Put>
+  MOE_DEVICE void rows_out(F f, Put put) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) at8(i, j) = f(i, j);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) put(k, at16(k * 8 + rr, rc));
+  }
+};
+
+// A place in the order of the tiles of a product: groups of kGroupM row tiles,
+// column tile outer, so that the tiles an XCD works on share operands.
+struct PpCursor {
+  int mt, nt;      // row tile, column tile
+  int base, rows;  // the group's first row tile, its row tiles
+
+  MOE_DEVICE void start(int m_tiles, int n_tiles, int t) {
+    base = __builtin_amdgcn_readfirstlane(t / (kGroupM * n_tiles) * kGroupM);
+    rows = min(kGroupM, m_tiles - base);
+    const int rem = t - base * n_tiles;
+    nt = __builtin_amdgcn_readfirstlane(rem / rows);
+    mt = base + rem - nt * rows;
+  }
+  // n places on; how often it began again behind the last
+  MOE_DEVICE int step(int m_tiles, int n_tiles, int n) {
+    int again = 0;
+    mt += n;
+    while (mt >= base + rows) {
+      mt -= rows;
+      if (++nt < n_tiles) continue;
+      nt = 0;
+      mt += rows;  // into the next group
+      base += rows;
+      if (base == m_tiles) {
+        mt -= base;
+        base = 0;
+        ++again;
+      }
+      rows = min(kGroupM, m_tiles - base);
+    }
+    return again;
+  }
+};
+
 // count: the workgroup's tiles; nk: stages of 64 k, the same for all of them.
 // get(): the next tile to load, asked for once each; done(acc): the epilogue of
-// the next tile, in the same order. acc[a][b][4g + q] is row 128 group + 32 a +
-// (lane & 31), column 64 (wave & 3) + 32 b + 8 g + 4 (lane >> 5) + q of the tile.
+// the next tile, in the same order: a wavefront's acc is rows from 128 group,
+// columns from 64 (wave & 3) on.
 template <bool F16, bool BKM, typename Get, typename Done>
 MOE_DEVICE void pp_tiles(u32x4_t *lds, int64_t lda, int64_t ldb, int nk, int count, Get get, Done done) {
   if (count <= 0) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int grp = wave >> 2, wn = wave & 3;
-  const int l32 = lane & 31, lhi = lane >> 5;
+  const int l16 = lane & 15, l4 = lane >> 4;
   const char *ldsc = reinterpret_cast<const char *>(lds);
   const uint32_t lds0 = (uint32_t)(uintptr_t)ldsc;
 
   // Fragment addresses, without slot (bit 15) and row block. Chunk c of a
-  // k-contiguous row r sits at c ^ swz(r); row blocks of odd 32 flip bit 2 of it,
-  // which is bit 1 of ks.
-  uint32_t la[4], lb[4];
+  // k-contiguous row r sits at c ^ swz(r): of row block b (16 rows) bit 0 of b
+  // flips bit 1 of the chunk and bit 1 of b flips bit 2, which is the k step.
+  uint32_t la[2][2], lb[2][2];  // [bit 0 of the row block][k step]
 #pragma unroll
-  for (int ks = 0; ks < 4; ++ks) {
-    const uint32_t a = (uint32_t)(l32 * 128 + (((ks * 2 + lhi) ^ swz(l32)) * 16));
-    la[ks] = a + (uint32_t)grp * 16384u;
-    lb[ks] = a + 65536u + (uint32_t)wn * 8192u;
-  }
-  if constexpr (BKM) {  // lb[j]: column block j, as Operand's transposing reads
-    const int b = lane & 15, q = lane >> 4;
+  for (int x = 0; x < 2; ++x)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int col = wn * 64 + j * 32 + 16 * (q & 1) + 4 * (b & 3);
-      const int k_lo = 8 * (q >> 1) + (b >> 2);
-      lb[j] = 65536u + (uint32_t)(k_lo * 512 + ((col >> 3) ^ (4 * (b >> 2))) * 16 + ((col >> 2) & 1) * 8);
+    for (int ks = 0; ks < 2; ++ks) {
+      const uint32_t a = (uint32_t)(l16 * 128 + (((ks * 4 + l4) ^ swz(l16) ^ (2 * x)) * 16));
+      la[x][ks] = a + (uint32_t)grp * 16384u;
+      lb[x][ks] = a + 65536u + (uint32_t)wn * 8192u;
     }
+  if constexpr (BKM) {
+    // lb[j][x]: column block 2j + x. Chunk c of k row r sits at c ^ 4 (r % 4) ^
+    // 2 (r / 8 % 2), so that the 16-lane groups of a transposing read, which are
+    // 8 rows apart, use different banks.
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int col = wn * 64 + j * 32 + x * 16 + 4 * (l16 & 3);
+        const int k_lo = 8 * l4 + (l16 >> 2);
+        const int c = (col >> 3) ^ (4 * (l16 >> 2)) ^ (2 * (l4 & 1));
+        lb[j][x] = 65536u + (uint32_t)(k_lo * 512 + c * 16 + ((col >> 2) & 1) * 8);
+      }
   }
   typedef typename std::conditional<F16, f16x8_t, bf16x8_t>::type frag_t;
-  frag_t fa[2][2][4], fb[2][4];  // [half][row block][k step], [half][k step]
+  frag_t fa[2][4][2], fb[2][2][2];  // [half][row block][k step]
   auto read_a = [&](int h) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
+      for (int ks = 0; ks < 2; ++ks)
         fa[h][i][ks] = __builtin_bit_cast(
-            frag_t, *reinterpret_cast<const u32x4_t *>(ldsc + la[ks ^ (2 * i)] + (h * 64 + i * 32) * 128));
+            frag_t, *reinterpret_cast<const u32x4_t *>(ldsc + la[i & 1][ks ^ (i >> 1)] + (h * 64 + i * 16) * 128));
   };
   auto read_b = [&](int j) {
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      if constexpr (BKM) {
-        typedef __attribute__((__vector_size__(8 * sizeof(short)))) short i16x8_t;
-        const i16x4_t lo = lds_read_tr16(ldsc + lb[j] + ks * 8192), hi = lds_read_tr16(ldsc + lb[j] + ks * 8192 + 2048);
-        const i16x8_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        fb[j][ks] = __builtin_bit_cast(frag_t, v);
-      } else {
-        fb[j][ks] = __builtin_bit_cast(
-            frag_t, *reinterpret_cast<const u32x4_t *>(ldsc + lb[ks ^ (2 * j)] + j * 32 * 128));
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        if constexpr (BKM) {
+          typedef __attribute__((__vector_size__(8 * sizeof(short)))) short i16x8_t;
+          const char *a = ldsc + lb[j][x] + ks * 16384;
+          const i16x4_t lo = lds_read_tr16(a), hi = lds_read_tr16(a + 2048);
+          const i16x8_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+          fb[j][x][ks] = __builtin_bit_cast(frag_t, v);
+        } else {
+          fb[j][x][ks] = __builtin_bit_cast(
+              frag_t, *reinterpret_cast<const u32x4_t *>(ldsc + lb[x][ks ^ j] + (j * 32 + x * 16) * 128));
+        }
       }
-    }
   };
 
   // The loading side: stage lk of tile lt into slot ls (a byte offset). Row
@@ -132,8 +231,8 @@ MOE_DEVICE void pp_tiles(u32x4_t *lds, int64_t lda, int64_t ldb, int nk, int cou
       }
     }
     if constexpr (BKM) {
-      const int r = wave * 2 + lhi;
-      const int col = (l32 ^ (4 * (r & 3))) * 8;
+      const int r = wave * 2 + (lane >> 5);
+      const int col = ((lane & 31) ^ (4 * (r & 3)) ^ (2 * (wave >> 2))) * 8;  // row i * 16 + r, bit 3 of it is wave >> 2
       vb[0] = col < t.n_valid ? (uint32_t)(((int64_t)r * ldb + col) * 2) : kPpOutside;
     }
     ra = make_rsrc(t.A, kPpRecords);
@@ -170,18 +269,15 @@ MOE_DEVICE void pp_tiles(u32x4_t *lds, int64_t lda, int64_t ldb, int nk, int cou
     }
   };
 
-  f32x16_t acc[4][2];
+  PpAcc acc;
   auto mma = [&](int h, int j) {
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks)
+    for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if constexpr (F16)
-          acc[h * 2 + i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb[j][ks], fa[h][i][ks], acc[h * 2 + i][j], 0, 0, 0);
-        else
-          acc[h * 2 + i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[j][ks], fa[h][i][ks], acc[h * 2 + i][j], 0, 0, 0);
-      }
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) acc[h * 4 + i][j * 2 + x] = mfma16(fb[j][x][ks], fa[h][i][ks], acc[h * 4 + i][j * 2 + x]);
     __builtin_amdgcn_s_setprio(0);
   };
   auto turn = [&]() {  // memory part -> compute part
@@ -216,15 +312,16 @@ MOE_DEVICE void pp_tiles(u32x4_t *lds, int64_t lda, int64_t ldb, int nk, int cou
     wait_vm<10>();  // A0 and B0 of the first stage
   }
   barrier();
-  read_a(0);
 
   for (int ti = 0; ti < count; ++ti) {
+    // read here and not in phase 3 of the tile before, so that the epilogue has
+    // those registers; waited for, as the part is refilled two barriers on
+    read_a(0);
+    wait_lds();
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     if (grp == 1) barrier();
     for (int kt = 0; kt < nk; ++kt) {
       read_b(0);
@@ -250,8 +347,8 @@ MOE_DEVICE void pp_tiles(u32x4_t *lds, int64_t lda, int64_t ldb, int nk, int cou
       end();
 
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) la[ks] ^= 32768u;
-      read_a(0);
+      for (int q = 0; q < 4; ++q) la[q >> 1][q & 1] ^= 32768u;
+      if (kt + 1 < nk) read_a(0);
       if constexpr (BKM) {
         issue_bk();
         wait_vm<8>();  // B of the next stage
@@ -262,7 +359,7 @@ MOE_DEVICE void pp_tiles(u32x4_t *lds, int64_t lda, int64_t ldb, int nk, int cou
       turn();
       mma(1, 0);
 #pragma unroll
-      for (int ks = 0; ks < (BKM ? 2 : 4); ++ks) lb[ks] ^= 32768u;
+      for (int q = 0; q < 4; ++q) lb[q >> 1][q & 1] ^= 32768u;
       end();
     }
     if (grp == 0) barrier();
