@@ -118,9 +118,8 @@ MOE_DEVICE void orth_quad_transpose(float (&v)[4], int lane) {
 // Global memory is read and written in whole rows of a block of 32 rows, which the
 // wavefront's own LDS scr turns into the accumulators' order and back. (Straight
 // from registers an instruction touches 32 rows, 32 bytes of each, and the
-// step's epilogue took 400 of 730 us.) All loads of a row block are in flight
-// together; their addresses are clamped, not masked, since a branch around each
-// would keep them apart.
+// step's epilogue took 400 of 730 us.) The loads of a row block and the next one
+// are in flight together.
 template <int FM, int MODE>
 MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x4_t (&acc)[FM][4], char *scr, int mat, int m0, int m_valid,
                               int row0, int col0, bool mirror) {
@@ -143,57 +142,63 @@ MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x4_t (&acc)[FM][4], ch
     return x;
   };
   auto pack = [](const f32x4_t &a) { return make_uint2(pack_h2(a[0], a[1]), pack_h2(a[2], a[3])); };
-  half_t *C = p.C + mat * p.strideC;
-  half_t *Clo = p.Clo ? p.Clo + mat * p.strideC : nullptr;
-  const half_t *src = (STEP ? p.B + mat * p.strideB : p.A + mat * p.strideA);  // X, or POLY: A
-  const half_t *srclo = STEP && !LAST && p.Xlo ? p.Xlo + mat * p.strideC : nullptr;
+  // the part's rows in every tensor of X's (A's) shape: 32 of a block and 64
+  // columns exist or none
+  const int rows = col0 < p.N ? m_valid - row0 : 0;
+  if (rows <= 0) return;
+  const int r0 = m0 + row0;
+  const int64_t at0 = (int64_t)r0 * p.ldc + col0;
+  const uint32_t pitch = (uint32_t)p.ldc * 2u, off0 = (uint32_t)rr * pitch + (uint32_t)rc * 16u;
+  auto off = [&](int i, int k) { return off0 + (uint32_t)(i * 32 + k * 8) * pitch; };
+  const bool low = STEP && !LAST && p.Xlo;
+  const TileRows src((STEP ? p.B + mat * p.strideB : p.A + mat * p.strideA) + at0, pitch, rows);  // X, or POLY: A
+  const TileRows srclo(p.Xlo + mat * p.strideC + at0, pitch, low ? rows : 0);
+  const TileRows dst(p.C + mat * p.strideC + at0, pitch, rows), dstlo(p.Clo + mat * p.strideC + at0, pitch, p.Clo ? rows : 0);
   const float *diag = p.diag + (int64_t)mat * p.S;
   const OrthOut &out = p.out;
-  const int64_t obase = mat * (int64_t)out.rows * out.cols;
   const bool ovec = (out.cols & 3) == 0;
-  const bool cok = col0 < p.N;  // 64 columns exist or none
-  u32x4_t gh[4], gl[4];
+  u32x4_t gh[2][4], gl[2][4];  // of a row block and the next one
   f32x4_t pv[2][4];
   (void)gh;
   (void)gl;
   (void)pv;
-  // row block i: its first row, 0 where it does not exist (32 rows do or none)
-  auto block_ok = [&](int i) { return row0 + i * 32 < m_valid && cok; };
-  auto block_row = [&](int i) { return m0 + (block_ok(i) ? row0 + i * 32 : 0); };
-  // the lane's row-wise access
-  auto row_wise = [&](int i) { return (int64_t)(block_row(i) + rr) * p.ldc + (cok ? col0 : 0) + rc * 8; };
-  // fp32 output block j (32 columns) of row block i: row k * 8 + rr, 4 columns from rc * 4 on
-  auto out_at = [&](int i, int j, int k, bool &in) -> int64_t {
-    const int cb = col0 + j * 32, br = block_row(i);
-    const int orow = (out.tall ? cb : br) + k * 8 + rr, ocol = (out.tall ? br : cb) + rc * 4;
-    in = block_ok(i) && orow < out.rows && ocol < out.cols;
-    return obase + (in ? (int64_t)orow * out.cols + ocol : 0);
+  // the part's place in the matrices given, and its 32 x 32 fp32 blocks there:
+  // row k * 8 + rr, 4 columns from rc * 4 on
+  const int64_t obase = mat * (int64_t)out.rows * out.cols;
+  const int orow0 = out.tall ? col0 : r0, ocol0 = out.tall ? r0 : col0;
+  auto out_at = [&](int i, int j, int k, int &left) -> int64_t {
+    const int orow = orow0 + (out.tall ? j : i) * 32 + k * 8 + rr, ocol = ocol0 + (out.tall ? i : j) * 32 + rc * 4;
+    left = orow < out.rows ? out.cols - ocol : 0;
+    return obase + (left > 0 ? (int64_t)orow * out.cols + ocol : 0);
+  };
+  auto load_rows = [&](int i) {
+    if constexpr (MODE != ORTH_GRAM) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) gh[i & 1][k] = src.load(off(i, k));
+    }
+    if constexpr (MODE == ORTH_STEP) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) gl[i & 1][k] = srclo.load<2>(off(i, k));  // zeros where there is none
+    }
   };
   auto load_param = [&](int i, int j) {
     if constexpr (MODE == ORTH_LAST_MUON) {
       if (!ovec) return;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        bool in;
-        pv[j][k] = *reinterpret_cast<const f32x4_t *>(out.param + out_at(i, j, k, in));
+        int left;
+        pv[j][k] = *reinterpret_cast<const f32x4_t *>(out.param + out_at(i, j, k, left));
       }
     }
   };
+  load_rows(0);
   load_param(0, 0);
   load_param(0, 1);
 #pragma unroll
   for (int i = 0; i < FM / 2; ++i) {
-    const bool rok = block_ok(i);
-    const int br = block_row(i);
-    const int64_t o0 = row_wise(i);
-    if constexpr (MODE != ORTH_GRAM) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) gh[k] = ld16(src + o0 + (int64_t)(k * 8) * p.ldc);
-      if (srclo) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) gl[k] = ld16_nt(srclo + o0 + (int64_t)(k * 8) * p.ldc);
-      }
-    }
+    if (i * 32 >= rows) break;
+    const int br = r0 + i * 32;
+    if (i + 1 < FM / 2) load_rows(i + 1);
     float dr[2] = {0.f, 0.f};
     if constexpr (MODE != ORTH_GRAM) {
       dr[0] = diag[br + l16];
@@ -215,12 +220,14 @@ MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x4_t (&acc)[FM][4], ch
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc_at(h, j)[e] = fmaf(dr[h], v[e], acc_at(h, j)[e]);
       };
-      blk.in_order(gh, add);
-      if (srclo) blk.in_order(gl, add);
+      blk.in_order(gh[i & 1], add);
+      if constexpr (MODE == ORTH_STEP) {
+        if (low) blk.in_order(gl[i & 1], add);
+      }
     } else if constexpr (MODE == ORTH_POLY) {
-      blk.in_order(gh, [&](int h, int j, const uint2 &g) {
+      blk.in_order(gh[i & 1], [&](int h, int j, const uint2 &g) {
         const f32x4_t v = unpack(g);
-        const f32x4_t dc = *reinterpret_cast<const f32x4_t *>(diag + (cok ? col(j) : 0));
+        const f32x4_t dc = *reinterpret_cast<const f32x4_t *>(diag + col(j));
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           acc_at(h, j)[e] =
@@ -240,7 +247,7 @@ MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x4_t (&acc)[FM][4], ch
                 // A' is zero there: b DA_i + c DA_i^2 is still to come
                 if (MODE == ORTH_POLY)
                   x = fmaf(fmaf(p.cc * dr[h] * kOrthUnscale + p.cb, dr[h], x), kOrthUnscale, p.ca);
-                if (rok) p.diag_out[(int64_t)mat * p.S + br + h * 16 + l16] = x;
+                p.diag_out[(int64_t)mat * p.S + br + h * 16 + l16] = x;
                 acc_at(h, j)[e] = 0.f;
               }
       }
@@ -261,19 +268,17 @@ MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x4_t (&acc)[FM][4], ch
         for (int k = 0; k < 4; ++k) {
           const int c = k * 16 + (lane >> 2), ch = lane & 3;
           const u32x4_t v = *reinterpret_cast<const u32x4_t *>(at(c, ch));
-          if (rok) st16(C + (int64_t)(col0 + c) * p.ldc + br + ch * 8, v);
+          st16(p.C + mat * p.strideC + (int64_t)(col0 + c) * p.ldc + br + ch * 8, v);
         }
       }
     }
     if constexpr (!LAST) {
-      auto rows_out = [&](half_t *dst) {
+      auto rows_out = [&](const TileRows &to) {
         blk.rows_out([&](int h, int j) { return pack(acc_at(h, j)); },
-                     [&](int k, const u32x4_t &v) {
-                       if (rok) st16_nt(dst + o0 + (int64_t)(k * 8) * p.ldc, v);
-                     });
+                     [&](int k, const u32x4_t &v) { to.store<2>(off(i, k), v); });
       };
-      rows_out(C);
-      if (STEP && Clo) {
+      rows_out(dst);
+      if (STEP && p.Clo) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -282,7 +287,7 @@ MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x4_t (&acc)[FM][4], ch
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc_at(h, j)[e] -= hi[e];
           }
-        rows_out(Clo);
+        rows_out(dstlo);
       }
     } else {
 #pragma unroll
@@ -305,18 +310,18 @@ MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x4_t (&acc)[FM][4], ch
           float x[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(w[e]);
-          bool in;
-          const int64_t o = out_at(i, j2, k, in);
+          int left;
+          const int64_t o = out_at(i, j2, k, left);
+          if (left <= 0) continue;
           if (ovec) {
             if constexpr (MODE == ORTH_LAST_MUON) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) x[e] = fmaf(-out.step_size, x[e], pv[j2][k][e] * out.decay);
-              if (in) *reinterpret_cast<f32x4_t *>(out.param + o) = f32x4_t{x[0], x[1], x[2], x[3]};
+              *reinterpret_cast<f32x4_t *>(out.param + o) = f32x4_t{x[0], x[1], x[2], x[3]};
             }
-            if (out.lowp && in)
+            if (out.lowp)
               *reinterpret_cast<uint2 *>(out.lowp + o) = make_uint2(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]));
-          } else if (in) {
-            const int left = out.cols - ((out.tall ? br : col0 + j2 * 32) + rc * 4);
+          } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               if (e >= left) break;

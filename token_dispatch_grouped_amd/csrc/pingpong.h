@@ -71,6 +71,26 @@ MOE_DEVICE f32x4_t mfma16(f16x8_t b, f16x8_t a, f32x4_t c) {
 // Accumulators of a wavefront's 128 x 64: [row block][column block].
 typedef f32x4_t PpAcc[8][4];
 
+// Rows of a wavefront's part of a tile in global memory, 32-bit byte offsets from
+// its first element. Rows past the last read zeros and are not written, by the
+// buffer's range check. aux 2: non-temporal.
+struct TileRows {
+  __amdgpu_buffer_rsrc_t r;
+  // base: the part's first element; pitch: bytes of a row; rows: that exist
+  MOE_DEVICE TileRows(const void *base, int64_t pitch, int rows)
+      : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, rows > 0 ? (int)(rows * pitch) : 0,
+                                            0x00020000)) {}
+  template <int AUX = 0>
+  MOE_DEVICE u32x4_t load(uint32_t off) const {
+    return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, AUX));
+  }
+  template <int AUX = 0>
+  MOE_DEVICE void store(uint32_t off, const u32x4_t &v) const {
+    typedef uint32_t vec_t __attribute__((ext_vector_type(4)));
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(vec_t, v), r, (int)off, 0, AUX);
+  }
+};
+
 // 32 rows of 64 16-bit values (or 32 of fp32) in a wavefront's own 4 KB of LDS,
 // between whole rows as global memory is read and written (8 lanes of 16 bytes)
 // and the accumulators' order.
