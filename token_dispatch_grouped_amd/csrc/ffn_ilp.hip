@@ -137,8 +137,8 @@ hipError_t launch_ffn_dense_wgrad(const FfnArgs &a, hipStream_t s) {
   return wgrad(prod, 2, ffn_wgrad_plan(a.T, a.d, a.F), a.T, static_cast<float *>(a.partial), a.accumulate, "ffn_wgrad", s);
 }
 
-// The dense product's weight gradient dW = dz^T x: the same launch with one
-// product.
+// The dense product's weight gradient dW = dz^T x on the small tiles: the same
+// launch with one product.
 hipError_t launch_linear_dw(const LinearArgs &a, hipStream_t s) {
   const WgradProduct prod = {a.dz, a.x, a.N, a.K, a.dw};
   return wgrad(&prod, 1, linear_wgrad_plan(a.T, a.K, a.N), a.T, a.partial, a.accumulate, "linear_wgrad", s);

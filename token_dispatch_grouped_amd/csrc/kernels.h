@@ -162,7 +162,7 @@ hipError_t launch_layernorm_fwd(const LayerNormArgs &a, hipStream_t s);
 hipError_t launch_layernorm_bwd(const LayerNormArgs &a, hipStream_t s);
 
 // ----- dense product with bias, activation and residual (linear.hip; the
-// weight gradient in ffn_ilp.hip) -----
+// weight gradient's small tiles in ffn_ilp.hip) -----
 struct LinearArgs {
   const void *x, *w, *bias, *add;  // bias, add may be NULL
   void *z, *y;                     // forward: z may be NULL
@@ -177,8 +177,8 @@ struct LinearArgs {
 hipError_t launch_linear_fwd(const LinearArgs &a, hipStream_t s);
 hipError_t launch_linear_dact(const LinearArgs &a, hipStream_t s);
 hipError_t launch_linear_dgrad(const LinearArgs &a, hipStream_t s);
-hipError_t launch_linear_dw(const LinearArgs &a, hipStream_t s);
-hipError_t launch_linear_db(const LinearArgs &a, hipStream_t s);
+hipError_t launch_linear_wgrad(const LinearArgs &a, hipStream_t s);
+hipError_t launch_linear_dw(const LinearArgs &a, hipStream_t s);  // the small tiles
 
 // ----- orthogonalisation and the step around it (orth.hip) -----
 struct OrthArgs {

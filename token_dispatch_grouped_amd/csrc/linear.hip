@@ -13,6 +13,7 @@
 #include "ffn_few.h"
 #include "ffn_kernel.h"
 #include "ffn_plan.h"
+#include "linear_dw.h"
 #include "linear_wide.h"
 
 namespace moe {
@@ -138,7 +139,7 @@ __global__ __launch_bounds__(64) void linear_db_reduce_kernel(const float *parti
   db[c] = accumulate ? db[c] + v : v;
 }
 
-hipError_t launch_linear_db(const LinearArgs &a, hipStream_t s) {
+static hipError_t linear_db(const LinearArgs &a, hipStream_t s) {
   const int slices = linear_db_slices(a.T);
   LaunchScope scope("linear_db", s);
   if (slices > 0) {
@@ -149,6 +150,51 @@ hipError_t launch_linear_db(const LinearArgs &a, hipStream_t s) {
     if (err != hipSuccess) return err;
   }
   linear_db_reduce_kernel<<<(unsigned)(a.N / 64), 64, 0, s>>>(a.db_partial, a.db, a.N, slices, a.accumulate ? 1 : 0);
+  return hipGetLastError();
+}
+
+// The weight gradient's large tiles: db comes with them, one launch adds the
+// slices of both. The small tiles (ffn_ilp.hip) leave db to the pass above.
+hipError_t launch_linear_wgrad(const LinearArgs &a, hipStream_t s) {
+  const FfnWgrad plan = linear_wgrad_plan(a.T, a.K, a.N);
+  if (plan.tile != kPpTile) {
+    const hipError_t err = launch_linear_dw(a, s);
+    return err != hipSuccess || !a.db ? err : linear_db(a, s);
+  }
+  const bool direct = plan.slices == 1;
+  if (plan.slices > 0) {
+    LaunchScope scope("linear_wgrad", s);
+    LinearDwParams p{};
+    p.dz = (const bf16_t *)a.dz;
+    p.x = (const bf16_t *)a.x;
+    p.dw = direct ? a.dw : a.partial;
+    p.db = !a.db ? nullptr : direct ? a.db : a.db_partial;
+    p.T = (int)a.T;
+    p.K = a.K;
+    p.N = a.N;
+    p.chunk = plan.chunk;
+    p.slices = plan.slices;
+    p.n_tiles = (a.N + kPpTile - 1) / kPpTile;
+    p.k_tiles = (a.K + kPpTile - 1) / kPpTile;
+    const int64_t total = (int64_t)p.n_tiles * p.k_tiles * plan.slices;
+    const dim3 grid((unsigned)std::min<int64_t>(persistent_grid(), ceil_div(total, 8) * 8));
+    if (direct && a.accumulate) linear_dw_kernel<true><<<grid, kPpThreads, 0, s>>>(p);
+    else linear_dw_kernel<false><<<grid, kPpThreads, 0, s>>>(p);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  if (direct) return hipSuccess;
+  LaunchScope scope("linear_wgrad_reduce", s);
+  LinearDwReduce r{};
+  r.dw_part = a.partial;
+  r.db_part = a.db_partial;
+  r.dw = a.dw;
+  r.db = a.db;
+  r.dw4 = (int64_t)a.N * a.K / 4;
+  r.db4 = a.db ? a.N / 4 : 0;
+  r.slices = plan.slices;
+  r.accumulate = a.accumulate ? 1 : 0;
+  linear_dw_reduce_kernel<<<(unsigned)ceil_div(r.dw4 + r.db4, 256), 256, 0, s>>>(r);
   return hipGetLastError();
 }
 

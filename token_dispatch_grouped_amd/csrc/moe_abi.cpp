@@ -1033,9 +1033,7 @@ moe_status moe_linear_wgrad(const moe_linear_shape *shape, const void *dz, const
   a.K = s.K;
   a.N = s.N;
   a.accumulate = !overwrite;
-  const hipError_t err = launch_linear_dw(a, as_stream(stream));
-  if (err != hipSuccess || !db) return hip_status(err, "linear_wgrad");
-  return hip_status(launch_linear_db(a, as_stream(stream)), "linear_wgrad");
+  return hip_status(launch_linear_wgrad(a, as_stream(stream)), "linear_wgrad");
 }
 
 moe_status moe_orthogonalize_workspace_size(const moe_orth_shape *shape, size_t *ws) {

@@ -15,6 +15,7 @@
 //   1       A0 B1      B1 of stage t         A0 of stage t + 2
 //   2       A1 B1      A1 of stage t         B0 of stage t + 2   (k-major: -)
 //   3       A1 B0      A0 of stage t + 1     B1 of stage t + 2   (k-major: B)
+// (A k-major as well, AKM: A1 is read in phase 0, A issued in phase 2.)
 // A part of a ring slot is read in a phase and refilled from the second phase
 // after it on: by then both groups have waited for those reads (at the start of
 // their compute parts) and passed a barrier. A part is waited for (vmcnt, every
@@ -52,12 +53,21 @@ MOE_DEVICE void bdma16s(rsrc_t rsrc, uint32_t voff, uint32_t soff, uint32_t lds_
                : "memory", "m0");
 }
 
-// Operands of one output tile. A: first row of the tile (k-contiguous); B: first
-// row (k-contiguous) or column (k-major) of the tile.
+// Operands of one output tile. A, B: first row of the tile (k-contiguous) or its
+// first column (k-major). AKM: k rows from k_valid on (of this tile's sum) are
+// zeros, so that a sum's length need be no multiple of a stage.
 struct PpTile {
   const uint16_t *A, *B;
   int m_valid, n_valid;
+  int k_valid;
 };
+
+// Chunk c (16 bytes) of a k-contiguous row r of 128 bytes sits at c ^ pp_swz(r): a
+// b128 read is served in four groups of 16 lanes (0-3 with 12-15 and 20-27, the
+// others between them, and so for the upper half), two rows to the 64 banks, and
+// with fragments of 16 rows each group finds every bank once. Counted: no
+// conflict cycles, one for each active one with (r ^ r / 8) % 8.
+MOE_DEVICE int pp_swz(int r) { return (r >> 1) & 7; }
 
 // MFMA of 16 x 16 x 32 with swapped operands: a lane holds row (lane & 15) of the
 // block, 4 consecutive columns from 4 (lane >> 4) on; a fragment, 8 consecutive
@@ -167,9 +177,13 @@ struct PpCursor {
 // count: the workgroup's tiles; nk: stages of 64 k, the same for all of them.
 // get(): the next tile to load, asked for once each; done(acc): the epilogue of
 // the next tile, in the same order: a wavefront's acc is rows from 128 group,
-// columns from 64 (wave & 3) on.
-template <bool F16, bool BKM, typename Get, typename Done>
-MOE_DEVICE void pp_tiles(u32x4_t *lds, int64_t lda, int64_t ldb, int nk, int count, Get get, Done done) {
+// columns from 64 (wave & 3) on. AKM: row block i of either half is rows from 16
+// (i ^ (wave & 3)) of it on, so that block 0 is another one in each of the four
+// wavefronts that hold the same rows; stage(a0, a1), once a stage, is given the
+// fragments of block 0 of both halves.
+template <bool F16, bool AKM, bool BKM, typename Get, typename Done, typename Stage>
+MOE_DEVICE void pp_tiles(u32x4_t *lds, int64_t lda, int64_t ldb, int nk, int count, Get get, Done done, Stage stage) {
+  static_assert(!AKM || BKM, "no product has A alone k-major");
   if (count <= 0) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -178,41 +192,55 @@ MOE_DEVICE void pp_tiles(u32x4_t *lds, int64_t lda, int64_t ldb, int nk, int cou
   const char *ldsc = reinterpret_cast<const char *>(lds);
   const uint32_t lds0 = (uint32_t)(uintptr_t)ldsc;
 
-  // Fragment addresses, without slot (bit 15) and row block. Chunk c of a
-  // k-contiguous row r sits at c ^ swz(r): of row block b (16 rows) bit 0 of b
-  // flips bit 1 of the chunk and bit 1 of b flips bit 2, which is the k step.
-  uint32_t la[2][2], lb[2][2];  // [bit 0 of the row block][k step]
+  // Fragment addresses, without slot (bit 15) and row block. k-contiguous: per k
+  // step, chunk c of row r at c ^ pp_swz(r), which no row block of 16 changes.
+  uint32_t la[2][2], lb[2][2];
 #pragma unroll
-  for (int x = 0; x < 2; ++x)
+  for (int ks = 0; ks < 2; ++ks) {
+    const uint32_t a = (uint32_t)(l16 * 128 + (((ks * 4 + l4) ^ pp_swz(l16)) * 16));
+    la[0][ks] = a + (uint32_t)grp * 16384u;
+    lb[0][ks] = a + 65536u + (uint32_t)wn * 8192u;
+  }
+  // k-major: of the 16 columns from `first` on. Chunk c of k row r sits at c ^ 4
+  // (r % 4) ^ 2 (r / 8 % 2), so that the 16-lane groups of a transposing read,
+  // which are 8 rows apart, use different banks.
+  auto km_addr = [&](int first) {
+    const int col = first + 4 * (l16 & 3);
+    const int k_lo = 8 * l4 + (l16 >> 2);
+    const int c = (col >> 3) ^ (4 * (l16 >> 2)) ^ (2 * (l4 & 1));
+    return (uint32_t)(k_lo * 512 + c * 16 + ((col >> 2) & 1) * 8);
+  };
+  if constexpr (BKM) {  // lb[j][x]: column block 2j + x
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      const uint32_t a = (uint32_t)(l16 * 128 + (((ks * 4 + l4) ^ swz(l16) ^ (2 * x)) * 16));
-      la[x][ks] = a + (uint32_t)grp * 16384u;
-      lb[x][ks] = a + 65536u + (uint32_t)wn * 8192u;
-    }
-  if constexpr (BKM) {
-    // lb[j][x]: column block 2j + x. Chunk c of k row r sits at c ^ 4 (r % 4) ^
-    // 2 (r / 8 % 2), so that the 16-lane groups of a transposing read, which are
-    // 8 rows apart, use different banks.
+    for (int q = 0; q < 4; ++q) lb[q >> 1][q & 1] = 65536u + km_addr(wn * 64 + q * 16);
+  }
+  // AKM: la[x][y]: column block 2x + y of either half (64 columns apart: bit 3 of
+  // the chunk, which the swizzle may flip: 128 bytes up or down)
+  int la_half = 0;
+  if constexpr (AKM) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int col = wn * 64 + j * 32 + x * 16 + 4 * (l16 & 3);
-        const int k_lo = 8 * l4 + (l16 >> 2);
-        const int c = (col >> 3) ^ (4 * (l16 >> 2)) ^ (2 * (l4 & 1));
-        lb[j][x] = 65536u + (uint32_t)(k_lo * 512 + c * 16 + ((col >> 2) & 1) * 8);
-      }
+    for (int q = 0; q < 4; ++q) la[q >> 1][q & 1] = km_addr(grp * 128 + (q ^ wn) * 16);
+    la_half = (int)(km_addr(grp * 128 + 64) - km_addr(grp * 128));
   }
   typedef typename std::conditional<F16, f16x8_t, bf16x8_t>::type frag_t;
   frag_t fa[2][4][2], fb[2][2][2];  // [half][row block][k step]
+  auto read_km = [&](const char *a) {
+    typedef __attribute__((__vector_size__(8 * sizeof(short)))) short i16x8_t;
+    const i16x4_t lo = lds_read_tr16(a), hi = lds_read_tr16(a + 2048);
+    const i16x8_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    return __builtin_bit_cast(frag_t, v);
+  };
   auto read_a = [&](int h) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks)
-        fa[h][i][ks] = __builtin_bit_cast(
-            frag_t, *reinterpret_cast<const u32x4_t *>(ldsc + la[i & 1][ks ^ (i >> 1)] + (h * 64 + i * 16) * 128));
+      for (int ks = 0; ks < 2; ++ks) {
+        if constexpr (AKM)
+          fa[h][i][ks] = read_km(ldsc + (la[i >> 1][i & 1] + (uint32_t)(h ? la_half : 0)) + ks * 16384);
+        else
+          fa[h][i][ks] = __builtin_bit_cast(
+              frag_t, *reinterpret_cast<const u32x4_t *>(ldsc + la[0][ks] + (h * 64 + i * 16) * 128));
+      }
   };
   auto read_b = [&](int j) {
 #pragma unroll
@@ -220,43 +248,47 @@ MOE_DEVICE void pp_tiles(u32x4_t *lds, int64_t lda, int64_t ldb, int nk, int cou
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         if constexpr (BKM) {
-          typedef __attribute__((__vector_size__(8 * sizeof(short)))) short i16x8_t;
-          const char *a = ldsc + lb[j][x] + ks * 16384;
-          const i16x4_t lo = lds_read_tr16(a), hi = lds_read_tr16(a + 2048);
-          const i16x8_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-          fb[j][x][ks] = __builtin_bit_cast(frag_t, v);
+          fb[j][x][ks] = read_km(ldsc + lb[j][x] + ks * 16384);
         } else {
           fb[j][x][ks] = __builtin_bit_cast(
-              frag_t, *reinterpret_cast<const u32x4_t *>(ldsc + lb[x][ks ^ j] + (j * 32 + x * 16) * 128));
+              frag_t, *reinterpret_cast<const u32x4_t *>(ldsc + lb[0][ks] + (j * 32 + x * 16) * 128));
         }
       }
   };
 
-  // The loading side: stage lk of tile lt into slot ls (a byte offset). Row
-  // groups of 8 rows go to wavefronts so that every group of a wavefront's has
-  // the same swizzle (up to bit 2 of the chunk for B1).
+  // The loading side: stage lk of tile lt into slot ls (a byte offset), a
+  // wavefront 8 rows a load.
   uint32_t va[4], vb[4];  // byte offsets: A0 of either group, A1; B0, B0, B1, B1 (k-major: one)
   rsrc_t ra, rb;
-  const uint16_t *bptr = nullptr;
+  const uint16_t *aptr = nullptr, *bptr = nullptr;
+  int k_valid = 0;
   const int qb = (wave & 3) + 8 * (wave >> 2);
+  // k-major: the lane's 16 bytes of k row wave * 2 + lane / 32 of a stage; row i *
+  // 16 + that one has the same swizzle (bit 3 of it is wave / 4)
+  auto km_off = [&](int64_t ld, int valid) {
+    const int r = wave * 2 + (lane >> 5);
+    const int col = ((lane & 31) ^ (4 * (r & 3)) ^ (2 * (wave >> 2))) * 8;
+    return col < valid ? (uint32_t)(((int64_t)r * ld + col) * 2) : kPpOutside;
+  };
   auto aim = [&](const PpTile &t) {
     const int l8 = lane >> 3;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = wave * 8 + l8 + (i & 1) * 128 + (i >> 1) * 64;
-      va[i] = r < t.m_valid ? (uint32_t)((int64_t)r * lda * 2) + (uint32_t)(((lane & 7) ^ swz(r)) * 16) : kPpOutside;
+      if constexpr (!AKM) {
+        const int r = wave * 8 + l8 + (i & 1) * 128 + (i >> 1) * 64;
+        va[i] = r < t.m_valid ? (uint32_t)((int64_t)r * lda * 2) + (uint32_t)(((lane & 7) ^ pp_swz(r)) * 16) : kPpOutside;
+      }
       if constexpr (!BKM) {
         const int s = (qb + (i & 1) * 16 + (i >> 1) * 4) * 8 + l8;
-        vb[i] = s < t.n_valid ? (uint32_t)((int64_t)s * ldb * 2) + (uint32_t)(((lane & 7) ^ swz(s)) * 16) : kPpOutside;
+        vb[i] = s < t.n_valid ? (uint32_t)((int64_t)s * ldb * 2) + (uint32_t)(((lane & 7) ^ pp_swz(s)) * 16) : kPpOutside;
       }
     }
-    if constexpr (BKM) {
-      const int r = wave * 2 + (lane >> 5);
-      const int col = ((lane & 31) ^ (4 * (r & 3)) ^ (2 * (wave >> 2))) * 8;  // row i * 16 + r, bit 3 of it is wave >> 2
-      vb[0] = col < t.n_valid ? (uint32_t)(((int64_t)r * ldb + col) * 2) : kPpOutside;
-    }
-    ra = make_rsrc(t.A, kPpRecords);
+    if constexpr (AKM) va[0] = km_off(lda, t.m_valid);
+    if constexpr (BKM) vb[0] = km_off(ldb, t.n_valid);
+    aptr = t.A;
     bptr = t.B;
+    k_valid = t.k_valid;
+    if constexpr (!AKM) ra = make_rsrc(t.A, kPpRecords);
     if constexpr (!BKM) rb = make_rsrc(t.B, kPpRecords);
   };
   int left = count - 1, lk = 0;  // tiles not asked for yet; the stage
@@ -271,12 +303,21 @@ MOE_DEVICE void pp_tiles(u32x4_t *lds, int64_t lda, int64_t ldb, int nk, int cou
     for (int i = 0; i < 2; ++i)
       bdma16s(rb, vb[j * 2 + i], (uint32_t)lk * 128u, lds0 + 65536u + ls + (uint32_t)((qb + i * 16 + j * 4) * 1024));
   };
-  auto issue_bk = [&]() {  // k-major
-    rb = make_rsrc(bptr + (int64_t)lk * 64 * ldb, kPpRecords);
+  // a whole k-major stage, rows past the sum's end by the range check: a lane
+  // offset below kPpOutside is in row floor(offset / pitch)
+  auto issue_km = [&](const uint16_t *ptr, int64_t ld, uint32_t voff, uint32_t dst) {
+    uint32_t records = kPpRecords;
+    if constexpr (AKM) records = (uint32_t)max(0, min(64, k_valid - lk * 64)) * (uint32_t)(ld * 2);
+    const rsrc_t r = make_rsrc(ptr + (int64_t)lk * 64 * ld, records);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      bdma16s(rb, vb[0], (uint32_t)(i * 32 * ldb), lds0 + 65536u + ls + (uint32_t)((i * 8 + wave) * 1024));
+    for (int i = 0; i < 4; ++i) {
+      // the row part in the lane's offset, which the range check surely sees
+      const uint32_t v = AKM ? voff + (uint32_t)(i * 32 * ld) : voff;
+      bdma16s(r, v, AKM ? 0u : (uint32_t)(i * 32 * ld), dst + (uint32_t)((i * 8 + wave) * 1024));
+    }
   };
+  auto issue_ak = [&]() { issue_km(aptr, lda, va[0], lds0 + ls); };
+  auto issue_bk = [&]() { issue_km(bptr, ldb, vb[0], lds0 + 65536u + ls); };
   auto advance = [&]() {
     ls ^= 32768u;
     if (++lk < nk) return;
@@ -313,23 +354,32 @@ MOE_DEVICE void pp_tiles(u32x4_t *lds, int64_t lda, int64_t ldb, int nk, int cou
   };
 
   aim(get());
-  issue_a(0);
-  if constexpr (BKM) {
+  if constexpr (AKM) {
+    issue_ak();
     issue_bk();
-  } else {
-    issue_b(0);
-    issue_b(1);
-  }
-  issue_a(1);
-  advance();
-  issue_a(0);
-  if constexpr (BKM) {
+    advance();
+    issue_ak();
     issue_bk();
-    wait_vm<8>();  // A0 and B of the first stage
+    wait_vm<8>();  // the first stage
   } else {
-    issue_b(0);
-    issue_b(1);
-    wait_vm<10>();  // A0 and B0 of the first stage
+    issue_a(0);
+    if constexpr (BKM) {
+      issue_bk();
+    } else {
+      issue_b(0);
+      issue_b(1);
+    }
+    issue_a(1);
+    advance();
+    issue_a(0);
+    if constexpr (BKM) {
+      issue_bk();
+      wait_vm<8>();  // A0 and B of the first stage
+    } else {
+      issue_b(0);
+      issue_b(1);
+      wait_vm<10>();  // A0 and B0 of the first stage
+    }
   }
   barrier();
 
@@ -345,7 +395,8 @@ MOE_DEVICE void pp_tiles(u32x4_t *lds, int64_t lda, int64_t ldb, int nk, int cou
     if (grp == 1) barrier();
     for (int kt = 0; kt < nk; ++kt) {
       read_b(0);
-      issue_a(1);
+      if constexpr (AKM) read_a(1);
+      else issue_a(1);
       if (!BKM) wait_vm<10>();  // B1 of this stage
       turn();
       mma(0, 0);
@@ -353,21 +404,29 @@ MOE_DEVICE void pp_tiles(u32x4_t *lds, int64_t lda, int64_t ldb, int nk, int cou
 
       read_b(1);
       advance();
-      issue_a(0);
-      wait_vm<10>();  // A1 of this stage
+      if constexpr (!AKM) {
+        issue_a(0);
+        wait_vm<10>();  // A1 of this stage
+      }
       turn();
       mma(0, 1);
+      if constexpr (AKM) stage(fa[0][0], fa[1][0]);
       end();
 
-      read_a(1);
-      if (!BKM) issue_b(0);
-      wait_vm<BKM ? 8 : 10>();  // A0 of the next stage
+      if constexpr (AKM) {
+        issue_ak();
+        wait_vm<8>();  // A of the next stage: only its B and this A are younger
+      } else {
+        read_a(1);
+        if (!BKM) issue_b(0);
+        wait_vm<BKM ? 8 : 10>();  // A0 of the next stage
+      }
       turn();
       mma(1, 1);
       end();
 
 #pragma unroll
-      for (int q = 0; q < 4; ++q) la[q >> 1][q & 1] ^= 32768u;
+      for (int q = 0; q < (AKM ? 4 : 2); ++q) la[q >> 1][q & 1] ^= 32768u;
       if (kt + 1 < nk) read_a(0);
       if constexpr (BKM) {
         issue_bk();
@@ -379,13 +438,18 @@ MOE_DEVICE void pp_tiles(u32x4_t *lds, int64_t lda, int64_t ldb, int nk, int cou
       turn();
       mma(1, 0);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) lb[q >> 1][q & 1] ^= 32768u;
+      for (int q = 0; q < (BKM ? 4 : 2); ++q) lb[q >> 1][q & 1] ^= 32768u;
       end();
     }
     if (grp == 0) barrier();
     done(acc);
   }
   wait_vm<0>();  // no load may land in the next workgroup's LDS
+}
+
+template <bool F16, bool BKM, typename Get, typename Done>
+MOE_DEVICE void pp_tiles(u32x4_t *lds, int64_t lda, int64_t ldb, int nk, int count, Get get, Done done) {
+  pp_tiles<F16, false, BKM>(lds, lda, ldb, nk, count, get, done, 0);
 }
 
 }  // namespace moe

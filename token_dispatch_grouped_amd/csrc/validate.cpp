@@ -225,19 +225,23 @@ static int64_t wgrad_tiles(int tile, int d, int F) {
   return ceil_div(2 * (int64_t)F, tile) * ceil_div(d, tile) + ceil_div(d, tile) * ceil_div(F, tile);
 }
 
-// `tiles(tile)`: tiles of all products; elems: their elements.
+// Times of the large tiles in us: of a stage with one round of workgroups and
+// with more, beside the stages (the launch, the start, the end), and the most
+// TFLOP/s. `tiles(tile)`: tiles of all products; elems: their elements.
+struct WgradRate {
+  double stage, crowded, fixed, tflops;
+};
 template <typename Tiles>
-static FfnWgrad wgrad_plan(int64_t T, double elems, Tiles count) {
-  // Time of n slices in us: a fixed 4, then rounds of workgroups, each a run of
-  // stages of 64 tokens. 256 x 256 tiles run one a CU, 1.35 us a stage while
-  // every workgroup has a CU from the start, 1.6 beyond; 128 x 128 tiles two a
-  // CU, 0.65 us a stage alone on one, 1.05 beyond; never more than 1060 TFLOP/s
-  // in all. A second launch writes and reads n times the gradients at 4 TB/s.
-  // Measured (tile, slices: us): d = 2048, F = 1408 at 2000 tokens 256, 1: 51,
+static FfnWgrad wgrad_plan(int64_t T, double elems, const WgradRate &large, Tiles count) {
+  // Time of n slices in us: a fixed part, then rounds of workgroups, each a run
+  // of stages of 64 tokens. 256 x 256 tiles run one a CU (`large`); 128 x 128
+  // tiles two a CU, 0.65 us a stage alone on one, 1.05 beyond, at most 1060
+  // TFLOP/s in all. A second launch writes and reads n times the gradients at 4
+  // TB/s. Measured for the dense block (tile, slices: us): d = 2048, F = 1408 at 2000 tokens 256, 1: 51,
   // 256, 3: 75, 128, 1: 59; at 7001 256, 1: 145, 256, 3: 149, 128, 2: 166; at
   // 32768 256, 1: 694, 256, 3: 589; d = 512, F = 320 at 3000 256, 11: 27, 128,
   // 1: 33, 128, 4: 18.5; d = 1088, F = 576 at 700 256, 1: 23, 128, 1: 12.
-  const double bytes = 4.0 * elems, least = 2.0 * (double)T * elems / 1.06e9;
+  const double bytes = 4.0 * elems;
   FfnWgrad w{256, 0, 0, 1};
   double best_us = 0.0;
   int64_t best = 1;
@@ -249,8 +253,9 @@ static FfnWgrad wgrad_plan(int64_t T, double elems, Tiles count) {
     if (most > w.most) w.most = (int)most;
     for (int64_t n = 1; n <= most; ++n) {
       const int64_t rounds = ceil_div(tiles * n, tile == 256 ? 256 : 512), stages = ceil_div(ceil_div(T, n), 64);
-      const double stage = tile == 256 ? (rounds > 1 ? 1.6 : 1.35) : (tiles * n > 256 ? 1.05 : 0.65);
-      double us = 4.0 + (double)(rounds * stages) * stage;
+      const double stage = tile == 256 ? (rounds > 1 ? large.crowded : large.stage) : (tiles * n > 256 ? 1.05 : 0.65);
+      const double least = 2.0 * (double)T * elems / (1e6 * (tile == 256 ? large.tflops : 1060.0));
+      double us = (tile == 256 ? large.fixed : 4.0) + (double)(rounds * stages) * stage;
       if (us < least) us = least;
       if (n > 1) us += 5.0 + (double)n * bytes / 4e6;
       if ((tile == 256 && n == 1) || us < best_us) {
@@ -265,8 +270,9 @@ static FfnWgrad wgrad_plan(int64_t T, double elems, Tiles count) {
   return w;
 }
 
+// 1.35 us a stage while every workgroup has a CU from the start, 1.6 beyond.
 FfnWgrad ffn_wgrad_plan(int64_t T, int d, int F) {
-  return wgrad_plan(T, 3.0 * d * F, [&](int tile) { return wgrad_tiles(tile, d, F); });
+  return wgrad_plan(T, 3.0 * d * F, {1.35, 1.6, 4.0, 1060.0}, [&](int tile) { return wgrad_tiles(tile, d, F); });
 }
 
 FfnWorkspace ffn_workspace(const moe_ffn_shape &s) {
@@ -317,14 +323,16 @@ moe_status validate_linear(const moe_linear_shape *s, std::string *why) {
 static int64_t linear_tiles(int tile, int K, int N) { return ceil_div(N, tile) * ceil_div(K, tile); }
 
 FfnWgrad linear_wgrad_plan(int64_t T, int K, int N) {
-  return wgrad_plan(T, (double)K * N, [&](int tile) { return linear_tiles(tile, K, N); });
+  return wgrad_plan(T, (double)K * N, {1.37, 1.37, 8.0, 1500.0}, [&](int tile) { return linear_tiles(tile, K, N); });
 }
 
 LinearWorkspace linear_workspace(const moe_linear_shape &s) {
   LinearWorkspace w{};
   if (s.T > 0 && linear_tiles(256, s.K, s.N) * 2 <= kWgradUnits)
     w.dw = align256((size_t)linear_wgrad_plan(s.T, s.K, s.N).most * (size_t)s.K * (size_t)s.N * 4);
-  w.db = align256((size_t)linear_db_slices(s.T) * (size_t)s.N * 4);
+  // of db: by the slices of the large tiles or of a pass of its own
+  const size_t slices = (size_t)std::max(linear_db_slices(s.T), s.T > 0 ? linear_wgrad_plan(s.T, s.K, s.N).most : 0);
+  w.db = align256(slices * (size_t)s.N * 4);
   w.total = w.dw + w.db;
   return w;
 }
