@@ -33,56 +33,60 @@ struct OrthIo {
 
 enum { SRC_F32 = 0, SRC_BF16 = 1, SRC_MUON = 2 };
 
-// U at 4 consecutive elements from `e` on (of the whole batch), `n` of them
-// there; vec: they are one aligned vector.
+// The inputs of U at 4 consecutive elements from `e` on (of the whole batch),
+// `n` of them there (at least one); vec: they are one aligned vector.
 template <int SRC>
-MOE_DEVICE void orth_u(const OrthIo &p, int64_t e, int n, bool vec, float (&u)[4], float (&buf)[4]) {
-  float g[4] = {0.f, 0.f, 0.f, 0.f};
-  if constexpr (SRC == SRC_BF16) {
-    const bf16_t *x = (const bf16_t *)p.x + e;
-    if (vec) {
-      const uint2 v = *reinterpret_cast<const uint2 *>(x);
-      g[0] = __uint_as_float(v.x << 16);
-      g[1] = __uint_as_float(v.x & 0xffff0000u);
-      g[2] = __uint_as_float(v.y << 16);
-      g[3] = __uint_as_float(v.y & 0xffff0000u);
-    } else {
+struct OrthIn {
+  float g[4], m[4];
+  MOE_DEVICE void load(const OrthIo &p, int64_t e, int n, bool vec) {
+    if constexpr (SRC == SRC_BF16) {
+      const bf16_t *x = (const bf16_t *)p.x + e;
+      if (vec) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(x);
+        g[0] = __uint_as_float(v.x << 16);
+        g[1] = __uint_as_float(v.x & 0xffff0000u);
+        g[2] = __uint_as_float(v.y << 16);
+        g[3] = __uint_as_float(v.y & 0xffff0000u);
+      } else {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (q < n) g[q] = bf2f(x[q]);
+        for (int q = 0; q < 4; ++q) g[q] = q < n ? bf2f(x[q]) : 0.f;
+      }
+      return;
     }
-  } else {
     const float *x = SRC == SRC_F32 ? (const float *)p.x + e : p.grad + e;
-    float m[4] = {0.f, 0.f, 0.f, 0.f};
     if (vec) {
       const f32x4_t v = *reinterpret_cast<const f32x4_t *>(x);
 #pragma unroll
       for (int q = 0; q < 4; ++q) g[q] = v[q];
-      if (SRC == SRC_MUON) {
+      if constexpr (SRC == SRC_MUON) {
         const f32x4_t w = *reinterpret_cast<const f32x4_t *>(p.mom + e);
 #pragma unroll
         for (int q = 0; q < 4; ++q) m[q] = w[q];
       }
     } else {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (q < n) {
-          g[q] = x[q];
-          if (SRC == SRC_MUON) m[q] = p.mom[e + q];
-        }
-    }
-    if (SRC == SRC_MUON) {
-#pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const float gs = g[q] * p.grad_scale;
-        buf[q] = fmaf(p.mu, m[q], gs);
-        g[q] = p.nesterov ? fmaf(p.mu, buf[q], gs) : buf[q];
+        g[q] = q < n ? x[q] : 0.f;
+        if (SRC == SRC_MUON) m[q] = q < n ? p.mom[e + q] : 0.f;
       }
     }
   }
+  MOE_DEVICE void zero() {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) u[q] = g[q];
-}
+    for (int q = 0; q < 4; ++q) g[q] = m[q] = 0.f;
+  }
+  // g becomes U, m the new momentum
+  MOE_DEVICE void combine(const OrthIo &p) {
+    if constexpr (SRC == SRC_MUON) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float gs = g[q] * p.grad_scale;
+        m[q] = fmaf(p.mu, m[q], gs);
+        g[q] = p.nesterov ? fmaf(p.mu, m[q], gs) : m[q];
+      }
+    }
+  }
+};
 
 MOE_DEVICE double wave_sum64(double v) {
 #pragma unroll
@@ -101,13 +105,35 @@ __global__ __launch_bounds__(kOrthThreads) void orth_norm_kernel(OrthIo p) {
   const int64_t first = part_id * chunk, last = first + chunk < n ? first + chunk : n;
   const bool aligned = (n & 3) == 0;  // every matrix starts on a vector
   double sum = 0.0;
-#pragma unroll 4
-  for (int64_t i = first + threadIdx.x * 4; i < last; i += kOrthThreads * 4) {
-    float u[4], b[4];
-    const int left = (int)(last - i < 4 ? last - i : 4);
-    orth_u<SRC>(p, mat * n + i, left, aligned && left == 4, u, b);
+  auto add = [&](OrthIn<SRC> &in) {
+    in.combine(p);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) sum = fma((double)u[q], (double)u[q], sum);
+    for (int q = 0; q < 4; ++q) sum = fma((double)in.g[q], (double)in.g[q], sum);
+  };
+  const int64_t at = mat * n + threadIdx.x * 4;
+  constexpr int kRow = kOrthThreads * 4;
+  int64_t i = first;
+  if (aligned) {  // whole rows of vectors, the loads of four in flight together
+    for (; i + 4 * kRow <= last; i += 4 * kRow) {
+      OrthIn<SRC> in[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) in[k].load(p, at + i + k * kRow, 4, true);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) add(in[k]);
+    }
+  }
+  // the rest, and matrices that start on no vector
+  for (; i < last; i += 4 * kRow) {
+    OrthIn<SRC> in[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t e = i + k * kRow + threadIdx.x * 4;
+      const int left = (int)(last - e < 4 ? last - e : 4);
+      in[k].zero();
+      if (left > 0) in[k].load(p, mat * n + e, left, aligned && left == 4);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) add(in[k]);
   }
   sum = wave_sum64(sum);
   if ((threadIdx.x & (kWave - 1)) == 0) part[threadIdx.x / kWave] = sum;
@@ -125,13 +151,14 @@ __global__ __launch_bounds__(kOrthThreads) void orth_prep_kernel(OrthIo p) {
   const int t = (int)(blockIdx.x - mat * rt * ct);
   const int r0 = t / ct * 64, c0 = t % ct * 64;
   const int lane = threadIdx.x & (kWave - 1);
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int64_t base = mat * p.rows * p.cols;
+  const bool vec = (p.cols & 3) == 0;
   double sum = 0.0;
   for (int i = lane; i < p.parts; i += kWave) sum += p.partial[mat * p.parts + i];
   sum = wave_sum64(sum);
   // a matrix that holds an infinity or a NaN becomes NaN altogether
   const double scale = sum < __builtin_huge_val() ? (double)kOrthScale / (sqrt(sum) + (double)p.eps) : __builtin_nan("");
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int64_t base = mat * p.rows * p.cols;
   auto put = [&](int64_t o, const float (&v)[4]) {
     *reinterpret_cast<uint2 *>(p.hi + mat * p.stride_x + o) = make_uint2(pack_h2(v[0], v[1]), pack_h2(v[2], v[3]));
     if (!p.lo) return;
@@ -140,7 +167,6 @@ __global__ __launch_bounds__(kOrthThreads) void orth_prep_kernel(OrthIo p) {
     for (int q = 0; q < 4; ++q) l[q] = v[q] - h2f(f2h(v[q]));
     *reinterpret_cast<uint2 *>(p.lo + mat * p.stride_x + o) = make_uint2(pack_h2(l[0], l[1]), pack_h2(l[2], l[3]));
   };
-  const bool vec = (p.cols & 3) == 0;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int r = r0 + ty + 16 * k, c = c0 + tx * 4;
@@ -148,12 +174,14 @@ __global__ __launch_bounds__(kOrthThreads) void orth_prep_kernel(OrthIo p) {
     float v[4] = {0.f, 0.f, 0.f, 0.f};
     if (left > 0) {
       const int64_t e = base + (int64_t)r * p.cols + c;
-      float u[4], buf[4];
-      orth_u<SRC>(p, e, left, vec, u, buf);
+      OrthIn<SRC> in;
+      in.load(p, e, left, vec);
+      in.combine(p);
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        if (q < left) v[q] = (float)((double)u[q] * scale);
+        if (q < left) v[q] = (float)((double)in.g[q] * scale);
       if constexpr (SRC == SRC_MUON) {
+        const float (&buf)[4] = in.m;
         if (vec) {
           *reinterpret_cast<f32x4_t *>(p.mom + e) = f32x4_t{buf[0], buf[1], buf[2], buf[3]};
           if (p.zero_grad) *reinterpret_cast<f32x4_t *>(p.grad + e) = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -210,16 +238,16 @@ static hipError_t sym_product(const OrthTileParams &p, int64_t batch, bool gram,
   const OrthTile t = choose(p.M, p.N, batch, true);
   if (gram) {
     switch (t) {
-      case kSmall: return run_orth_tile<64, 64, 32, 64, 4, 2, ORTH_GRAM>(p, batch, s);
-      case kPair: return run_orth_tile<128, 128, 64, 64, 2, 2, ORTH_GRAM>(p, batch, s);
-      case kSquare: return run_orth_tile<128, 128, 64, 64, 1, 2, ORTH_GRAM>(p, batch, s);
+      case kSmall: return run_orth_tile<64, 64, 16, 64, 2, 4, ORTH_GRAM>(p, batch, s);
+      case kPair: return run_orth_tile<128, 128, 32, 64, 1, 4, ORTH_GRAM>(p, batch, s);
+      case kSquare: return run_orth_tile<128, 128, 32, 64, 1, 2, ORTH_GRAM>(p, batch, s);
       default: return run_orth_wide<ORTH_GRAM>(p, batch, s);
     }
   }
   switch (t) {
-    case kSmall: return run_orth_tile<64, 64, 32, 64, 4, 2, ORTH_POLY>(p, batch, s);
-    case kPair: return run_orth_tile<128, 128, 64, 64, 2, 2, ORTH_POLY>(p, batch, s);
-    case kSquare: return run_orth_tile<128, 128, 64, 64, 1, 2, ORTH_POLY>(p, batch, s);
+    case kSmall: return run_orth_tile<64, 64, 16, 64, 2, 4, ORTH_POLY>(p, batch, s);
+    case kPair: return run_orth_tile<128, 128, 32, 64, 1, 4, ORTH_POLY>(p, batch, s);
+    case kSquare: return run_orth_tile<128, 128, 32, 64, 1, 2, ORTH_POLY>(p, batch, s);
     default: return run_orth_wide<ORTH_POLY>(p, batch, s);
   }
 }
@@ -227,9 +255,9 @@ static hipError_t sym_product(const OrthTileParams &p, int64_t batch, bool gram,
 template <int MODE>
 static hipError_t step_tiles(const OrthTileParams &p, int64_t batch, hipStream_t s) {
   switch (choose(p.M, p.N, batch, false)) {
-    case kSmall: return run_orth_tile<64, 128, 32, 64, 2, 2, MODE>(p, batch, s);
-    case kPair: return run_orth_tile<128, 128, 64, 64, 2, 2, MODE>(p, batch, s);
-    case kSquare: return run_orth_tile<128, 128, 64, 64, 1, 2, MODE>(p, batch, s);
+    case kSmall: return run_orth_tile<64, 128, 16, 64, 1, 4, MODE>(p, batch, s);
+    case kPair: return run_orth_tile<128, 128, 32, 64, 1, 4, MODE>(p, batch, s);
+    case kSquare: return run_orth_tile<128, 128, 32, 64, 1, 2, MODE>(p, batch, s);
     default: return run_orth_wide<MODE>(p, batch, s);
   }
 }

@@ -112,7 +112,7 @@ MOE_DEVICE void orth_quad_transpose(float (&v)[4], int lane) {
 }
 
 // Epilogue of a wavefront's sub-tile of FM x 4 blocks of 16 x 16, from row m0 +
-// row0 and column col0 on; m_valid: rows of the tile that exist, mirror: store
+// row0 and column col0 on (FM 1: 16 rows); m_valid: rows of the tile that exist, mirror: store
 // the transpose as well.
 //
 // Global memory is read and written in whole rows of a block of 32 rows, which the
@@ -123,6 +123,8 @@ MOE_DEVICE void orth_quad_transpose(float (&v)[4], int lane) {
 template <int FM, int MODE>
 MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x4_t (&acc)[FM][4], char *scr, int mat, int m0, int m_valid,
                               int row0, int col0, bool mirror) {
+  constexpr int H = FM > 1 ? 2 : 1, RB = (FM + 1) / 2;  // blocks of 16 rows in a row block (of 32, or 16); row blocks
+  static_assert(FM == 1 || FM % 2 == 0, "whole row blocks");
   constexpr bool STEP = orth_step(MODE);
   constexpr bool LAST = MODE == ORTH_LAST || MODE == ORTH_LAST_MUON;
   int lane = threadIdx.x & 63;
@@ -168,17 +170,17 @@ MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x4_t (&acc)[FM][4], ch
   const int orow0 = out.tall ? col0 : r0, ocol0 = out.tall ? r0 : col0;
   auto out_at = [&](int i, int j, int k, int &left) -> int64_t {
     const int orow = orow0 + (out.tall ? j : i) * 32 + k * 8 + rr, ocol = ocol0 + (out.tall ? i : j) * 32 + rc * 4;
-    left = orow < out.rows ? out.cols - ocol : 0;
+    left = orow < out.rows && (H > 1 || (out.tall ? rc * 4 : k * 8 + rr) < 16) ? out.cols - ocol : 0;
     return obase + (left > 0 ? (int64_t)orow * out.cols + ocol : 0);
   };
   auto load_rows = [&](int i) {
     if constexpr (MODE != ORTH_GRAM) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) gh[i & 1][k] = src.load(off(i, k));
+      for (int k = 0; k < 2 * H; ++k) gh[i & 1][k] = src.load(off(i, k));
     }
     if constexpr (MODE == ORTH_STEP) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) gl[i & 1][k] = srclo.load<2>(off(i, k));  // zeros where there is none
+      for (int k = 0; k < 2 * H; ++k) gl[i & 1][k] = srclo.load<2>(off(i, k));  // zeros where there is none
     }
   };
   auto load_param = [&](int i, int j) {
@@ -195,20 +197,20 @@ MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x4_t (&acc)[FM][4], ch
   load_param(0, 0);
   load_param(0, 1);
 #pragma unroll
-  for (int i = 0; i < FM / 2; ++i) {
+  for (int i = 0; i < RB; ++i) {
     if (i * 32 >= rows) break;
     const int br = r0 + i * 32;
-    if (i + 1 < FM / 2) load_rows(i + 1);
+    if (i + 1 < RB) load_rows(i + 1);
     float dr[2] = {0.f, 0.f};
     if constexpr (MODE != ORTH_GRAM) {
       dr[0] = diag[br + l16];
-      dr[1] = diag[br + 16 + l16];
+      if (H > 1) dr[1] = diag[br + 16 + l16];
     }
     __builtin_amdgcn_sched_barrier(0);
     // acc -> the new values, in place
     auto acc_at = [&](int h, int j) -> f32x4_t & { return acc[i * 2 + h][j]; };
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < H; ++h)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -220,12 +222,12 @@ MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x4_t (&acc)[FM][4], ch
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc_at(h, j)[e] = fmaf(dr[h], v[e], acc_at(h, j)[e]);
       };
-      blk.in_order(gh[i & 1], add);
+      blk.template in_order<H>(gh[i & 1], add);
       if constexpr (MODE == ORTH_STEP) {
-        if (low) blk.in_order(gl[i & 1], add);
+        if (low) blk.template in_order<H>(gl[i & 1], add);
       }
     } else if constexpr (MODE == ORTH_POLY) {
-      blk.in_order(gh[i & 1], [&](int h, int j, const uint2 &g) {
+      blk.template in_order<H>(gh[i & 1], [&](int h, int j, const uint2 &g) {
         const f32x4_t v = unpack(g);
         const f32x4_t dc = *reinterpret_cast<const f32x4_t *>(diag + col(j));
 #pragma unroll
@@ -235,9 +237,9 @@ MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x4_t (&acc)[FM][4], ch
       });
     }
     if constexpr (!STEP) {
-      if (br < col0 + 64 && col0 < br + 32) {  // a block on the diagonal
+      if (br < col0 + 64 && col0 < br + 16 * H) {  // a block on the diagonal
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < H; ++h)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -252,11 +254,11 @@ MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x4_t (&acc)[FM][4], ch
               }
       }
       if (mirror) {
-        // transposed: 64 columns of 32 rows (64 bytes) in scr, 16-byte chunks
-        // swizzled by bits 1 and 2 of the column
+        // transposed: 64 columns of 32 (16) rows in scr, 64 bytes each, 16-byte
+        // chunks swizzled by bits 1 and 2 of the column
         auto at = [&](int c, int ch) { return scr + c * 64 + ((ch ^ ((c >> 1) & 3)) * 16); };
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < H; ++h)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint2 d = pack(acc_at(h, j));
@@ -265,8 +267,8 @@ MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x4_t (&acc)[FM][4], ch
             *reinterpret_cast<uint2 *>(at(j * 16 + 4 * l4 + (lane & 3), r4 >> 1) + (r4 & 1) * 8) = d;
           }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int c = k * 16 + (lane >> 2), ch = lane & 3;
+        for (int k = 0; k < 2 * H; ++k) {
+          const int c = k * (32 / H) + (lane / (2 * H)), ch = lane % (2 * H);
           const u32x4_t v = *reinterpret_cast<const u32x4_t *>(at(c, ch));
           st16(p.C + mat * p.strideC + (int64_t)(col0 + c) * p.ldc + br + ch * 8, v);
         }
@@ -274,13 +276,13 @@ MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x4_t (&acc)[FM][4], ch
     }
     if constexpr (!LAST) {
       auto rows_out = [&](const TileRows &to) {
-        blk.rows_out([&](int h, int j) { return pack(acc_at(h, j)); },
+        blk.template rows_out<H>([&](int h, int j) { return pack(acc_at(h, j)); },
                      [&](int k, const u32x4_t &v) { to.store<2>(off(i, k), v); });
       };
       rows_out(dst);
       if (STEP && p.Clo) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < H; ++h)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const f32x4_t hi = unpack(pack(acc_at(h, j)));
@@ -293,7 +295,7 @@ MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x4_t (&acc)[FM][4], ch
 #pragma unroll
       for (int j2 = 0; j2 < 2; ++j2) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < H; ++h)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             float v[4];
@@ -333,7 +335,7 @@ MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x4_t (&acc)[FM][4], ch
             }
           }
         }
-        if (i + 1 < FM / 2) load_param(i + 1, j2);
+        if (i + 1 < RB) load_param(i + 1, j2);
       }
     }
   }
@@ -421,6 +423,18 @@ __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void orth_tile_
   OpB opb;
   opa.init(Ab, p.lda, m_valid, wave, lane, [&](int r) { return r < m_valid ? r : m_valid - 1; });
   opb.init(Bb, p.ldb, n_valid, wave, lane, [&](int r) { return BKM || r < n_valid ? r : n_valid - 1; });
+  // the chunks' order is pingpong.h's, whose fragments are these
+  auto reorder = [&](auto &op, int valid, bool km) {
+    using Op = std::remove_reference_t<decltype(op)>;
+#pragma unroll
+    for (int i = 0; i < Op::NDMA; ++i) {
+      const int r = (i * NW + wave) * Op::RPI + lane / Op::CPR, phys = lane % Op::CPR;
+      if (km) op.ptr[i] += min((phys ^ pp_swz_km(r)) * 8, valid - 8) - min((phys ^ (4 * (r & 3))) * 8, valid - 8);
+      else op.ptr[i] += ((phys ^ pp_swz(r)) - (phys ^ swz(r))) * 8;
+    }
+  };
+  reorder(opa, m_valid, false);
+  reorder(opb, n_valid, BKM);
 
   const uint32_t lds0 = (uint32_t)(uintptr_t)ldsc;
   auto issue = [&](int kt) {  // the group's stage kt
@@ -432,13 +446,12 @@ __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void orth_tile_
   // 8 consecutive k of row lane & 15 from 8 (lane >> 4) on
   auto rows16 = [&](const char *tile, int rb, int ks) {
     const int r = rb + (lane & 15), c = ks * 4 + (lane >> 4);
-    return __builtin_bit_cast(f16x8_t, *reinterpret_cast<const u32x4_t *>(tile + (r * 8 + (c ^ swz(r))) * 16));
+    return __builtin_bit_cast(f16x8_t, *reinterpret_cast<const u32x4_t *>(tile + (r * 8 + (c ^ pp_swz(r))) * 16));
   };
-  auto cols16 = [&](const char *tile, int cb, int ks) {  // of column lane & 15, k-major (Operand's layout)
+  auto cols16 = [&](const char *tile, int cb, int ks) {  // of column lane & 15, k-major
     typedef __attribute__((__vector_size__(8 * sizeof(short)))) short i16x8_t;
-    const int b = lane & 15, col = cb + 4 * (b & 3);
-    const char *a = tile + (ks * 32 + 8 * (lane >> 4) + (b >> 2)) * OpB::ROWB + ((col >> 3) ^ (4 * (b >> 2))) * 16 +
-                    ((col >> 2) & 1) * 8;
+    const int b = lane & 15, col = cb + 4 * (b & 3), k_lo = 8 * (lane >> 4) + (b >> 2);
+    const char *a = tile + (ks * 32 + k_lo) * OpB::ROWB + ((col >> 3) ^ pp_swz_km(k_lo)) * 16 + ((col >> 2) & 1) * 8;
     const i16x4_t lo = lds_read_tr16(a), hi = lds_read_tr16(a + 4 * OpB::ROWB);
     const i16x8_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
     return __builtin_bit_cast(f16x8_t, v);
@@ -466,10 +479,17 @@ __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void orth_tile_
   };
   // wait until at most `younger` whole stages are still in flight
   auto wait_stages = [&](int younger) {
-    if (STAGES > 3 && younger >= 3) wait_vm<3 * PER_STAGE>();
-    else if (STAGES > 2 && younger >= 2) wait_vm<2 * PER_STAGE>();
-    else if (younger >= 1) wait_vm<PER_STAGE>();
-    else wait_vm<0>();
+    static_assert(STAGES <= 8, "one wait for each number of younger stages");
+    switch (min(younger, STAGES - 1)) {
+      case 7: return wait_vm<(STAGES > 7 ? 7 : 0) * PER_STAGE>();
+      case 6: return wait_vm<(STAGES > 6 ? 6 : 0) * PER_STAGE>();
+      case 5: return wait_vm<(STAGES > 5 ? 5 : 0) * PER_STAGE>();
+      case 4: return wait_vm<(STAGES > 4 ? 4 : 0) * PER_STAGE>();
+      case 3: return wait_vm<(STAGES > 3 ? 3 : 0) * PER_STAGE>();
+      case 2: return wait_vm<(STAGES > 2 ? 2 : 0) * PER_STAGE>();
+      case 1: return wait_vm<PER_STAGE>();
+      default: return wait_vm<0>();
+    }
   };
   for (int st = 0; st < STAGES; ++st)
     if (st < nk) issue(st);
@@ -511,9 +531,9 @@ __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void orth_tile_
     if (mine) mma(FM - 1, 1, (KS - 1) & 1);
   }
 
+  __syncthreads();  // every ring is done with
   if constexpr (KG > 1) {
     // the groups' sums, added in the order of the groups by the first one
-    __syncthreads();  // every ring is done with
     f32x4_t *sum = reinterpret_cast<f32x4_t *>(lds);
     auto at = [&](int g, int f) -> f32x4_t & { return sum[(g * FM * FN + f) * NT + tid]; };
     if (kg > 0) {
@@ -531,9 +551,7 @@ __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void orth_tile_
         for (int e = 0; e < 4; ++e) acc[f / FN][f % FN][e] += v[e];
       }
   }
-
-  // scratch: behind the groups' sums, in rings that every wavefront is done with
-  if (KG == 1) __syncthreads();
+  // scratch: behind the groups' sums
   char *scr = reinterpret_cast<char *>(lds) + (KG - 1) * BM * BN * 4 + wave * RowBlock::kBytes;
   orth_epilogue<FM, MODE>(p, acc, scr, mat, m0, m_valid, wm * WM, n0 + wn * WN, mt != nt);
 }

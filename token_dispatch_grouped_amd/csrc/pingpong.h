@@ -68,6 +68,9 @@ struct PpTile {
 // with fragments of 16 rows each group finds every bank once. Counted: no
 // conflict cycles, one for each active one with (r ^ r / 8) % 8.
 MOE_DEVICE int pp_swz(int r) { return (r >> 1) & 7; }
+// And of a k-major row r of 128 columns or more at c ^ pp_swz_km(r), so that the
+// 16-lane groups of a transposing read, which are 8 rows apart, use different banks.
+MOE_DEVICE int pp_swz_km(int r) { return 4 * (r & 3) ^ 2 * ((r >> 3) & 1); }
 
 // MFMA of 16 x 16 x 32 with swapped operands: a lane holds row (lane & 15) of the
 // block, 4 consecutive columns from 4 (lane >> 4) on; a fragment, 8 consecutive
@@ -118,25 +121,26 @@ struct RowBlock {
     const int r = i * 16 + l16;
     return *reinterpret_cast<uint2 *>(scr + r * 128 + (((j * 2 + (l4 >> 1)) ^ (r & 7)) * 16) + (l4 & 1) * 8);
   }
-  // rows g[k] = row k * 8 + rr, chunk rc to f(i, j, the 4 values of block (i, j))
-  template <typename F>
+  // rows g[k] = row k * 8 + rr, chunk rc to f(i, j, the 4 values of block (i, j));
+  // H: row blocks of 16, 2 or 1
+  template <int H = 2, typename F>
   MOE_DEVICE void in_order(const u32x4_t (&g)[4], F f) const {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) at16(k * 8 + rr, rc) = g[k];
+    for (int k = 0; k < 2 * H; ++k) at16(k * 8 + rr, rc) = g[k];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < H; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) f(i, j, at8(i, j));
   }
   // f(i, j) of every block to rows, put(k, chunk rc of row k * 8 + rr)
-  template <typename F, typename Put>
+  template <int H = 2, typename F, typename Put>
   MOE_DEVICE void rows_out(F f, Put put) const {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < H; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) at8(i, j) = f(i, j);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) put(k, at16(k * 8 + rr, rc));
+    for (int k = 0; k < 2 * H; ++k) put(k, at16(k * 8 + rr, rc));
   }
 };
 
@@ -201,13 +205,11 @@ MOE_DEVICE void pp_tiles(u32x4_t *lds, int64_t lda, int64_t ldb, int nk, int cou
     la[0][ks] = a + (uint32_t)grp * 16384u;
     lb[0][ks] = a + 65536u + (uint32_t)wn * 8192u;
   }
-  // k-major: of the 16 columns from `first` on. Chunk c of k row r sits at c ^ 4
-  // (r % 4) ^ 2 (r / 8 % 2), so that the 16-lane groups of a transposing read,
-  // which are 8 rows apart, use different banks.
+  // k-major: of the 16 columns from `first` on
   auto km_addr = [&](int first) {
     const int col = first + 4 * (l16 & 3);
     const int k_lo = 8 * l4 + (l16 >> 2);
-    const int c = (col >> 3) ^ (4 * (l16 >> 2)) ^ (2 * (l4 & 1));
+    const int c = (col >> 3) ^ pp_swz_km(k_lo);
     return (uint32_t)(k_lo * 512 + c * 16 + ((col >> 2) & 1) * 8);
   };
   if constexpr (BKM) {  // lb[j][x]: column block 2j + x
@@ -267,7 +269,7 @@ MOE_DEVICE void pp_tiles(u32x4_t *lds, int64_t lda, int64_t ldb, int nk, int cou
   // 16 + that one has the same swizzle (bit 3 of it is wave / 4)
   auto km_off = [&](int64_t ld, int valid) {
     const int r = wave * 2 + (lane >> 5);
-    const int col = ((lane & 31) ^ (4 * (r & 3)) ^ (2 * (wave >> 2))) * 8;
+    const int col = ((lane & 31) ^ pp_swz_km(r)) * 8;
     return col < valid ? (uint32_t)(((int64_t)r * ld + col) * 2) : kPpOutside;
   };
   auto aim = [&](const PpTile &t) {
