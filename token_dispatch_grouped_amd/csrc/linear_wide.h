@@ -136,6 +136,7 @@ __global__ __launch_bounds__(kPpThreads, 2) void linear_wide_kernel(FfnTileParam
   char *scr = reinterpret_cast<char *>(lds) + kPpLdsBytes + wave * RowBlock::kBytes;
   auto done = [&](PpAcc &acc) {
     const int m0 = put.mt * kPpTile + (wave >> 2) * 128;
+    const FfnTileParams &p = late_args<FfnTileParams>();
     linear_epilogue<DX, ADD, ACT>(p, acc, scr, m0, min(128, p.M - m0), put.nt * kPpTile + (wave & 3) * 64);
     put.step(p.m_tiles, p.n_tiles, step);
   };

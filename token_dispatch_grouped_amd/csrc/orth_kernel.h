@@ -595,6 +595,7 @@ __global__ __launch_bounds__(kPpThreads, 2) void orth_wide_kernel(OrthTileParams
   char *scr = reinterpret_cast<char *>(lds) + kPpLdsBytes + wave * RowBlock::kBytes;
   auto done = [&](PpAcc &acc) {
     const int m0 = put.mt * kPpTile;
+    const OrthTileParams &p = late_args<OrthTileParams>();
     orth_epilogue<8, MODE>(p, acc, scr, put.mat, m0, min(kPpTile, p.M - m0), (wave >> 2) * 128,
                               put.nt * kPpTile + (wave & 3) * 64, put.mt != put.nt);
     put.step(p, step);

@@ -84,6 +84,16 @@ MOE_DEVICE f32x4_t mfma16(f16x8_t b, f16x8_t a, f32x4_t c) {
 // Accumulators of a wavefront's 128 x 64: [row block][column block].
 typedef f32x4_t PpAcc[8][4];
 
+// The kernel's one argument, to be read where it is used: an epilogue that names
+// the argument itself holds dozens of scalar registers through the main loop.
+template <typename P>
+MOE_DEVICE const P &late_args() {
+  const __attribute__((address_space(4))) void *k =
+      (const __attribute__((address_space(4))) void *)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(k));
+  return *(const P *)k;
+}
+
 // Rows of a wavefront's part of a tile in global memory, 32-bit byte offsets from
 // its first element. Rows past the last read zeros and are not written, by the
 // buffer's range check. aux 2: non-temporal.
