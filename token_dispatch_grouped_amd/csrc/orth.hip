@@ -141,19 +141,34 @@ __global__ __launch_bounds__(kOrthThreads) void orth_norm_kernel(OrthIo p) {
   if (threadIdx.x == 0) p.partial[blockIdx.x] = (part[0] + part[1]) + (part[2] + part[3]);
 }
 
-// A 64 x 64 tile of a matrix given; rows and columns past its end are zeros
-// (the padding of X).
-template <int SRC>
+// X0 and the momentum. Rows and columns past the matrix's end are zeros (the
+// padding of X). Where X is the matrix itself a workgroup takes 4096 elements of X
+// on end, where it is the transpose, a 64 x 64 tile, turned in LDS.
+constexpr int kPrepVectors = 4;  // of 4 elements, a thread's
+template <int SRC, bool TALL>
 __global__ __launch_bounds__(kOrthThreads) void orth_prep_kernel(OrthIo p) {
-  __shared__ float tile[64][65];
+  __shared__ float tile[TALL ? 64 : 1][65];
   const int rt = (p.rows + 63) / 64, ct = (p.cols + 63) / 64;
-  const int64_t mat = blockIdx.x / ((int64_t)rt * ct);
-  const int t = (int)(blockIdx.x - mat * rt * ct);
+  const int row_vectors = ct * 16, vectors = rt * 64 * row_vectors;  // of X, padded
+  const int per = TALL ? rt * ct : (vectors + kPrepVectors * kOrthThreads - 1) / (kPrepVectors * kOrthThreads);
+  const int64_t mat = blockIdx.x / per;
+  const int t = (int)(blockIdx.x - mat * per);
   const int r0 = t / ct * 64, c0 = t % ct * 64;
   const int lane = threadIdx.x & (kWave - 1);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int64_t base = mat * p.rows * p.cols;
   const bool vec = (p.cols & 3) == 0;
+  OrthIn<SRC> in[kPrepVectors];
+  int row[kPrepVectors], col[kPrepVectors], left[kPrepVectors];
+#pragma unroll
+  for (int k = 0; k < kPrepVectors; ++k) {
+    const int i = (t * kPrepVectors + k) * kOrthThreads + threadIdx.x;
+    row[k] = TALL ? r0 + ty + 16 * k : i / row_vectors;
+    col[k] = TALL ? c0 + tx * 4 : (i - row[k] * row_vectors) * 4;
+    left[k] = row[k] < p.rows ? min(4, p.cols - col[k]) : 0;
+    in[k].zero();
+    if (left[k] > 0) in[k].load(p, base + (int64_t)row[k] * p.cols + col[k], left[k], vec);
+  }
   double sum = 0.0;
   for (int i = lane; i < p.parts; i += kWave) sum += p.partial[mat * p.parts + i];
   sum = wave_sum64(sum);
@@ -168,48 +183,45 @@ __global__ __launch_bounds__(kOrthThreads) void orth_prep_kernel(OrthIo p) {
     *reinterpret_cast<uint2 *>(p.lo + mat * p.stride_x + o) = make_uint2(pack_h2(l[0], l[1]), pack_h2(l[2], l[3]));
   };
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int r = r0 + ty + 16 * k, c = c0 + tx * 4;
-    const int left = r < p.rows ? min(4, p.cols - c) : 0;
+  for (int k = 0; k < kPrepVectors; ++k) {
     float v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (left > 0) {
-      const int64_t e = base + (int64_t)r * p.cols + c;
-      OrthIn<SRC> in;
-      in.load(p, e, left, vec);
-      in.combine(p);
+    if (left[k] > 0) {
+      const int64_t e = base + (int64_t)row[k] * p.cols + col[k];
+      in[k].combine(p);
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        if (q < left) v[q] = (float)((double)in.g[q] * scale);
+        if (q < left[k]) v[q] = (float)((double)in[k].g[q] * scale);
       if constexpr (SRC == SRC_MUON) {
-        const float (&buf)[4] = in.m;
+        const float (&buf)[4] = in[k].m;
         if (vec) {
           *reinterpret_cast<f32x4_t *>(p.mom + e) = f32x4_t{buf[0], buf[1], buf[2], buf[3]};
           if (p.zero_grad) *reinterpret_cast<f32x4_t *>(p.grad + e) = f32x4_t{0.f, 0.f, 0.f, 0.f};
         } else {
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            if (q < left) {
+            if (q < left[k]) {
               p.mom[e + q] = buf[q];
               if (p.zero_grad) p.grad[e + q] = 0.f;
             }
         }
       }
     }
-    if (!p.tall) {
-      put((int64_t)r * p.ldx + c, v);
-    } else {
+    if constexpr (TALL) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) tile[ty + 16 * k][tx * 4 + q] = v[q];
+    } else if (row[k] < rt * 64) {
+      put((int64_t)row[k] * p.ldx + col[k], v);
     }
   }
-  if (!p.tall) return;
-  __syncthreads();
+  if constexpr (TALL) {
+    __syncthreads();
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    float v[4];
+    for (int k = 0; k < 4; ++k) {
+      float v[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = tile[tx * 4 + q][ty + 16 * k];
-    put((int64_t)(c0 + ty + 16 * k) * p.ldx + r0 + tx * 4, v);
+      for (int q = 0; q < 4; ++q) v[q] = tile[tx * 4 + q][ty + 16 * k];
+      put((int64_t)(c0 + ty + 16 * k) * p.ldx + r0 + tx * 4, v);
+    }
   }
 }
 
@@ -277,8 +289,13 @@ static hipError_t enter(const OrthIo &io, int64_t batch, hipStream_t s) {
     if (err != hipSuccess) return err;
   }
   LaunchScope scope("orth_prep", s);
-  const int64_t blocks = batch * ceil_div(io.rows, 64) * ceil_div(io.cols, 64);
-  orth_prep_kernel<SRC><<<(unsigned)blocks, kOrthThreads, 0, s>>>(io);
+  const int64_t tiles = ceil_div(io.rows, 64) * ceil_div(io.cols, 64);
+  if (io.tall) {
+    orth_prep_kernel<SRC, true><<<(unsigned)(batch * tiles), kOrthThreads, 0, s>>>(io);
+  } else {
+    const int64_t per = ceil_div(tiles * 1024, kPrepVectors * kOrthThreads);
+    orth_prep_kernel<SRC, false><<<(unsigned)(batch * per), kOrthThreads, 0, s>>>(io);
+  }
   return hipGetLastError();
 }
 
