@@ -279,3 +279,28 @@ def test_offsets_past_32_bits():
     yc = y[:, cols].double()
     _near(_h(dw[cols]), _h(yc.t() @ x.double()), _h(T * STEP * (yc.abs().t() @ x.double().abs())), "dw")
     _near(_h(db[cols]), _h(yc.sum(0)), _h(T * STEP * yc.abs().sum(0)), "db")
+
+
+def test_gelu_tail_keeps_its_digits():
+    """gelu and its slope down the tail, where the values are far below any absolute error: 2^-16 of the value (the fit's
+    4e-6 and the exponent's argument, off by 2 half steps of at most 85) and half a step of bf16. The slope Phi + z phi
+    is a difference of up to z^2 times its size, -z phi / (z phi + Phi) >= 1 - 1 / z^2 of the terms."""
+    import torch
+    m = _moe()
+    z = torch.linspace(-12.75, -1.5, 64 * 8, device="cuda").bfloat16().reshape(8, 64)
+    z64 = _h(z)
+    x = torch.zeros(8, 64, device="cuda").bfloat16()
+    one = torch.ones(8, 64, device="cuda").bfloat16()
+    dz = _nan(8, 64)
+    m.moe_linear_dact(m.make_linear_shape(8, 64, 64, act=ACTS.index("gelu")), one, z, dz)
+    want = oracle.act_slope("gelu", z64)
+    phi, cdf = np.exp(-z64 ** 2 / 2) / np.sqrt(2 * np.pi), oracle.act("gelu", z64) / z64
+    _near(_h(dz), want, 2.0 ** -15 * (np.abs(z64) * phi + cdf) + HALF * np.abs(want), "slope")
+    for row in range(8):
+        x[:, 0] = 1.0
+        w = torch.zeros(64, 64, device="cuda").bfloat16()
+        w[:, 0] = z[row]
+        y = _nan(8, 64)
+        m.moe_linear_fwd(m.make_linear_shape(8, 64, 64, act=ACTS.index("gelu")), x, w, None, None, None, y)
+        want = oracle.act("gelu", z64[row])
+        _near(_h(y[3]), want, 1.01 * 2.0 ** -16 * np.abs(want) + HALF * np.abs(want), "gelu")
