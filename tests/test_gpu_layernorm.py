@@ -212,6 +212,38 @@ def test_backward(T, d, bf16):
         assert torch.equal(dw3, dw)
 
 
+@pytest.mark.parametrize("T,d", [(5, 256), (300, 2112), (2100, 512), (2, 16384)])
+def test_backward_of_rows_whose_mean_is_many_times_their_spread(T, d):
+    """As test_backward, but with no term of the size of mean * rstd: r - mean of neighbours in fp32 is off by half a
+    step of itself at most, so n by that, rstd's scaling and the product, 2 steps of n; the means and sums as there."""
+    import torch
+    m = _moe()
+    rng = np.random.default_rng(T + 3 * d)
+    w, dy = _rand(rng, d, bf16=False), _rand(rng, T, d, bf16=False, std=0.3)
+    s = m.make_norm_shape(T, d, m.MOE_DTYPE_F32, EPS, m.MOE_NORM_OVERWRITE_DW)
+    ws = torch.empty(m.moe_layernorm_workspace_size(s), dtype=torch.uint8, device="cuda")
+    for at, sd in ((1e3, 1.0), (-1e5, 1.0), (1e3, 0.05), (0.25 * 2.0 ** 124, 2.0 ** 124)):
+        r = _rand(rng, T, d, bf16=False, mean=at, std=sd)
+        assert np.isfinite(_h(r)).all()
+        mean = np.mean(_h(r), axis=1).astype(np.float32)
+        rstd = (1 / np.sqrt(np.var(_h(r), axis=1) + EPS)).astype(np.float32)
+        dx, dw, db = _nan(T, d), _nan(d), _nan(d)
+        m.moe_layernorm_bwd(s, dy, r, w, torch.from_numpy(mean).cuda(), torch.from_numpy(rstd).cuda(), None, dx, dw, db,
+                            ws, ws.numel())
+        torch.cuda.synchronize()
+        dx64, dw64, db64 = oracle.layernorm_bwd(_h(dy), _h(r), _h(w), mean, rstd)
+        rs = rstd[:, None].astype(np.float64)
+        n = np.abs(_h(r) - mean[:, None]) * rs
+        g = np.abs(_h(dy) * _h(w))
+        c = (d / 64 + 20) / 8
+        terms = rs * (g + c * np.mean(g, axis=1, keepdims=True) + n * c * np.mean(g * n, axis=1, keepdims=True))
+        tiny = 2.0 ** -149 * (2 if sd > 1 else 0)  # dx of rows past 2^120 are subnormal numbers
+        assert np.all(np.abs(_h(dx) - dx64) <= 8 * U * terms + tiny)
+        chain = T / 512 + 1 + 4 + 8 + 64 + 4
+        assert np.all(np.abs(_h(dw) - dw64) <= chain * U * np.sum(np.abs(_h(dy)) * n, axis=0))
+        assert np.all(np.abs(_h(db) - db64) <= chain * U * np.sum(np.abs(_h(dy)), axis=0))
+
+
 def test_gradients_against_differences():
     """fp32, through the forward itself: differences of h = 1e-2 of a loss whose third derivatives are of order 1 are
     off by h^2 of it and by a few steps of y (2^-22) over h."""

@@ -240,8 +240,15 @@ struct LnBwdParams {
   float inv_d;
 };
 
-// n = r * rstd - mean * rstd in one fma: no intermediate passes fp32's range.
-MOE_DEVICE float ln_n(float r, float rstd, float shift) { return fmaf(r, rstd, shift); }
+// n = (r - mean) * rstd as (r / 2 - mean / 2) * 2 rstd: the difference comes first
+// and is rounded once, so that rows whose mean is many times their spread keep
+// the spread's digits (r rstd - mean rstd would be off by a step of mean rstd), and
+// by halves no difference passes fp32's range.
+struct LnN {
+  float half_mean, twice_rstd;
+  MOE_DEVICE LnN(float mean, float rstd) : half_mean(0.5f * mean), twice_rstd(2.0f * rstd) {}
+  MOE_DEVICE float operator()(float r) const { return fmaf(r, 0.5f, -half_mean) * twice_rstd; }
+};
 
 // The workgroups share the rows out evenly; a thread keeps the same columns
 // of every row and holds their two sums in registers, which become one pair of
@@ -294,7 +301,8 @@ __global__ __launch_bounds__(kLnThreads) void layernorm_bwd_kernel(LnBwdParams p
       rv[j] = rn[j];
       ev[j] = en[j];
     }
-    const float rstd = rstd_n, shift = -mean_n * rstd_n;
+    const float rstd = rstd_n;
+    const LnN norm(mean_n, rstd_n);
     if (row + step < p.T) fetch(row + step);
     float sg = 0.f, sn = 0.f;
 #pragma unroll
@@ -307,7 +315,7 @@ __global__ __launch_bounds__(kLnThreads) void layernorm_bwd_kernel(LnBwdParams p
       float a = 0.f, b = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float gn = g[i] * ln_n(r[i], rstd, shift);
+        const float gn = g[i] * norm(r[i]);
         if (c < n) {
           dw[j][i] += gn;
           db[j][i] += g[i];
@@ -334,7 +342,7 @@ __global__ __launch_bounds__(kLnThreads) void layernorm_bwd_kernel(LnBwdParams p
       Elem<T>::unpack(rv[j], r);
       Elem<T>::unpack(wv[j], w);
 #pragma unroll
-      for (int i = 0; i < V; ++i) g[i] = rstd * fmaf(-ln_n(r[i], rstd, shift), mn, fmaf(g[i], w[i], -mg));
+      for (int i = 0; i < V; ++i) g[i] = rstd * fmaf(-norm(r[i]), mn, fmaf(g[i], w[i], -mg));
       if (p.dres) {
         float e[V];
         Elem<T>::unpack(ev[j], e);
@@ -392,7 +400,8 @@ __global__ __launch_bounds__(kLnThreads) void layernorm_bwd_long_kernel(LnBwdPar
   int turn = 0;
   for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
     const int64_t base = row * p.d;
-    const float rstd = p.rstd[row], shift = -p.mean[row] * rstd;
+    const float rstd = p.rstd[row];
+    const LnN norm(p.mean[row], rstd);
     float sg = 0.f, sn = 0.f;
     for (int c = threadIdx.x; c < n; c += kLnThreads) {
       float g[V], r[V], w[V];
@@ -401,7 +410,7 @@ __global__ __launch_bounds__(kLnThreads) void layernorm_bwd_long_kernel(LnBwdPar
       Elem<T>::unpack(ld16((const T *)p.w + c * V), w);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float gn = g[i] * ln_n(r[i], rstd, shift);
+        const float gn = g[i] * norm(r[i]);
         float *o = out + c * V + i;
         o[0] = first ? gn : o[0] + gn;
         o[p.d] = first ? g[i] : o[p.d] + g[i];
@@ -419,7 +428,7 @@ __global__ __launch_bounds__(kLnThreads) void layernorm_bwd_long_kernel(LnBwdPar
       Elem<T>::unpack(ld16((const T *)p.r + base + c * V), r);
       Elem<T>::unpack(ld16((const T *)p.w + c * V), w);
 #pragma unroll
-      for (int i = 0; i < V; ++i) g[i] = rstd * fmaf(-ln_n(r[i], rstd, shift), mn, fmaf(g[i], w[i], -mg));
+      for (int i = 0; i < V; ++i) g[i] = rstd * fmaf(-norm(r[i]), mn, fmaf(g[i], w[i], -mg));
       if (p.dres) {
         float e[V];
         Elem<T>::unpack(ld16((const T *)p.dres + base + c * V), e);
