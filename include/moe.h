@@ -629,7 +629,9 @@ moe_status moe_layernorm_bwd(const moe_norm_shape *shape, const void *dy, const 
  * (T == 0 then writes zeros and the other tensors may be NULL). Sums run in
  * fp32 in an order that depends on the shape alone (no atomics). ws serves
  * moe_linear_wgrad and every smaller T of the same K and N. T == 0 otherwise
- * writes nothing.
+ * writes nothing. An output shares memory with no other tensor of its call but
+ * those named here, and with those from the same address on (refused otherwise;
+ * so in moe_layernorm_* and moe_muon_step).
  * Supported: T < 2^24, K and N positive multiples of 64, at most 65536, T *
  * max(K, N) small enough for one launch, dtype BF16. shape->act is the
  * product's own activation (moe_linear_fwd, moe_linear_dact); the other calls
@@ -669,7 +671,8 @@ moe_status moe_linear_wgrad(const moe_linear_shape *shape, const void *dz, const
  * far below its largest. x is fp32 or bf16 (shape->dtype); o may be x itself
  * where x is bf16. The products take fp16 operands and fp32 sums (X to 22 bits
  * in the terms that carry it): against the formula the result is off by about
- * 5e-4 of its norm before o's rounding. A matrix that holds an infinity or a
+ * 5e-4 of its norm before o's rounding, as long as |U| is not far below eps
+ * (elements of U / (|U| + eps) under 2^-36 count as zeros). A matrix that holds an infinity or a
  * NaN gives NaN throughout; a matrix of zeros, zeros.
  *
  * The step, with G = grad_scale * grad, on fp32 weights and momentum:

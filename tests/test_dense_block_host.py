@@ -91,6 +91,37 @@ def test_linear_pointers():
         refused(st, moe.moe_linear_wgrad, s, *[FAKE] * 4, ws, size)
 
 
+def test_outputs_in_other_tensors_memory():
+    """An output over an input that another workgroup still reads, in whole or shifted by a row, is refused."""
+    A = lambda i: (i + 1) << 24  # noqa: E731  far enough apart
+    row, T, K, N = 256, 4, 128, 192  # bytes of a row of 128 bf16 values
+    ln = moe.make_norm_shape(T, 128, BF16)
+    for out in (dict(r=A(0) + row), dict(r=A(1) + row), dict(y=A(0) + row), dict(y=A(1) + 3 * row), dict(y=A(4)), dict(r=A(2)),
+                dict(y=A(3))):
+        a = {**dict(x=A(0), residual=A(1), weight=A(2), bias=A(3), r=A(4), y=A(5), mean=A(6), rstd=A(7)), **out}
+        refused(ARG, moe.moe_layernorm_fwd, ln, *a.values(), word="shares memory")
+    n = moe.moe_layernorm_workspace_size(ln)
+    for dx in (A(0) + row, A(1) + row, A(5) + row, A(2)):
+        refused(ARG, moe.moe_layernorm_bwd, ln, *[A(i) for i in range(6)], dx, A(7), A(8), A(9), n, word="shares memory")
+    lin = moe.make_linear_shape(T, K, N, act=moe.MOE_ACT_GELU)
+    for out in (dict(y=A(0)), dict(z=A(0)), dict(y=A(1) + 64), dict(z=A(1)), dict(y=A(3) + 2 * N), dict(z=A(3) + 2 * N),
+                dict(z=A(5) + 2 * N), dict(y=A(2))):
+        a = {**dict(x=A(0), w=A(1), bias=A(2), residual=A(3), z=A(4), y=A(5)), **out}
+        refused(ARG, moe.moe_linear_fwd, lin, *a.values(), word="shares memory")
+    for dz in (A(0) + 2 * N, A(1) + 2 * N):
+        refused(ARG, moe.moe_linear_dact, lin, A(0), A(1), dz, word="shares memory")
+    for dx in (A(0), A(1), A(2) + row, A(3) + row):
+        refused(ARG, moe.moe_linear_dgrad, lin, A(0), A(1), A(2), moe.MOE_ACT_GELU, A(3), dx, word="shares memory")
+    n = moe.moe_linear_workspace_size(lin)
+    for dw, db in ((A(0), A(3)), (A(1), A(3)), (A(2), A(0)), (A(2), A(1)), (A(2), A(2) + 1024)):
+        refused(ARG, moe.moe_linear_wgrad, lin, A(0), A(1), dw, db, A(5), n, word="shares memory")
+    orth = moe.make_orth_shape(2, 100, 70)
+    n = moe.moe_orthogonalize_workspace_size(orth)
+    for a in ((A(0), A(0), A(2), A(3)), (A(0), A(1), A(1), A(3)), (A(0), A(1), A(0) + 400, A(3)), (A(0), A(1), A(2), A(0)),
+              (A(0), A(1), A(2), A(1) + 64)):
+        refused(ARG, moe.moe_muon_step, moe.make_muon_config(0.1), orth, *a, A(5), n, word="shares memory")
+
+
 ORTH = dict(batch=2, rows=100, cols=70, dtype=F32, steps=5, coef=moe._lib.ORTH_COEF, eps=1e-7)
 
 
@@ -243,3 +274,10 @@ def test_orthogonalizer_and_muon_objects():
         with pytest.raises(ValueError, match="gradient"):
             opt.step(bad)
     assert all(not m.any() for m in opt.momenta)
+
+
+def test_muon_refuses_weights_without_rows_or_columns():
+    for shape in ((0, 6), (4, 0), (2, 0, 6)):
+        with pytest.raises(ValueError, match="rows and columns"):
+            optim.ExpertMuon([t(*shape)], 0.1)
+    assert [s.batch for s in optim.ExpertMuon([t(0, 4, 6)], 0.1).shapes] == [0]

@@ -861,6 +861,13 @@ moe_status moe_layernorm_fwd(const moe_norm_shape *shape, const void *x, const v
                          {"mean", mean, true, false},     {"rstd", rstd, true, false}};
   st = validate_ptrs(args, 8, &why);
   if (st != MOE_OK) return report(st, why);
+  const size_t width = s.dtype == MOE_DTYPE_BF16 ? 2 : 4, row = (size_t)s.d * width, all = (size_t)s.T * row;
+  const Span xs{"x", x, all}, rs{"residual", residual, all}, ws{"weight", weight, row}, bs{"bias", bias, row},
+      r_out{"r", r, all}, y_out{"y", y, all};
+  st = validate_apart({{r_out, xs, true}, {r_out, rs, true}, {y_out, xs, true}, {y_out, rs, true}, {y_out, r_out, false},
+                       {r_out, ws, false}, {y_out, ws, false}, {r_out, bs, false}, {y_out, bs, false}},
+                      &why);
+  if (st != MOE_OK) return report(st, why);
   LayerNormArgs a{};
   a.x = x;
   a.residual = residual;
@@ -894,6 +901,12 @@ moe_status moe_layernorm_bwd(const moe_norm_shape *shape, const void *dy, const 
   st = validate_ptrs(args, 9, &why);
   if (st != MOE_OK) return report(st, why);
   st = validate_workspace(ws, ws_bytes, layernorm_workspace(s), &why);
+  if (st != MOE_OK) return report(st, why);
+  const size_t width = s.dtype == MOE_DTYPE_BF16 ? 2 : 4, row = (size_t)s.d * width, all = (size_t)s.T * row;
+  const Span out{"dx", dx, all};
+  st = validate_apart({{out, {"dy", dy, all}, true}, {out, {"r", r, all}, true}, {out, {"dres", dres, all}, true},
+                       {out, {"weight", weight, row}, false}},
+                      &why);
   if (st != MOE_OK) return report(st, why);
   LayerNormArgs a{};
   a.dy = dy;
@@ -934,8 +947,13 @@ moe_status moe_linear_fwd(const moe_linear_shape *shape, const void *x, const vo
                          {"z", z, false, false},      {"y", y, true, false}};
   st = validate_ptrs(args, 6, &why);
   if (st != MOE_OK) return report(st, why);
-  if (z && (z == y || z == residual))
-    return report(MOE_ERR_INVALID_ARGUMENT, "moe_linear_fwd: z is written beside y and may be neither y nor residual");
+  const size_t in = (size_t)s.T * (size_t)s.K * 2, out = (size_t)s.T * (size_t)s.N * 2, mat = (size_t)s.N * (size_t)s.K * 2;
+  const Span xs{"x", x, in}, ws{"w", w, mat}, bs{"bias", bias, (size_t)s.N * 2}, rs{"residual", residual, out},
+      z_out{"z", z, out}, y_out{"y", y, out};
+  st = validate_apart({{z_out, y_out, false}, {z_out, rs, false}, {y_out, rs, true}, {y_out, xs, false}, {z_out, xs, false},
+                       {y_out, ws, false}, {z_out, ws, false}, {y_out, bs, false}, {z_out, bs, false}},
+                      &why);
+  if (st != MOE_OK) return report(st, why);
   LinearArgs a{};
   a.x = x;
   a.w = w;
@@ -962,6 +980,10 @@ moe_status moe_linear_dact(const moe_linear_shape *shape, const void *dy, const 
   if (s.T == 0) return MOE_OK;
   const PtrArg args[] = {{"dy", dy, true, false}, {"z", z, true, false}, {"dz", dz, true, false}};
   st = validate_ptrs(args, 3, &why);
+  if (st != MOE_OK) return report(st, why);
+  const size_t all = (size_t)s.T * (size_t)s.N * 2;
+  const Span out{"dz", dz, all};
+  st = validate_apart({{out, {"dy", dy, all}, true}, {out, {"z", z, all}, true}}, &why);
   if (st != MOE_OK) return report(st, why);
   LinearArgs a{};
   a.dy = dy;
@@ -992,6 +1014,12 @@ moe_status moe_linear_dgrad(const moe_linear_shape *shape, const void *dz, const
                          {"dx", dx, true, false}};
   st = validate_ptrs(args, 5, &why);
   if (st != MOE_OK) return report(st, why);
+  const size_t in = (size_t)s.T * (size_t)s.N * 2, all = (size_t)s.T * (size_t)s.K * 2, mat = (size_t)s.N * (size_t)s.K * 2;
+  const Span out{"dx", dx, all};
+  st = validate_apart({{out, {"dz", dz, in}, false}, {out, {"w", w, mat}, false}, {out, {"z_in", z_in, all}, true},
+                       {out, {"add", add, all}, true}},
+                      &why);
+  if (st != MOE_OK) return report(st, why);
   LinearArgs a{};
   a.dz = const_cast<void *>(dz);
   a.w = w;
@@ -1021,6 +1049,12 @@ moe_status moe_linear_wgrad(const moe_linear_shape *shape, const void *dz, const
   if (st != MOE_OK) return report(st, why);
   const LinearWorkspace w = linear_workspace(s);
   st = validate_workspace(ws, ws_bytes, w.total, &why);
+  if (st != MOE_OK) return report(st, why);
+  const size_t ins = (size_t)s.T * (size_t)s.N * 2, inx = (size_t)s.T * (size_t)s.K * 2;
+  const Span dzs{"dz", dz, ins}, xs{"x", x, inx}, dbs{"db", db, (size_t)s.N * 4},
+      dws{"dw", dw, (size_t)s.N * (size_t)s.K * 4};
+  st = validate_apart({{dws, dzs, false}, {dws, xs, false}, {dbs, dzs, false}, {dbs, xs, false}, {dws, dbs, false}},
+                      &why);
   if (st != MOE_OK) return report(st, why);
   LinearArgs a{};
   a.dz = const_cast<void *>(dz);
@@ -1096,6 +1130,13 @@ moe_status moe_muon_step(const moe_muon_config *cfg, const moe_orth_shape *shape
   st = validate_ptrs(args, 4, &why);
   if (st != MOE_OK) return report(st, why);
   st = validate_workspace(ws, ws_bytes, orth_workspace(s.batch, s.rows, s.cols).total, &why);
+  if (st != MOE_OK) return report(st, why);
+  const size_t n = (size_t)s.batch * (size_t)s.rows * (size_t)s.cols;
+  const Span ps{"param", param, n * 4}, gs{"grad", grad, n * 4}, ms{"momentum", momentum, n * 4},
+      copy{"param_bf16", param_bf16, n * 2};
+  st = validate_apart({{ps, gs, false}, {ps, ms, false}, {ms, gs, false}, {copy, ps, false}, {copy, gs, false},
+                       {copy, ms, false}},
+                      &why);
   if (st != MOE_OK) return report(st, why);
   OrthArgs a = orth_args(s, ws);
   a.param = param;

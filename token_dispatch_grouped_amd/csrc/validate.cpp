@@ -112,6 +112,18 @@ moe_status validate_ptrs(const PtrArg *args, int n, std::string *why) {
   return MOE_OK;
 }
 
+moe_status validate_apart(std::initializer_list<Beside> pairs, std::string *why) {
+  for (const Beside &p : pairs) {
+    const uintptr_t a = (uintptr_t)p.out.ptr, b = (uintptr_t)p.other.ptr;
+    if (!a || !b || a >= b + p.other.bytes || b >= a + p.out.bytes || (p.same_ok && a == b)) continue;
+    char buf[160];
+    snprintf(buf, sizeof buf, "%s is written and shares memory with %s%s", p.out.name, p.other.name,
+             p.same_ok ? ", which it may only do from the same address on" : "");
+    return fail(why, MOE_ERR_INVALID_ARGUMENT, buf);
+  }
+  return MOE_OK;
+}
+
 moe_status validate_workspace(const void *ws, size_t have, size_t need, std::string *why) {
   if (need == 0) return MOE_OK;
   if (!ws) return fail(why, MOE_ERR_WORKSPACE, "workspace is NULL");

@@ -5,6 +5,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <initializer_list>
 #include <string>
 
 #include "moe.h"
@@ -147,6 +148,21 @@ struct OrthWorkspace {
   size_t partial, hi[2], lo[2], a, b, da, db, total;  // byte offsets
 };
 OrthWorkspace orth_workspace(int64_t batch, int rows, int cols);
+
+// Memory a call writes (`out`) and memory it reads or writes beside it: apart, or
+// where `same_ok` starting at the same address, so that every element is written
+// by the thread that read it. Rows shifted against each other would be read after
+// another workgroup has written them. NULL passes.
+struct Span {
+  const char *name;
+  const void *ptr;
+  size_t bytes;
+};
+struct Beside {
+  Span out, other;
+  bool same_ok;
+};
+moe_status validate_apart(std::initializer_list<Beside> pairs, std::string *why);
 
 // Workspace check: NULL or short -> MOE_ERR_WORKSPACE (a zero requirement
 // accepts anything).

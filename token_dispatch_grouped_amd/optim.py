@@ -102,6 +102,8 @@ class ExpertMuon:
         for w, p in zip(self.weights, parts):
             if not w.is_contiguous() or w.dtype not in (torch.bfloat16, torch.float32) or w.dim() not in (2, 3):
                 raise ValueError("weights must be contiguous bf16 or fp32 tensors of 2 or 3 dimensions")
+            if not w.shape[-2] or not w.shape[-1]:
+                raise ValueError("weights must have rows and columns")
             if p < 1 or w.shape[-2] % p:
                 raise ValueError(f"a weight of {w.shape[-2]} rows does not stack {p} matrices")
             rows, cols = w.shape[-2] // p, w.shape[-1]
