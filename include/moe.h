@@ -672,8 +672,8 @@ moe_status moe_linear_wgrad(const moe_linear_shape *shape, const void *dz, const
  * where x is bf16. The products take fp16 operands and fp32 sums (X to 22 bits
  * in the terms that carry it): against the formula the result is off by about
  * 5e-4 of its norm before o's rounding, as long as |U| is not far below eps
- * (elements of U / (|U| + eps) under 2^-36 count as zeros). A matrix that holds an infinity or a
- * NaN gives NaN throughout; a matrix of zeros, zeros.
+ * (elements of U / (|U| + eps) under 2^-36 count as zeros). A matrix that
+ * holds an infinity or a NaN gives NaN throughout; a matrix of zeros, zeros.
  *
  * The step, with G = grad_scale * grad, on fp32 weights and momentum:
  *   momentum = mu * momentum + G
