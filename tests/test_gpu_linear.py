@@ -126,6 +126,13 @@ def test_dgrad(T, K, N):
             assert torch.equal(_bits(dx2), _bits(dx))
 
 
+# few tokens: 32 and 64 columns a workgroup with 1, 2 and 3 groups of 16 tokens, sums shorter than the wavefronts share
+@pytest.mark.parametrize("T,K,N", [(5, 16384, 128), (20, 8256, 64), (40, 8256, 192), (100, 4096, 320), (48, 8192, 128),
+                                   (17, 1024, 8192), (144, 65536, 64), (1, 64, 65536), (80, 2048, 1088), (16, 512, 2048)])
+def test_dgrad_of_few_tokens(T, K, N):
+    test_dgrad(T, K, N)
+
+
 @pytest.mark.parametrize("T,K,N", SHAPES + [(20011, 128, 192), (32768, 320, 512), (3000, 2048, 2048), (700, 8192, 2048)])
 def test_wgrad(T, K, N):
     """Sums over T tokens in fp32: T 2^-23 sum|terms|. Added to a gradient already there, slice by slice: the first sum's

@@ -3,7 +3,8 @@
 //   dz = dy act'(z)                                  (linear_dact)
 //   dx = (dz W) act_in'(z_in) + add                  (linear_dgrad)
 //   dW (+)= dz^T x, db (+)= sum over tokens of dz    (linear_wgrad)
-// on the dense block's kernels (ffn_kernel.h, ffn_few.h) and on large
+// on the dense block's kernels (ffn_kernel.h, ffn_few.h), a form of its own for
+// input gradients of few workgroups (linear_few_dx.h) and on large
 // tiles of its own (linear_wide.h; the weight
 // gradient's in ffn_ilp.hip), with epilogues of its own: bias, activation and
 // residual are applied to the fp32 sums, so that z and y are each rounded once.
@@ -14,6 +15,7 @@
 #include "ffn_kernel.h"
 #include "ffn_plan.h"
 #include "linear_dw.h"
+#include "linear_few_dx.h"
 #include "linear_wide.h"
 
 namespace moe {
@@ -50,6 +52,7 @@ hipError_t launch_linear_fwd(const LinearArgs &a, hipStream_t s) {
 
 static hipError_t dgrad(const FfnTileParams &p, hipStream_t s) {
   LaunchScope scope("linear_dgrad", s);
+  if (linear_few_dx_fits(p)) return run_linear_few_dx(p, s);
   switch (choose(p.M, p.N, false, false, true)) {
     case kNarrow: return run_ffn_tile<false, 64, 128, 32, 64, 2, 2, true, FFN_LINEAR_DX>(p, s);
     case kPair: return run_ffn_tile<false, 128, 128, 64, 64, 2, 2, true, FFN_LINEAR_DX>(p, s);
