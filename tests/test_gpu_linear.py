@@ -126,6 +126,13 @@ def test_dgrad(T, K, N):
             assert torch.equal(_bits(dx2), _bits(dx))
 
 
+# few columns: the sum in eight runs, many rows of workgroups, with 1, 2 and 3 groups of 16 tokens each
+@pytest.mark.parametrize("T,K,N", [(145, 2048, 512), (1000, 512, 128), (3001, 64, 64), (700, 4096, 256), (2500, 1088, 64),
+                                   (333, 65536, 64), (257, 320, 192), (192, 2048, 2048), (384, 576, 1024), (1400, 4096, 256)])
+def test_forward_of_few_columns(T, K, N):
+    test_forward(T, K, N)
+
+
 # few tokens: 32 and 64 columns a workgroup with 1, 2 and 3 groups of 16 tokens, sums shorter than the wavefronts share
 @pytest.mark.parametrize("T,K,N", [(5, 16384, 128), (20, 8256, 64), (40, 8256, 192), (100, 4096, 320), (48, 8192, 128),
                                    (17, 1024, 8192), (144, 65536, 64), (1, 64, 65536), (80, 2048, 1088), (16, 512, 2048)])

@@ -20,8 +20,20 @@
 
 namespace moe {
 
+// The few-token kernel also where 32 columns and 48 tokens a workgroup leave a CU
+// to each: a workgroup's wavefronts share the sum, which a tile takes stage by
+// stage. us against the tiles: 64 columns, K 4096, 192 tokens 4.4, 14.9; 512
+// columns, K 2048, 320 tokens 4.7, 9.4, 768 tokens (256 workgroups) 6.1, 9.7; 2048
+// columns, K 8192, 192 tokens (256) 16.6, 30.5; 256 columns, K 4096, 1400 tokens (240)
+// 16.0, 18.3. The slowest, 64 columns, K 4096, 3000 tokens (252 of 16 columns) 15.8,
+// 15.1.
+static bool few_workgroups(const FfnTileParams &p) {
+  return p.N / 32 * ceil_div(ceil_div(p.M, 16), 3) <= persistent_grid();
+}
+
 static hipError_t forward(const FfnTileParams &p, hipStream_t s) {
   LaunchScope scope("linear_fwd", s);
+  if (few_workgroups(p)) return run_ffn_few<false, FFN_LINEAR>(p, s);
   switch (choose(p.M, p.N, false, false, false)) {
     case kFew: return run_ffn_few<false, FFN_LINEAR>(p, s);
     case kSmall: return run_ffn_tile<false, 64, 64, 32, 64, 4, 2, false, FFN_LINEAR>(p, s);
