@@ -195,6 +195,13 @@ def test_workspaces_never_shrink(K, N):
     assert sizes == sorted(sizes) and sizes[0] == 0
 
 
+def test_orthogonalisation_workspace_serves_every_smaller_batch():
+    """Also where a smaller batch takes the sums of X X^T in slices and a larger one does not."""
+    for rows, cols in ((1500, 4200), (4200, 1500), (2048, 8192), (2816, 4096), (2817, 4096), (64, 65536), (2048, 4032)):
+        sizes = [moe.moe_orthogonalize_workspace_size(moe.make_orth_shape(b, rows, cols)) for b in range(6)]
+        assert sizes == sorted(sizes) and sizes[0] == 0
+
+
 def t(*shape, dtype=torch.bfloat16):
     return torch.zeros(*shape, dtype=dtype)
 

@@ -89,6 +89,12 @@ def test_orthogonalize(batch, rows, cols, bf16):
         assert torch.equal(_orth(y, out=y), o)
 
 
+# X X^T in 2 and 3 slices of the sum, their partial sums joined: one matrix, several, tall
+@pytest.mark.parametrize("batch,rows,cols", [(1, 1500, 4200), (5, 700, 4100), (1, 6200, 1430)])
+def test_long_sums_in_slices(batch, rows, cols):
+    test_orthogonalize(batch, rows, cols, False)
+
+
 @pytest.mark.parametrize("distinct,copies,rows,cols", [(3, 80, 256, 448), (3, 60, 520, 300), (2, 100, 512, 640), (2, 24, 900, 1024),
                                                        (2, 40, 1024, 1030)])
 def test_many_matrices(distinct, copies, rows, cols):

@@ -12,6 +12,7 @@
 // buf; it is formed twice, in norm and in prep, from the same inputs.
 #include "kernels.h"
 #include "orth_kernel.h"
+#include "validate.h"
 
 namespace moe {
 
@@ -245,10 +246,18 @@ static OrthTile choose(int M, int N, int64_t batch, bool sym) {
   return 145 * ceil_div(tiles(256, 256), cus) < 100 * ceil_div(tiles(128, 128), 2 * cus) ? kLarge : kSquare;
 }
 
-static hipError_t sym_product(const OrthTileParams &p, int64_t batch, bool gram, hipStream_t s) {
+static hipError_t sym_product(OrthTileParams p, int64_t batch, bool gram, hipStream_t s) {
   LaunchScope scope(gram ? "orth_gram" : "orth_poly", s);
   const OrthTile t = choose(p.M, p.N, batch, true);
   if (gram) {
+    if (t == kPair) {
+      // long sums of tiles that leave CUs idle: slices of them, joined by a launch
+      // of its own, which ends in the epilogue. 136 tiles of 8192 long sums (a
+      // matrix of 8192 x 2048) in 3 slices: the whole step 920 -> 862 us.
+      const int64_t m = ceil_div(p.M, 128);
+      p.slices = orth_gram_slices(p.M, p.K, batch * m * (m + 1) / 2);
+      if (p.slices > 1) return run_orth_tile<128, 128, 32, 64, 1, 2, ORTH_GRAM>(p, batch, s);
+    }
     switch (t) {
       case kSmall: return run_orth_tile<64, 64, 16, 64, 2, 4, ORTH_GRAM>(p, batch, s);
       case kPair: return run_orth_tile<128, 128, 32, 64, 1, 4, ORTH_GRAM>(p, batch, s);
@@ -345,6 +354,7 @@ hipError_t launch_orth(const OrthArgs &a, hipStream_t s) {
     p.S = w.S;
     p.A = p.B = hi[cur];
     p.C = A;
+    p.sums = reinterpret_cast<f32x4_t *>(ws + w.sums);
     p.diag_out = da;
     p.M = p.N = w.S;
     p.K = w.L;

@@ -65,6 +65,8 @@ struct OrthTileParams {
   int S;                    // stride of the diagonals
   int m_tiles, n_tiles, tiles;        // tiles: of one matrix
   int64_t total;            // tiles of all matrices
+  int slices;               // GRAM: of the sum, a multiple of 64 k each, in `sums`
+  f32x4_t *sums;            // [tile, slice, fragment, thread]
   OrthOut out;              // LAST
 };
 
@@ -401,12 +403,18 @@ __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void orth_tile_
   __shared__ u32x4_t lds[KG * STAGES * STAGE_BYTES / 16];
 
   // each XCD takes a contiguous share of the tiles, matrix by matrix
-  const int64_t lo = (int64_t)(blockIdx.x & 7) * p.total >> 3, hi = (int64_t)((blockIdx.x & 7) + 1) * p.total >> 3;
-  const int64_t id = lo + (int64_t)(blockIdx.x >> 3);
-  if (id >= hi) return;
+  const int slices = MODE == ORTH_GRAM && KG == 1 ? p.slices : 1;
+  const int64_t parts = p.total * slices;
+  const int64_t lo = (int64_t)(blockIdx.x & 7) * parts >> 3, hi = (int64_t)((blockIdx.x & 7) + 1) * parts >> 3;
+  const int64_t part = lo + (int64_t)(blockIdx.x >> 3);
+  if (part >= hi) return;
+  const int64_t id = slices == 1 ? part : part / slices;
   OrthCursor<SYM> at;
   at.start(p, id);
   const int mat = at.mat, mt = at.mt, nt = at.nt;
+  // the slice's stages
+  const int all = p.K / BK, slice = (int)(part - id * slices);
+  const int first_stage = slice * all / slices, stages = (slice + 1) * all / slices - first_stage;
   const int m0 = mt * BM, n0 = nt * BN;
   const int m_valid = min(BM, p.M - m0), n_valid = min(BN, p.N - n0);
 
@@ -417,8 +425,8 @@ __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void orth_tile_
   const int wm = wave / WAVES_N, wn = wave % WAVES_N;
   const int wave_u = __builtin_amdgcn_readfirstlane(wave);
 
-  const half_t *Ab = p.A + mat * p.strideA + (int64_t)m0 * p.lda;
-  const half_t *Bb = p.B + mat * p.strideB + (BKM ? (int64_t)n0 : (int64_t)n0 * p.ldb);
+  const half_t *Ab = p.A + mat * p.strideA + (int64_t)m0 * p.lda + first_stage * BK;
+  const half_t *Bb = p.B + mat * p.strideB + (BKM ? (int64_t)n0 : (int64_t)n0 * p.ldb + first_stage * BK);
   OpA opa;
   OpB opb;
   opa.init(Ab, p.lda, m_valid, wave, lane, [&](int r) { return r < m_valid ? r : m_valid - 1; });
@@ -469,7 +477,6 @@ __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void orth_tile_
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  const int stages = p.K / BK;
   const int nk = (stages - kg + KG - 1) / KG;  // the group's own
   const int nk_max = (stages + KG - 1) / KG;   // barriers are the workgroup's
   f16x8_t fa[2], fb[2][FN];
@@ -551,9 +558,44 @@ __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void orth_tile_
         for (int e = 0; e < 4; ++e) acc[f / FN][f % FN][e] += v[e];
       }
   }
+  if (slices > 1) {
+#pragma unroll
+    for (int f = 0; f < FM * FN; ++f) p.sums[(part * FM * FN + f) * NT + tid] = acc[f / FN][f % FN];
+    return;
+  }
   // scratch: behind the groups' sums
   char *scr = reinterpret_cast<char *>(lds) + (KG - 1) * BM * BN * 4 + wave * RowBlock::kBytes;
   orth_epilogue<FM, MODE>(p, acc, scr, mat, m0, m_valid, wm * WM, n0 + wn * WN, mt != nt);
+}
+
+// The slices' sums of a symmetric product's tiles, added in order, to the epilogue, in
+// the threads' places that the tiles' kernel has.
+template <int BM, int WM, int WN, int MODE>
+__global__ __launch_bounds__((BM / WM) * (BM / WN) * 64, 2) void orth_sum_kernel(OrthTileParams p) {
+  constexpr int WAVES_N = BM / WN, NW = BM / WM * WAVES_N, NT = NW * 64, FM = WM / 16, FN = WN / 16;
+  __shared__ u32x4_t lds[NW * RowBlock::kBytes / 16];
+  const int64_t id = blockIdx.x;
+  OrthCursor<true> at;
+  at.start(p, id);
+  const int m0 = at.mt * BM, n0 = at.nt * BM;
+  const int tid = threadIdx.x, wave = tid >> 6, wm = wave / WAVES_N, wn = wave % WAVES_N;
+  f32x4_t acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const f32x4_t *src = p.sums + id * p.slices * FM * FN * NT + tid;
+#pragma unroll 2
+  for (int s = 0; s < p.slices; ++s) {
+#pragma unroll
+    for (int f = 0; f < FM * FN; ++f) {
+      const f32x4_t v = src[(int64_t)(s * FM * FN + f) * NT];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[f / FN][f % FN][e] += v[e];
+    }
+  }
+  char *scr = reinterpret_cast<char *>(lds) + wave * RowBlock::kBytes;
+  orth_epilogue<FM, MODE>(p, acc, scr, at.mat, m0, min(BM, p.M - m0), wm * WM, n0 + wn * WN, at.mt != at.nt);
 }
 
 template <int BM, int BN, int WM, int WN, int KG, int STAGES, int MODE>
@@ -563,8 +605,16 @@ hipError_t run_orth_tile(OrthTileParams p, int64_t batch, hipStream_t s) {
   p.n_tiles = (p.N + BN - 1) / BN;
   p.tiles = orth_step(MODE) ? p.m_tiles * p.n_tiles : p.m_tiles * (p.m_tiles + 1) / 2;
   p.total = batch * p.tiles;
-  const unsigned grid = (unsigned)(ceil_div(p.total, 8) * 8);
+  if (MODE != ORTH_GRAM || KG > 1 || p.slices < 1) p.slices = 1;
+  const unsigned grid = (unsigned)(ceil_div(p.total * p.slices, 8) * 8);
   orth_tile_kernel<BM, BN, WM, WN, KG, STAGES, MODE><<<dim3(grid), NT, 0, s>>>(p);
+  if constexpr (MODE == ORTH_GRAM && KG == 1) {
+    if (p.slices > 1) {
+      const hipError_t err = hipGetLastError();
+      if (err != hipSuccess) return err;
+      orth_sum_kernel<BM, WM, WN, MODE><<<dim3((unsigned)p.total), NT, 0, s>>>(p);
+    }
+  }
   return hipGetLastError();
 }
 

@@ -436,6 +436,7 @@ OrthWorkspace orth_workspace(int64_t batch, int rows, int cols) {
   w.b = take(n * (size_t)w.S * (size_t)w.S * 2);
   w.da = take(n * (size_t)w.S * 4);
   w.db = take(n * (size_t)w.S * 4);
+  w.sums = take(batch > 0 && orth_gram_sliced(w.S, w.L) ? (size_t)kOrthSliceTiles * 128 * 128 * 4 : 0);
   w.total = at;
   return w;
 }

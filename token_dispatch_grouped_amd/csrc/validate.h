@@ -5,6 +5,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <initializer_list>
 #include <string>
 
@@ -145,8 +146,16 @@ moe_status validate_muon(const moe_muon_config *cfg, std::string *why);
 struct OrthWorkspace {
   int S, L;                              // padded short and long side
   int parts;                             // partial sums of a matrix
-  size_t partial, hi[2], lo[2], a, b, da, db, total;  // byte offsets
+  size_t partial, hi[2], lo[2], a, b, da, db, sums, total;  // byte offsets
 };
+// Slices of the sum of the product X X^T on 128 x 128 tiles, `tiles` of them, where
+// they leave CUs idle, and the tiles' partial sums at most (of every batch whose
+// sides are S and L).
+constexpr int kOrthSliceTiles = 512;
+inline bool orth_gram_sliced(int S, int L) { return L >= 4096 && ceil_div(S, 128) <= 22; }
+inline int orth_gram_slices(int S, int L, int64_t tiles) {
+  return orth_gram_sliced(S, L) && tiles <= kOrthSliceTiles ? (int)std::min<int64_t>(kOrthSliceTiles / tiles, L / 2048) : 1;
+}
 OrthWorkspace orth_workspace(int64_t batch, int rows, int cols);
 
 // Memory a call writes (`out`) and memory it reads or writes beside it: apart, or
