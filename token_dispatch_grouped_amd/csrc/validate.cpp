@@ -417,8 +417,8 @@ OrthWorkspace orth_workspace(int64_t batch, int rows, int cols) {
   const int small = rows < cols ? rows : cols, large = rows < cols ? cols : rows;
   w.S = (small + 63) / 64 * 64;
   w.L = (large + 63) / 64 * 64;
-  // partial sums of 16384 elements or more, 256 of a matrix at most
-  const int64_t parts = ceil_div((int64_t)rows * cols, 16384);
+  // partial sums of 4096 elements or more (16 a thread), 256 of a matrix at most
+  const int64_t parts = ceil_div((int64_t)rows * cols, 4096);
   w.parts = (int)(parts < 256 ? parts : 256);
   size_t at = 0;
   const auto take = [&](size_t bytes) {
