@@ -257,3 +257,40 @@ def test_another_stream_by_its_handle():
     side.synchronize()
     for a, b in zip(want, got):
         assert torch.equal(a, b)
+
+
+def test_the_event_timer_has_one_record_a_launch():
+    import torch
+    import token_dispatch_grouped_amd as m
+    from token_dispatch_grouped_amd import _lib
+
+    def records(call, calls=3):
+        call()
+        torch.cuda.synchronize()
+        _lib.moe_profiler_reset()
+        _lib.moe_profiler_enable(True)
+        try:
+            for _ in range(calls):
+                call()
+            torch.cuda.synchronize()
+            return {k: n for k, (n, _) in _lib.moe_profiler_read_all().items()}
+        finally:
+            _lib.moe_profiler_enable(False)
+            _lib.moe_profiler_reset()
+
+    # sums of X X^T in slices and their join
+    x = torch.randn(1, 1500, 4200, device="cuda")
+    s = m.make_orth_shape(1, 1500, 4200)
+    ws = torch.empty(m.moe_orthogonalize_workspace_size(s), dtype=torch.uint8, device="cuda")
+    o = torch.empty(1, 1500, 4200, dtype=torch.bfloat16, device="cuda")
+    rec = records(lambda: m.moe_orthogonalize(s, x, o, ws, ws.numel()))
+    assert rec == {"orth_norm": 3, "orth_prep": 3, "orth_gram": 15, "orth_gram_sum": 15, "orth_poly": 15, "orth_step": 12,
+                   "orth_last": 3}, rec
+    # a bias gradient in a pass of its own
+    T, K, N = 300, 64, 64
+    dz, x = (torch.randn(T, c, device="cuda").bfloat16() for c in (N, K))
+    dw, db = torch.zeros(N, K, device="cuda"), torch.zeros(N, device="cuda")
+    s = m.make_linear_shape(T, K, N)
+    ws = torch.empty(m.moe_linear_workspace_size(s), dtype=torch.uint8, device="cuda")
+    rec = records(lambda: m.moe_linear_wgrad(s, dz, x, dw, db, ws, ws.numel()))
+    assert rec["linear_wgrad"] == rec["linear_db"] == rec["linear_db_reduce"] == 3, rec

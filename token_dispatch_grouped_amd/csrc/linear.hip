@@ -156,14 +156,15 @@ __global__ __launch_bounds__(64) void linear_db_reduce_kernel(const float *parti
 
 static hipError_t linear_db(const LinearArgs &a, hipStream_t s) {
   const int slices = linear_db_slices(a.T);
-  LaunchScope scope("linear_db", s);
   if (slices > 0) {
+    LaunchScope scope("linear_db", s);
     const int chunk = (int)(ceil_div(ceil_div(a.T, slices), 32) * 32);
     linear_db_partial_kernel<<<dim3((unsigned)(a.N / 64), (unsigned)slices), 256, 0, s>>>(
         (const bf16_t *)a.dz, a.db_partial, (int)a.T, a.N, chunk);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
+  LaunchScope scope("linear_db_reduce", s);
   linear_db_reduce_kernel<<<(unsigned)(a.N / 64), 64, 0, s>>>(a.db_partial, a.db, a.N, slices, a.accumulate ? 1 : 0);
   return hipGetLastError();
 }

@@ -247,17 +247,25 @@ static OrthTile choose(int M, int N, int64_t batch, bool sym) {
 }
 
 static hipError_t sym_product(OrthTileParams p, int64_t batch, bool gram, hipStream_t s) {
-  LaunchScope scope(gram ? "orth_gram" : "orth_poly", s);
   const OrthTile t = choose(p.M, p.N, batch, true);
-  if (gram) {
-    if (t == kPair) {
-      // long sums of tiles that leave CUs idle: slices of them, joined by a launch
-      // of its own, which ends in the epilogue. 136 tiles of 8192 long sums (a
-      // matrix of 8192 x 2048) in 3 slices: the whole step 920 -> 862 us.
-      const int64_t m = ceil_div(p.M, 128);
-      p.slices = orth_gram_slices(p.M, p.K, batch * m * (m + 1) / 2);
-      if (p.slices > 1) return run_orth_tile<128, 128, 32, 64, 1, 2, ORTH_GRAM>(p, batch, s);
+  if (gram && t == kPair) {
+    // long sums of tiles that leave CUs idle: slices of them, joined by a launch
+    // of its own, which ends in the epilogue. 136 tiles of 8192 long sums (a
+    // matrix of 8192 x 2048) in 3 slices: the whole step 920 -> 862 us.
+    const int64_t m = ceil_div(p.M, 128);
+    p.slices = orth_gram_slices(p.M, p.K, batch * m * (m + 1) / 2);
+    if (p.slices > 1) {
+      {
+        LaunchScope scope("orth_gram", s);
+        const hipError_t err = run_orth_tile<128, 128, 32, 64, 1, 2, ORTH_GRAM>(p, batch, s);
+        if (err != hipSuccess) return err;
+      }
+      LaunchScope scope("orth_gram_sum", s);
+      return run_orth_sum<128, 32, 64, ORTH_GRAM>(p, batch, s);
     }
+  }
+  LaunchScope scope(gram ? "orth_gram" : "orth_poly", s);
+  if (gram) {
     switch (t) {
       case kSmall: return run_orth_tile<64, 64, 16, 64, 2, 4, ORTH_GRAM>(p, batch, s);
       case kPair: return run_orth_tile<128, 128, 32, 64, 1, 4, ORTH_GRAM>(p, batch, s);

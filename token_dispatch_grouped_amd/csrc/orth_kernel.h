@@ -608,13 +608,16 @@ hipError_t run_orth_tile(OrthTileParams p, int64_t batch, hipStream_t s) {
   if (MODE != ORTH_GRAM || KG > 1 || p.slices < 1) p.slices = 1;
   const unsigned grid = (unsigned)(ceil_div(p.total * p.slices, 8) * 8);
   orth_tile_kernel<BM, BN, WM, WN, KG, STAGES, MODE><<<dim3(grid), NT, 0, s>>>(p);
-  if constexpr (MODE == ORTH_GRAM && KG == 1) {
-    if (p.slices > 1) {
-      const hipError_t err = hipGetLastError();
-      if (err != hipSuccess) return err;
-      orth_sum_kernel<BM, WM, WN, MODE><<<dim3((unsigned)p.total), NT, 0, s>>>(p);
-    }
-  }
+  return hipGetLastError();
+}
+
+// Behind run_orth_tile with slices, on the same tiles.
+template <int BM, int WM, int WN, int MODE>
+hipError_t run_orth_sum(OrthTileParams p, int64_t batch, hipStream_t s) {
+  p.m_tiles = p.n_tiles = (p.M + BM - 1) / BM;
+  p.tiles = p.m_tiles * (p.m_tiles + 1) / 2;
+  p.total = batch * p.tiles;
+  orth_sum_kernel<BM, WM, WN, MODE><<<dim3((unsigned)p.total), (BM / WM) * (BM / WN) * 64, 0, s>>>(p);
   return hipGetLastError();
 }
 
