@@ -583,7 +583,8 @@ moe_status moe_ffn_wgrad(const moe_ffn_shape *shape, const void *dy, const void 
  *   mean = mean_d(r)                                   [T] fp32
  *   rstd = 1 / sqrt(mean_d((r - mean)^2) + eps)        [T] fp32
  *   y    = (r - mean) * rstd * weight + bias           [T,d] s
- * The shape, the roundings and the rules for r are moe_rmsnorm_fwd's. weight
+ * The shape, the roundings and the rules for r are moe_rmsnorm_fwd's; y, too,
+ * may be x or residual itself, if r is another. weight
  * and bias are [d] s; bias may be NULL (none). Rows whose mean is many times
  * their spread keep the spread's digits, and rows of any finite r have their
  * mean and rstd, also those whose sums pass fp32's range. T == 0 writes
@@ -592,9 +593,11 @@ moe_status moe_ffn_wgrad(const moe_ffn_shape *shape, const void *dy, const void 
  * Backward, from dL/dy, with n = (r - mean) * rstd and g = dy * weight:
  *   dx  = rstd * (g - mean_d(g) - n * mean_d(g * n)) + dres     [T,d] s
  *   dw += sum_t dy * n,   db += sum_t dy                        [d] fp32
- * db may be NULL (not wanted). dres, dx, MOE_NORM_OVERWRITE_DW (which holds
- * for dw and db), the order of the sums and ws (the bytes
- * moe_layernorm_workspace_size reports) are as in moe_rmsnorm_bwd.
+ * db may be NULL (not wanted). dres, dx (which may also be r itself),
+ * MOE_NORM_OVERWRITE_DW (which holds for dw and db), the order of the sums and
+ * ws (the bytes moe_layernorm_workspace_size reports) are as in moe_rmsnorm_bwd.
+ * Any other tensor in the memory of an output (r, y, mean, rstd; dx, dw, db) is
+ * refused, rows shifted against each other too.
  */
 moe_status moe_layernorm_workspace_size(const moe_norm_shape *shape, size_t *bwd_ws);
 moe_status moe_layernorm_fwd(const moe_norm_shape *shape, const void *x, const void *residual, const void *weight,

@@ -863,9 +863,12 @@ moe_status moe_layernorm_fwd(const moe_norm_shape *shape, const void *x, const v
   if (st != MOE_OK) return report(st, why);
   const size_t width = s.dtype == MOE_DTYPE_BF16 ? 2 : 4, row = (size_t)s.d * width, all = (size_t)s.T * row;
   const Span xs{"x", x, all}, rs{"residual", residual, all}, ws{"weight", weight, row}, bs{"bias", bias, row},
-      r_out{"r", r, all}, y_out{"y", y, all};
+      r_out{"r", r, all}, y_out{"y", y, all}, m_out{"mean", mean, (size_t)s.T * 4}, v_out{"rstd", rstd, (size_t)s.T * 4};
   st = validate_apart({{r_out, xs, true}, {r_out, rs, true}, {y_out, xs, true}, {y_out, rs, true}, {y_out, r_out, false},
-                       {r_out, ws, false}, {y_out, ws, false}, {r_out, bs, false}, {y_out, bs, false}},
+                       {r_out, ws, false}, {y_out, ws, false}, {r_out, bs, false}, {y_out, bs, false},
+                       {m_out, v_out, false}, {m_out, xs, false}, {v_out, xs, false}, {m_out, rs, false}, {v_out, rs, false},
+                       {m_out, ws, false}, {v_out, ws, false}, {m_out, bs, false}, {v_out, bs, false},
+                       {m_out, r_out, false}, {v_out, r_out, false}, {m_out, y_out, false}, {v_out, y_out, false}},
                       &why);
   if (st != MOE_OK) return report(st, why);
   LayerNormArgs a{};
@@ -903,9 +906,14 @@ moe_status moe_layernorm_bwd(const moe_norm_shape *shape, const void *dy, const 
   st = validate_workspace(ws, ws_bytes, layernorm_workspace(s), &why);
   if (st != MOE_OK) return report(st, why);
   const size_t width = s.dtype == MOE_DTYPE_BF16 ? 2 : 4, row = (size_t)s.d * width, all = (size_t)s.T * row;
-  const Span out{"dx", dx, all};
-  st = validate_apart({{out, {"dy", dy, all}, true}, {out, {"r", r, all}, true}, {out, {"dres", dres, all}, true},
-                       {out, {"weight", weight, row}, false}},
+  const Span out{"dx", dx, all}, dws{"dw", dw, (size_t)s.d * 4}, dbs{"db", db, (size_t)s.d * 4}, dys{"dy", dy, all},
+      rs{"r", r, all}, ds{"dres", dres, all}, wts{"weight", weight, row}, ms{"mean", mean, (size_t)s.T * 4},
+      vs{"rstd", rstd, (size_t)s.T * 4};
+  st = validate_apart({{out, dys, true}, {out, rs, true}, {out, ds, true}, {out, wts, false}, {out, ms, false},
+                       {out, vs, false}, {dws, dbs, false}, {dws, out, false}, {dbs, out, false}, {dws, dys, false},
+                       {dbs, dys, false}, {dws, rs, false}, {dbs, rs, false}, {dws, ds, false}, {dbs, ds, false},
+                       {dws, wts, false}, {dbs, wts, false}, {dws, ms, false}, {dbs, ms, false}, {dws, vs, false},
+                       {dbs, vs, false}},
                       &why);
   if (st != MOE_OK) return report(st, why);
   LayerNormArgs a{};
