@@ -634,7 +634,9 @@ moe_status moe_layernorm_bwd(const moe_norm_shape *shape, const void *dy, const 
  * moe_linear_wgrad and every smaller T of the same K and N. T == 0 otherwise
  * writes nothing. An output shares memory with no other tensor of its call but
  * those named here, and with those from the same address on (refused otherwise;
- * so in moe_layernorm_* and moe_muon_step).
+ * so in moe_layernorm_* and moe_muon_step). ws, as far as the call uses it, lies
+ * apart from every tensor (refused otherwise, so in moe_layernorm_bwd,
+ * moe_orthogonalize and moe_muon_step).
  * Supported: T < 2^24, K and N positive multiples of 64, at most 65536, T *
  * max(K, N) small enough for one launch, dtype BF16. shape->act is the
  * product's own activation (moe_linear_fwd, moe_linear_dact); the other calls

@@ -72,3 +72,33 @@ def test_layernorm_gradients_in_other_tensors(dtype):
 def test_layernorm_gradients_of_no_rows_in_one_tensor():
     s, n = _norm(BF16, L.MOE_NORM_OVERWRITE_DW, 0)
     refused(lambda *a, stream: moe.moe_layernorm_bwd(s, *a, None, 0, stream=stream), [None] * 7 + [at(0), at(0)], "dw", "db")
+
+
+def _scratch(call, need, tensors):
+    """Each tensor over the workspace's first and last bytes, and all around it."""
+    ws = at(20)
+    for name, size in tensors.items():
+        for place in (ws, ws + need - 16, ws - size + 16):
+            refused(lambda *a, stream: call(*a, ws, need, stream=stream),
+                    {**{n: at(i) for i, n in enumerate(tensors)}, name: place}.values(), "ws", name)
+
+
+@pytest.mark.parametrize("flags", [0, 1])
+def test_workspace_in_other_tensors(flags):
+    """The calls write their workspace before the last tensor is read."""
+    s, n = _norm(F32, flags)
+    row = 4 * D
+    _scratch(lambda *a, stream: moe.moe_layernorm_bwd(s, *a, stream=stream), n,
+             dict(dy=T * row, r=T * row, weight=row, mean=4 * T, rstd=4 * T, dres=T * row, dx=T * row, dw=row, db=row))
+    for rows, K, N in ((T, 128, 192), (9001, 1088, 1088)):
+        lin = moe.make_linear_shape(rows, K, N, flags=flags)
+        _scratch(lambda *a, stream: moe.moe_linear_wgrad(lin, *a, stream=stream), moe.moe_linear_workspace_size(lin),
+                 dict(dz=rows * N * 2, x=rows * K * 2, dw=N * K * 4, db=N * 4))
+    orth = moe.make_orth_shape(2, 100, 70, BF16 if flags else F32)
+    n = moe.moe_orthogonalize_workspace_size(orth)
+    _scratch(lambda *a, stream: moe.moe_orthogonalize(orth, *a, stream=stream), n,
+             dict(x=14000 * (2 if flags else 4), o=14000 * 2))
+    orth = moe.make_orth_shape(2, 100, 70)
+    cfg = moe.make_muon_config(0.1, nesterov=bool(flags))
+    _scratch(lambda *a, stream: moe.moe_muon_step(cfg, orth, *a, stream=stream), n,
+             dict(param=56000, grad=56000, momentum=56000, param_bf16=28000))

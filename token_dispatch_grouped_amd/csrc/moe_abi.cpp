@@ -908,12 +908,14 @@ moe_status moe_layernorm_bwd(const moe_norm_shape *shape, const void *dy, const 
   const size_t width = s.dtype == MOE_DTYPE_BF16 ? 2 : 4, row = (size_t)s.d * width, all = (size_t)s.T * row;
   const Span out{"dx", dx, all}, dws{"dw", dw, (size_t)s.d * 4}, dbs{"db", db, (size_t)s.d * 4}, dys{"dy", dy, all},
       rs{"r", r, all}, ds{"dres", dres, all}, wts{"weight", weight, row}, ms{"mean", mean, (size_t)s.T * 4},
-      vs{"rstd", rstd, (size_t)s.T * 4};
+      vs{"rstd", rstd, (size_t)s.T * 4}, scratch{"ws", ws, layernorm_workspace(s)};
   st = validate_apart({{out, dys, true}, {out, rs, true}, {out, ds, true}, {out, wts, false}, {out, ms, false},
                        {out, vs, false}, {dws, dbs, false}, {dws, out, false}, {dbs, out, false}, {dws, dys, false},
                        {dbs, dys, false}, {dws, rs, false}, {dbs, rs, false}, {dws, ds, false}, {dbs, ds, false},
                        {dws, wts, false}, {dbs, wts, false}, {dws, ms, false}, {dbs, ms, false}, {dws, vs, false},
-                       {dbs, vs, false}},
+                       {dbs, vs, false}, {scratch, dys, false}, {scratch, rs, false}, {scratch, wts, false},
+                       {scratch, ms, false}, {scratch, vs, false}, {scratch, ds, false}, {scratch, out, false},
+                       {scratch, dws, false}, {scratch, dbs, false}},
                       &why);
   if (st != MOE_OK) return report(st, why);
   LayerNormArgs a{};
@@ -1060,8 +1062,9 @@ moe_status moe_linear_wgrad(const moe_linear_shape *shape, const void *dz, const
   if (st != MOE_OK) return report(st, why);
   const size_t ins = (size_t)s.T * (size_t)s.N * 2, inx = (size_t)s.T * (size_t)s.K * 2;
   const Span dzs{"dz", dz, ins}, xs{"x", x, inx}, dbs{"db", db, (size_t)s.N * 4},
-      dws{"dw", dw, (size_t)s.N * (size_t)s.K * 4};
-  st = validate_apart({{dws, dzs, false}, {dws, xs, false}, {dbs, dzs, false}, {dbs, xs, false}, {dws, dbs, false}},
+      dws{"dw", dw, (size_t)s.N * (size_t)s.K * 4}, scratch{"ws", ws, w.total};
+  st = validate_apart({{dws, dzs, false}, {dws, xs, false}, {dbs, dzs, false}, {dbs, xs, false}, {dws, dbs, false},
+                       {scratch, dzs, false}, {scratch, xs, false}, {scratch, dws, false}, {scratch, dbs, false}},
                       &why);
   if (st != MOE_OK) return report(st, why);
   LinearArgs a{};
@@ -1112,7 +1115,13 @@ moe_status moe_orthogonalize(const moe_orth_shape *shape, const void *x, void *o
   const PtrArg args[] = {{"x", x, true, false}, {"o", o, true, false}};
   st = validate_ptrs(args, 2, &why);
   if (st != MOE_OK) return report(st, why);
-  st = validate_workspace(ws, ws_bytes, orth_workspace(s.batch, s.rows, s.cols).total, &why);
+  const size_t need = orth_workspace(s.batch, s.rows, s.cols).total;
+  st = validate_workspace(ws, ws_bytes, need, &why);
+  if (st != MOE_OK) return report(st, why);
+  const size_t n = (size_t)s.batch * (size_t)s.rows * (size_t)s.cols;
+  const Span scratch{"ws", ws, need};
+  st = validate_apart({{scratch, {"x", x, n * (s.dtype == MOE_DTYPE_BF16 ? 2 : 4)}, false}, {scratch, {"o", o, n * 2}, false}},
+                      &why);
   if (st != MOE_OK) return report(st, why);
   OrthArgs a = orth_args(s, ws);
   a.x = x;
@@ -1137,13 +1146,15 @@ moe_status moe_muon_step(const moe_muon_config *cfg, const moe_orth_shape *shape
                          {"param_bf16", param_bf16, false, false}};
   st = validate_ptrs(args, 4, &why);
   if (st != MOE_OK) return report(st, why);
-  st = validate_workspace(ws, ws_bytes, orth_workspace(s.batch, s.rows, s.cols).total, &why);
+  const size_t need = orth_workspace(s.batch, s.rows, s.cols).total;
+  st = validate_workspace(ws, ws_bytes, need, &why);
   if (st != MOE_OK) return report(st, why);
   const size_t n = (size_t)s.batch * (size_t)s.rows * (size_t)s.cols;
   const Span ps{"param", param, n * 4}, gs{"grad", grad, n * 4}, ms{"momentum", momentum, n * 4},
-      copy{"param_bf16", param_bf16, n * 2};
+      copy{"param_bf16", param_bf16, n * 2}, scratch{"ws", ws, need};
   st = validate_apart({{ps, gs, false}, {ps, ms, false}, {ms, gs, false}, {copy, ps, false}, {copy, gs, false},
-                       {copy, ms, false}},
+                       {copy, ms, false}, {scratch, ps, false}, {scratch, gs, false}, {scratch, ms, false},
+                       {scratch, copy, false}},
                       &why);
   if (st != MOE_OK) return report(st, why);
   OrthArgs a = orth_args(s, ws);
