@@ -13,7 +13,8 @@
 // The mean is summed twice, as m0 = sum(r) / d rounded to fp32 and delta =
 // sum(r - m0) / d, so that rows whose mean is many times their spread keep
 // the spread's digits: (r - m0) is exact there, and the variance is
-// sum((r - m0)^2) / d - delta^2.
+// sum((r - m0)^2) / d - delta^2. Where delta is more than the spread, m0 + delta
+// takes m0's place and the second sums are taken again.
 #include "common.h"
 #include "kernels.h"
 #include "mx8.h"
@@ -71,18 +72,26 @@ MOE_DEVICE RowNorm row_norm(Each each, float inv_d, float eps, LnPart (&part)[4]
     float s = 0.f, none = 0.f;
     each([&](float r) { s = fmaf(r, scale, s); });
     row_sums<TPR>(s, none, pa);
-    const float m0 = s * inv_d;
-    float s1 = 0.f, s2 = 0.f;
-    each([&](float r) {
-      const float c = fmaf(r, scale, -m0);
-      s1 += c;
-      s2 = fmaf(c, c, s2);
-    });
-    row_sums<TPR>(s1, s2, pb);
     k.scale = scale;
-    k.m0 = m0;
-    k.delta = s1 * inv_d;
-    var = fmaxf(fmaf(s2, inv_d, -k.delta * k.delta), 0.f);
+    k.m0 = s * inv_d;
+    float s2;
+    // Again from m0 + delta where m0 is off by more than the spread (a row of one
+    // value, or of steps of it): there the variance is what is left of two equal
+    // terms, and n was a rounding of m0's error (1e4, where r is 1.6e15 throughout).
+    for (bool again = false;; again = true) {
+      float s1 = 0.f;
+      s2 = 0.f;
+      each([&](float r) {
+        const float c = fmaf(r, scale, -k.m0);
+        s1 += c;
+        s2 = fmaf(c, c, s2);
+      });
+      row_sums<TPR>(s1, s2, again ? pa : pb);  // all have read pa by the sum in pb
+      k.delta = s1 * inv_d;
+      var = fmaxf(fmaf(s2, inv_d, -k.delta * k.delta), 0.f);
+      if (again || !(var < k.delta * k.delta)) break;  // all threads of the row alike
+      k.m0 += k.delta;
+    }
     return s2;
   };
   float var;
