@@ -111,7 +111,9 @@ __global__ __launch_bounds__(kPpThreads, 2) void linear_dw_kernel(LinearDwParams
   pp_tiles<false, true, true>(lds, p.N, p.K, p.chunk / 64, (hi - first + step - 1) / step, get, done, stage);
 }
 
-// The sums of the slices, in order: chunks of 16 bytes of dw, then of db.
+// The sums of the slices, in order, and the gradient already there added to their
+// sum (one rounding at its size, however many slices): chunks of 16 bytes of dw,
+// then of db.
 struct LinearDwReduce {
   const float *dw_part, *db_part;
   float *dw, *db;
@@ -127,14 +129,16 @@ __global__ __launch_bounds__(256) void linear_dw_reduce_kernel(LinearDwReduce p)
   if (i >= n) return;
   const f32x4_t *src = reinterpret_cast<const f32x4_t *>(bias ? p.db_part : p.dw_part) + i;
   f32x4_t *dst = reinterpret_cast<f32x4_t *>(bias ? p.db : p.dw) + i;
-  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-  if (p.accumulate) v = *dst;
+  f32x4_t old = {0.f, 0.f, 0.f, 0.f}, v = old;
+  if (p.accumulate) old = *dst;
 #pragma unroll 4
   for (int s = 0; s < p.slices; ++s) {
     const f32x4_t q = src[s * n];
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] += q[e];
   }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] += old[e];
   *dst = v;
 }
 
