@@ -250,8 +250,7 @@ static hipError_t sym_product(OrthTileParams p, int64_t batch, bool gram, hipStr
   const OrthTile t = choose(p.M, p.N, batch, true);
   if (gram && t == kPair) {
     // long sums of tiles that leave CUs idle: slices of them, joined by a launch
-    // of its own, which ends in the epilogue. 136 tiles of 8192 long sums (a
-    // matrix of 8192 x 2048) in 3 slices: the whole step 920 -> 862 us.
+    // of its own, which ends in the epilogue
     const int64_t m = ceil_div(p.M, 128);
     p.slices = orth_gram_slices(p.M, p.K, batch * m * (m + 1) / 2);
     if (p.slices > 1) {
