@@ -9,8 +9,8 @@ from tests.launched import kernels
 pytestmark = pytest.mark.gpu
 
 
-# matrices, rows, cols: wide and tall, in 3 and 4 slices, stages that are no multiple of them
-@pytest.mark.parametrize("copies,rows,cols", [(1, 1450, 6150), (1, 6400, 1472), (9, 500, 8200)])
+# matrices, rows, cols: wide and tall, in 3 to 5 slices, stages that are no multiple of them, sums from 4096 on
+@pytest.mark.parametrize("copies,rows,cols", [(1, 1450, 6150), (1, 6400, 1472), (9, 500, 8200), (1, 1500, 4200), (5, 4100, 700)])
 @pytest.mark.parametrize("muon", [False, True])
 def test_slices(copies, rows, cols, muon):
     import torch

@@ -150,19 +150,24 @@ struct OrthWorkspace {
 };
 // Slices of the sum of the product X X^T on 128 x 128 tiles, `tiles` of them, where
 // they leave CUs idle, and the tiles' partial sums at most (of every batch whose
-// sides are S and L): of 2048 at least, as many as make two workgroups a CU, and
-// three or none. The launch that joins them takes 8 us, and two slices of more than
-// half as many tiles as CUs are a round of workgroups and a rest. Muon step in us,
-// whole against in slices, (matrices x) S x L: in 3 to 6 slices 2048 x 6144 726, 715;
-// 2048 x 8192 906, 846; 2176 x 8192 1167, 1127; 2 x 1408 x 8192 1035, 972; 9 x 512 x
-// 8192 1056, 948; 1472 x 16384 1327, 1040; 2048 x 16384 1675, 1491; 1664 x 65536 5025,
-// 3702. In 2: 2816 x 8192 1456, 1488; 2560 x 8192 1336, 1348. L 4096, in 2 and 3: 2176
-// 611, 655, 657; 2304 640, 691; 2048 568, 579, 560; 20 x 320 608, 627, 605; 2 x 1408
-// 547, 569, 560; 1472 441, 438, 410.
+// sides are S and L): of 1365 terms at least, as many as make two workgroups a CU,
+// and three or none; of more tiles than half the CUs only sums from 6144 on. The
+// launch that joins them takes 8 us. Muon step in us, whole against in 3 to 6 slices,
+// (matrices x) S x L: 1472 x 4096 441, 410; 1500 x 4200 467, 428; 5 x 700 x 4100 503,
+// 495; 20 x 320 x 4096 608, 601; 2048 x 6144 726, 715; 2048 x 8192 906, 846; 2176 x
+// 8192 1167, 1127; 2 x 1408 x 8192 1035, 972; 9 x 512 x 8192 1056, 940; 1472 x 16384
+// 1327, 1040; 2048 x 16384 1675, 1491. On the other side: 2176 x 4096 611, 657; 2 x 1408
+// x 4096 547, 560; 2048 x 3008 485, 502; 2048 x 2048 381, 406 (2048 x 4096 568, 560, and
+// 1472 x 3008 382, 367, gain a little). In 2: 2816 x 8192 1456, 1488; 2560 x 8192 1336,
+// 1348; 2304 x 4096 640, 691; 2048 x 4096 568, 579 (2560 x 16384 2230, 2182).
 constexpr int kOrthSliceTiles = 512;
-inline bool orth_gram_sliced(int S, int L) { return L >= 3 * 2048 && ceil_div(S, 128) <= 17; }  // 153 tiles of a matrix
+inline bool orth_gram_sliced(int S, int L) {  // for any batch
+  const int64_t m = ceil_div(S, 128);
+  return (L >= 4096 && m <= 15) || (L >= 6144 && m <= 17);  // 120 and 153 tiles of a matrix
+}
 inline int orth_gram_slices(int S, int L, int64_t tiles) {
-  const int n = orth_gram_sliced(S, L) && tiles > 0 ? (int)std::min<int64_t>(kOrthSliceTiles / tiles, L / 2048) : 1;
+  if (!orth_gram_sliced(S, L) || tiles < 1 || (tiles > 128 && L < 6144)) return 1;
+  const int n = (int)std::min<int64_t>(kOrthSliceTiles / tiles, L / 1365);
   return n < 3 ? 1 : n;
 }
 OrthWorkspace orth_workspace(int64_t batch, int rows, int cols);
