@@ -229,9 +229,9 @@ __global__ __launch_bounds__(kOrthThreads) void orth_prep_kernel(OrthIo p) {
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
-//   small   64 x 64 (step: 64 x 128) tiles, 4 (2) k groups a workgroup
-//   pair    128 x 128 tiles, 2 k groups
-//   square  128 x 128 tiles, two workgroups a CU
+//   small   64 x 64 tiles in 2 k groups (step: 64 x 128 in one), rings of 4 stages
+//   pair    128 x 128 tiles, a ring of 4 stages, a workgroup a CU
+//   square  128 x 128 tiles, a ring of 2 stages, two workgroups a CU
 //   large   256 x 256 tiles
 enum OrthTile { kSmall, kPair, kSquare, kLarge };
 

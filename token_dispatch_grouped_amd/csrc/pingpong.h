@@ -27,7 +27,8 @@
 // leaves the ring alone; both groups meet in front of it and fall apart again
 // behind it.
 //
-// Measured on 8192^3 bf16 (normal values): 1.54 PFLOP/s, and 1.38 with MFMAs of
+// Measured on 8192^3 bf16 (normal values): 1.55 PFLOP/s (a large library product of
+// the same operands in turn 1.59), and 1.38 with MFMAs of
 // 32 x 32 x 16, which read and write twice the accumulators for a product: the
 // power that they draw bounds the clock (on zeros the same loop reaches 1.7).
 #pragma once
