@@ -674,10 +674,12 @@ moe_status moe_linear_wgrad(const moe_linear_shape *shape, const void *dz, const
  * (Taller than wide, the same on the transpose.) With a, b, c = 3.4445, -4.7750,
  * 2.0315 and 5 steps the singular values of o lie near 1, but for those of U
  * far below its largest. x is fp32 or bf16 (shape->dtype); o may be x itself
- * where x is bf16. The products take fp16 operands and fp32 sums (X to 22 bits
- * in the terms that carry it): against the formula the result is off by about
- * 5e-4 of its norm before o's rounding (with it 1.73e-3, where the rounding alone
- * is 1.66e-3), as long as |U| is not far below eps
+ * where x is bf16. The products take fp16 operands and fp32 sums. Where the
+ * shorter side is at most 384, every operand is taken in two halves, 22 bits, and
+ * the result is fp32's (about 2e-7 of its norm off the formula, before o's rounding);
+ * where it is longer, X is, in the terms that carry it: 4e-4 to 6e-4 of the norm, 8e-4
+ * where a few directions hold nearly all the weight (with o's rounding 1.73e-3, where
+ * that alone is 1.66e-3). This holds as long as |U| is not far below eps
  * (elements of U / (|U| + eps) under 2^-36 count as zeros). A matrix that
  * holds an infinity or a NaN gives NaN throughout; a matrix of zeros, zeros.
  *
@@ -685,10 +687,9 @@ moe_status moe_linear_wgrad(const moe_linear_shape *shape, const void *dz, const
  *   momentum = mu * momentum + G
  *   U        = G + mu * momentum (MOE_MUON_NESTEROV) or momentum
  *   param    = param * (1 - lr * weight_decay) - lr * scale * o
- * with o before its rounding to bf16 (the products' fp16 operands put it off by
- * about 5e-4 of its norm, as above: less than bf16 would, more than fp32 products;
- * momentum, decay and sum are fp32's); param_bf16 (may be NULL) is written with the
- * rounded new param, the working copy, and MOE_MUON_ZERO_GRAD clears grad on the way.
+ * with o before its rounding to bf16, off by as much as above; momentum, decay and
+ * sum are fp32's. param_bf16 (may be NULL) is written with the rounded new param, the
+ * working copy, and MOE_MUON_ZERO_GRAD clears grad on the way.
  * `scale` is the caller's: sqrt(max(1, rows / cols)), or 0.2 * sqrt(max(rows,
  * cols)) for updates of the size AdamW's have, are in use.
  *

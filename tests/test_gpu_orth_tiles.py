@@ -19,12 +19,17 @@ PAIR, SQUARE, LARGE = "orth_tile_kernel<128, 128, 32, 64, 1, 4, ", "orth_tile_ke
 
 # copies of 2 matrices, rows, cols, the tile of the symmetric products, of the step: wide and tall; 4 columns and more in
 # one store, or (cols % 4 != 0) each by itself; sides that leave tiles partly empty; more tiles than workgroups
-CASES = [
+CASES = [  # short sides, in both halves
     (1, 100, 257, SMALL_SYM, SMALL), (1, 257, 100, SMALL_SYM, SMALL),
     (15, 200, 300, PAIR, PAIR), (15, 300, 200, PAIR, PAIR), (10, 320, 450, PAIR, PAIR), (10, 450, 333, PAIR, PAIR),
     (40, 300, 200, PAIR, SQUARE), (15, 320, 450, PAIR, SQUARE), (15, 450, 330, PAIR, SQUARE), (40, 200, 300, PAIR, SQUARE),
-    (32, 320, 448, SQUARE, LARGE), (32, 450, 333, SQUARE, LARGE), (32, 333, 450, SQUARE, LARGE), (50, 448, 320, SQUARE, LARGE),
+    (32, 320, 448, SQUARE, SQUARE), (32, 450, 333, SQUARE, SQUARE),
+    # the others
     (42, 500, 644, LARGE, LARGE), (42, 642, 500, LARGE, LARGE), (85, 640, 500, LARGE, LARGE),
+    (1, 700, 780, SMALL_SYM, SMALL), (1, 778, 700, SMALL_SYM, SMALL),
+    (3, 700, 780, PAIR, PAIR), (3, 770, 700, PAIR, PAIR), (4, 833, 701, PAIR, SQUARE), (4, 700, 780, PAIR, SQUARE),
+    (4, 780, 700, PAIR, SQUARE), (4, 700, 778, PAIR, SQUARE), (7, 700, 780, SQUARE, LARGE), (7, 778, 700, SQUARE, LARGE),
+    (9, 700, 778, SQUARE, LARGE), (21, 700, 780, LARGE, LARGE), (21, 778, 700, LARGE, LARGE), (42, 780, 700, LARGE, LARGE),
 ]
 
 
@@ -33,14 +38,15 @@ def _dev(a):
     return torch.from_numpy(a.astype(np.float32)).cuda()
 
 
-def _launched(call, sym, step, last):
+def _launched(call, short, sym, step, last):
     """Five times gram, polynomial and step, behind the norm and the first pass."""
     got = kernels(call)
     if got is None:
         return
+    end = lambda tile, mode: tile + (f"{mode}>" if tile == LARGE else f"{mode}, {'true' if short else 'false'}>")  # noqa: E731
     want = ["orth_norm_kernel", "orth_prep_kernel"]
     for k in range(5):
-        want += [sym + "0>", sym + "1>", step + (last if k == 4 else "2>")]
+        want += [end(sym, 0), end(sym, 1), end(step, last if k == 4 else 2)]
     assert len(got) == len(want) and all(g.startswith(w) for g, w in zip(got, want)), got
 
 
@@ -55,7 +61,7 @@ def test_orthogonalize(copies, rows, cols, sym, step):
     ws = torch.full((m.moe_orthogonalize_workspace_size(s),), 0xFF, dtype=torch.uint8, device="cuda")
     o = torch.full(x.shape, float("nan"), dtype=torch.bfloat16, device="cuda")
     print(f"[orth] 2 x {copies} of {rows} x {cols}", flush=True)
-    _launched(lambda: m.moe_orthogonalize(s, x, o, ws, ws.numel()), sym, step, "3>")
+    _launched(lambda: m.moe_orthogonalize(s, x, o, ws, ws.numel()), min(rows, cols) <= 384, sym, step, 3)
     o = o.view(copies, 2, rows, cols)
     for i in range(2):
         base._check(base._h(o[0, i]), base._h(one[i]))
@@ -80,7 +86,7 @@ def test_muon_step(copies, rows, cols, sym, step):
     ws = torch.full((m.moe_orthogonalize_workspace_size(s),), 0xFF, dtype=torch.uint8, device="cuda")
     cfg = m.make_muon_config(lr, mu, wd, scale, gs, True, True)
     print(f"[muon] 2 x {copies} of {rows} x {cols}", flush=True)
-    _launched(lambda: m.moe_muon_step(cfg, s, p, g, mom, low, ws, ws.numel()), sym, step, "4>")
+    _launched(lambda: m.moe_muon_step(cfg, s, p, g, mom, low, ws, ws.numel()), min(rows, cols) <= 384, sym, step, 4)
     for t in (p, mom, g, low):
         assert (t[n:] == 7).all()
         every = t[:n].view(copies, 2, rows, cols)
@@ -102,7 +108,7 @@ def test_muon_step(copies, rows, cols, sym, step):
         assert np.linalg.norm(d) <= lr * scale * norm + np.linalg.norm(own)
 
 
-@pytest.mark.parametrize("batch,rows,cols", [(6, 200, 330), (6, 330, 200), (96, 320, 448)])
+@pytest.mark.parametrize("batch,rows,cols", [(6, 200, 330), (6, 330, 200), (96, 320, 448), (28, 700, 780)])
 def test_the_same_bits_with_fewer_matrices(batch, rows, cols):
     """The first n matrices of larger buffers, which the same tiles take as the whole batch: the same bits, and the rest
     of every tensor untouched."""
@@ -114,7 +120,7 @@ def test_the_same_bits_with_fewer_matrices(batch, rows, cols):
     cfg = m.make_muon_config(0.01, zero_grad=True)
     ws = torch.empty(m.moe_orthogonalize_workspace_size(m.make_orth_shape(batch, rows, cols)), dtype=torch.uint8, device="cuda")
     first, names = None, None
-    for n in (batch, batch - 1, batch - 7 if batch > 7 else 1, batch):
+    for n in (batch, batch - 1, batch - 2 if batch > 7 else 1, batch):
         t = [p.clone(), g.clone(), mom.clone(), torch.full_like(p, 7.0).bfloat16()]
         ws.fill_(0xFF)
         print(f"[muon] {n} of {batch} x {rows} x {cols}", flush=True)

@@ -235,7 +235,7 @@ __global__ __launch_bounds__(kOrthThreads) void orth_prep_kernel(OrthIo p) {
 //   large   256 x 256 tiles
 enum OrthTile { kSmall, kPair, kSquare, kLarge };
 
-static OrthTile choose(int M, int N, int64_t batch, bool sym) {
+static OrthTile choose(int M, int N, int64_t batch, bool sym, bool both) {
   const int64_t cus = persistent_grid();
   const auto tiles = [&](int bm, int bn) {
     const int64_t m = ceil_div(M, bm), n = ceil_div(N, bn);
@@ -243,11 +243,13 @@ static OrthTile choose(int M, int N, int64_t batch, bool sym) {
   };
   if (tiles(64, sym ? 64 : 128) <= cus) return kSmall;
   if (tiles(128, 128) <= cus) return kPair;
+  if (both) return kSquare;
   return 145 * ceil_div(tiles(256, 256), cus) < 100 * ceil_div(tiles(128, 128), 2 * cus) ? kLarge : kSquare;
 }
 
+template <bool BOTH>
 static hipError_t sym_product(OrthTileParams p, int64_t batch, bool gram, hipStream_t s) {
-  const OrthTile t = choose(p.M, p.N, batch, true);
+  const OrthTile t = choose(p.M, p.N, batch, true, BOTH);
   if (gram && t == kPair) {
     // long sums of tiles that leave CUs idle: slices of them, joined by a launch
     // of its own, which ends in the epilogue
@@ -256,44 +258,45 @@ static hipError_t sym_product(OrthTileParams p, int64_t batch, bool gram, hipStr
     if (p.slices > 1) {
       {
         LaunchScope scope("orth_gram", s);
-        const hipError_t err = run_orth_tile<128, 128, 32, 64, 1, 2, ORTH_GRAM>(p, batch, s);
+        const hipError_t err = run_orth_tile<128, 128, 32, 64, 1, 2, ORTH_GRAM, BOTH>(p, batch, s);
         if (err != hipSuccess) return err;
       }
       LaunchScope scope("orth_gram_sum", s);
-      return run_orth_sum<128, 32, 64, ORTH_GRAM>(p, batch, s);
+      return run_orth_sum<128, 32, 64, ORTH_GRAM, BOTH>(p, batch, s);
     }
   }
   LaunchScope scope(gram ? "orth_gram" : "orth_poly", s);
   if (gram) {
     switch (t) {
-      case kSmall: return run_orth_tile<64, 64, 16, 64, 2, 4, ORTH_GRAM>(p, batch, s);
-      case kPair: return run_orth_tile<128, 128, 32, 64, 1, 4, ORTH_GRAM>(p, batch, s);
-      case kSquare: return run_orth_tile<128, 128, 32, 64, 1, 2, ORTH_GRAM>(p, batch, s);
+      case kSmall: return run_orth_tile<64, 64, 16, 64, 2, 4, ORTH_GRAM, BOTH>(p, batch, s);
+      case kPair: return run_orth_tile<128, 128, 32, 64, 1, 4, ORTH_GRAM, BOTH>(p, batch, s);
+      case kSquare: return run_orth_tile<128, 128, 32, 64, 1, 2, ORTH_GRAM, BOTH>(p, batch, s);
       default: return run_orth_wide<ORTH_GRAM>(p, batch, s);
     }
   }
   switch (t) {
-    case kSmall: return run_orth_tile<64, 64, 16, 64, 2, 4, ORTH_POLY>(p, batch, s);
-    case kPair: return run_orth_tile<128, 128, 32, 64, 1, 4, ORTH_POLY>(p, batch, s);
-    case kSquare: return run_orth_tile<128, 128, 32, 64, 1, 2, ORTH_POLY>(p, batch, s);
+    case kSmall: return run_orth_tile<64, 64, 16, 64, 2, 4, ORTH_POLY, BOTH>(p, batch, s);
+    case kPair: return run_orth_tile<128, 128, 32, 64, 1, 4, ORTH_POLY, BOTH>(p, batch, s);
+    case kSquare: return run_orth_tile<128, 128, 32, 64, 1, 2, ORTH_POLY, BOTH>(p, batch, s);
     default: return run_orth_wide<ORTH_POLY>(p, batch, s);
   }
 }
 
-template <int MODE>
+template <int MODE, bool BOTH>
 static hipError_t step_tiles(const OrthTileParams &p, int64_t batch, hipStream_t s) {
-  switch (choose(p.M, p.N, batch, false)) {
-    case kSmall: return run_orth_tile<64, 128, 16, 64, 1, 4, MODE>(p, batch, s);
-    case kPair: return run_orth_tile<128, 128, 32, 64, 1, 4, MODE>(p, batch, s);
-    case kSquare: return run_orth_tile<128, 128, 32, 64, 1, 2, MODE>(p, batch, s);
+  switch (choose(p.M, p.N, batch, false, BOTH)) {
+    case kSmall: return run_orth_tile<64, 128, 16, 64, 1, 4, MODE, BOTH>(p, batch, s);
+    case kPair: return run_orth_tile<128, 128, 32, 64, 1, 4, MODE, BOTH>(p, batch, s);
+    case kSquare: return run_orth_tile<128, 128, 32, 64, 1, 2, MODE, BOTH>(p, batch, s);
     default: return run_orth_wide<MODE>(p, batch, s);
   }
 }
 
+template <bool BOTH>
 static hipError_t step_product(const OrthTileParams &p, int64_t batch, bool last, hipStream_t s) {
   LaunchScope scope(last ? "orth_last" : "orth_step", s);
-  if (!last) return step_tiles<ORTH_STEP>(p, batch, s);
-  return p.out.param ? step_tiles<ORTH_LAST_MUON>(p, batch, s) : step_tiles<ORTH_LAST>(p, batch, s);
+  if (!last) return step_tiles<ORTH_STEP, BOTH>(p, batch, s);
+  return p.out.param ? step_tiles<ORTH_LAST_MUON, BOTH>(p, batch, s) : step_tiles<ORTH_LAST, BOTH>(p, batch, s);
 }
 
 template <int SRC>
@@ -321,6 +324,8 @@ hipError_t launch_orth(const OrthArgs &a, hipStream_t s) {
   half_t *hi[2] = {(half_t *)(ws + w.hi[0]), (half_t *)(ws + w.hi[1])};
   half_t *lo[2] = {(half_t *)(ws + w.lo[0]), (half_t *)(ws + w.lo[1])};
   half_t *A = (half_t *)(ws + w.a), *B = (half_t *)(ws + w.b);
+  const bool both = orth_both_halves(w.S);
+  half_t *Alo = both ? (half_t *)(ws + w.alo) : nullptr, *Blo = both ? (half_t *)(ws + w.blo) : nullptr;
   float *da = (float *)(ws + w.da), *db = (float *)(ws + w.db);
   OrthIo io{};
   io.x = a.x;
@@ -369,28 +374,36 @@ hipError_t launch_orth(const OrthArgs &a, hipStream_t s) {
     p.ldc = w.S;
     p.strideA = p.strideB = io.stride_x;
     p.strideC = (int64_t)w.S * w.S;
-    err = sym_product(p, a.batch, true, s);
+    if (both) {
+      p.Alo = p.Blo = lo[cur];
+      p.Clo = Alo;
+    }
+    err = both ? sym_product<true>(p, a.batch, true, s) : sym_product<false>(p, a.batch, true, s);
     if (err != hipSuccess) break;
     p.A = p.B = A;
     p.C = B;
+    p.Alo = p.Blo = p.Xlo = Alo;
+    p.Clo = Blo;
     p.diag = da;
     p.diag_out = db;
     p.K = w.S;
     p.lda = p.ldb = w.S;
     p.strideA = p.strideB = p.strideC;
-    err = sym_product(p, a.batch, false, s);
+    err = both ? sym_product<true>(p, a.batch, false, s) : sym_product<false>(p, a.batch, false, s);
     if (err != hipSuccess) break;
     p.A = B;
+    p.Alo = Blo;
     p.B = hi[cur];
-    p.Xlo = lo[cur];
+    p.Blo = p.Xlo = lo[cur];
     p.C = hi[cur ^ 1];
-    p.Clo = k + 2 < a.steps ? lo[cur ^ 1] : nullptr;
+    p.Clo = k + (both ? 1 : 2) < a.steps ? lo[cur ^ 1] : nullptr;
     p.out = out;
     p.diag = db;
     p.N = w.L;
     p.ldb = p.ldc = w.L;
     p.strideB = p.strideC = io.stride_x;
-    err = step_product(p, a.batch, k + 1 == a.steps, s);
+    const bool last = k + 1 == a.steps;
+    err = both ? step_product<true>(p, a.batch, last, s) : step_product<false>(p, a.batch, last, s);
     cur ^= 1;
   }
   return err;

@@ -19,7 +19,10 @@
 //     a X + B X = (a + DB_i) X + B'X.
 // Measured on a 704 x 1024 matrix against fp64: 5e-4 of the norm, 1.3e-3
 // without, 1e-2 with everything in bf16; where a few directions hold nearly
-// all the weight, 8e-4, 3e-2 and 2e-1.
+// all the weight, 8e-4, 3e-2 and 2e-1. Where the short side is short those
+// roundings are larger (fewer terms average them) and the products cheap: there
+// (orth_both_halves) X, A' and B' are held in two halves throughout and each
+// product is high x high + high x low + low x high, 2e-7 of the norm.
 //
 // The kernel is the dense block's tile (ffn_kernel.h): a ring of 64-deep
 // stages filled by the LDS DMA, MFMAs with swapped operands, KG
@@ -54,8 +57,8 @@ struct OrthOut {
 struct OrthTileParams {
   const half_t *A, *B;      // operands, per matrix
   half_t *C;                // GRAM: A', POLY: B', STEP: high half of X'
-  half_t *Clo;              // STEP: low half of X', or NULL (the last X)
-  const half_t *Xlo;        // STEP: low half of X (its high half is B), or NULL
+  half_t *Clo;              // STEP: low half of X', or NULL (the last X); BOTH: of every result
+  const half_t *Xlo;        // STEP: low half of X (its high half is B), or NULL; BOTH, POLY: of A
   const float *diag;        // POLY: DA, STEP: DB (with a added)
   float *diag_out;          // GRAM: DA, POLY: DB + a
   float ca, cb, cc;         // coefficients a, b, c
@@ -68,6 +71,7 @@ struct OrthTileParams {
   int slices;               // GRAM: of the sum, a multiple of 64 k each, in `sums`
   f32x4_t *sums;            // [tile, slice, fragment, thread]
   OrthOut out;              // LAST
+  const half_t *Alo, *Blo;  // BOTH: the operands' low halves
 };
 
 MOE_DEVICE uint32_t pack_h2(float a, float b) {  // nearest-even
@@ -122,7 +126,7 @@ MOE_DEVICE void orth_quad_transpose(float (&v)[4], int lane) {
 // from registers an instruction touches 32 rows, 32 bytes of each, and the
 // step's epilogue took 400 of 730 us.) The loads of a row block and the next one
 // are in flight together.
-template <int FM, int MODE>
+template <int FM, int MODE, bool BOTH = false>
 MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x4_t (&acc)[FM][4], char *scr, int mat, int m0, int m_valid,
                               int row0, int col0, bool mirror) {
   constexpr int H = FM > 1 ? 2 : 1, RB = (FM + 1) / 2;  // blocks of 16 rows in a row block (of 32, or 16); row blocks
@@ -154,7 +158,7 @@ MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x4_t (&acc)[FM][4], ch
   const int64_t at0 = (int64_t)r0 * p.ldc + col0;
   const uint32_t pitch = (uint32_t)p.ldc * 2u, off0 = (uint32_t)rr * pitch + (uint32_t)rc * 16u;
   auto off = [&](int i, int k) { return off0 + (uint32_t)(i * 32 + k * 8) * pitch; };
-  const bool low = STEP && !LAST && p.Xlo;
+  const bool low = BOTH ? MODE != ORTH_GRAM : STEP && !LAST && p.Xlo;
   const TileRows src((STEP ? p.B + mat * p.strideB : p.A + mat * p.strideA) + at0, pitch, rows);  // X, or POLY: A
   const TileRows srclo(p.Xlo + mat * p.strideC + at0, pitch, low ? rows : 0);
   const TileRows dst(p.C + mat * p.strideC + at0, pitch, rows), dstlo(p.Clo + mat * p.strideC + at0, pitch, p.Clo ? rows : 0);
@@ -180,7 +184,7 @@ MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x4_t (&acc)[FM][4], ch
 #pragma unroll
       for (int k = 0; k < 2 * H; ++k) gh[i & 1][k] = src.load(off(i, k));
     }
-    if constexpr (MODE == ORTH_STEP) {
+    if constexpr (MODE == ORTH_STEP || (BOTH && MODE != ORTH_GRAM)) {
 #pragma unroll
       for (int k = 0; k < 2 * H; ++k) gl[i & 1][k] = srclo.load<2>(off(i, k));  // zeros where there is none
     }
@@ -225,7 +229,7 @@ MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x4_t (&acc)[FM][4], ch
         for (int e = 0; e < 4; ++e) acc_at(h, j)[e] = fmaf(dr[h], v[e], acc_at(h, j)[e]);
       };
       blk.template in_order<H>(gh[i & 1], add);
-      if constexpr (MODE == ORTH_STEP) {
+      if constexpr (MODE == ORTH_STEP || BOTH) {
         if (low) blk.template in_order<H>(gl[i & 1], add);
       }
     } else if constexpr (MODE == ORTH_POLY) {
@@ -237,6 +241,14 @@ MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x4_t (&acc)[FM][4], ch
           acc_at(h, j)[e] =
               fmaf(p.cb, v[e], p.cc * fmaf((dr[h] + dc[e]) * kOrthUnscale, v[e], acc_at(h, j)[e]));
       });
+      if constexpr (BOTH)
+        blk.template in_order<H>(gl[i & 1], [&](int h, int j, const uint2 &g) {
+          const f32x4_t v = unpack(g);
+          const f32x4_t dc = *reinterpret_cast<const f32x4_t *>(diag + col(j));
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc_at(h, j)[e] = fmaf(fmaf(p.cc, (dr[h] + dc[e]) * kOrthUnscale, p.cb), v[e], acc_at(h, j)[e]);
+        });
     }
     if constexpr (!STEP) {
       if (br < col0 + 64 && col0 < br + 16 * H) {  // a block on the diagonal
@@ -255,6 +267,8 @@ MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x4_t (&acc)[FM][4], ch
                 acc_at(h, j)[e] = 0.f;
               }
       }
+    }
+    auto mirror_out = [&](half_t *C) {
       if (mirror) {
         // transposed: 64 columns of 32 (16) rows in scr, 64 bytes each, 16-byte
         // chunks swizzled by bits 1 and 2 of the column
@@ -272,17 +286,18 @@ MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x4_t (&acc)[FM][4], ch
         for (int k = 0; k < 2 * H; ++k) {
           const int c = k * (32 / H) + (lane / (2 * H)), ch = lane % (2 * H);
           const u32x4_t v = *reinterpret_cast<const u32x4_t *>(at(c, ch));
-          st16(p.C + mat * p.strideC + (int64_t)(col0 + c) * p.ldc + br + ch * 8, v);
+          st16(C + mat * p.strideC + (int64_t)(col0 + c) * p.ldc + br + ch * 8, v);
         }
       }
-    }
+    };
+    if constexpr (!STEP) mirror_out(p.C);
     if constexpr (!LAST) {
       auto rows_out = [&](const TileRows &to) {
         blk.template rows_out<H>([&](int h, int j) { return pack(acc_at(h, j)); },
                      [&](int k, const u32x4_t &v) { to.store<2>(off(i, k), v); });
       };
       rows_out(dst);
-      if (STEP && p.Clo) {
+      if ((STEP || BOTH) && p.Clo) {
 #pragma unroll
         for (int h = 0; h < H; ++h)
 #pragma unroll
@@ -291,6 +306,7 @@ MOE_DEVICE void orth_epilogue(const OrthTileParams &p, f32x4_t (&acc)[FM][4], ch
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc_at(h, j)[e] -= hi[e];
           }
+        if constexpr (!STEP) mirror_out(p.Clo);
         rows_out(dstlo);
       }
     } else {
@@ -383,14 +399,18 @@ struct OrthCursor {
   }
 };
 
-template <int BM, int BN, int WM, int WN, int KG, int STAGES, int MODE>
+// BOTH: every operand in both its halves. A stage is then 32 k, the high half's
+// chunks (k-major: rows) in front of the low half's, and three products of them are
+// taken: high x high, high x low, low x high (low x low is below fp32's rounding).
+template <int BM, int BN, int WM, int WN, int KG, int STAGES, int MODE, bool BOTH>
 __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void orth_tile_kernel(OrthTileParams p) {
   constexpr bool BKM = orth_step(MODE);  // X is [k, n] there
   constexpr bool SYM = !orth_step(MODE);
   static_assert(!SYM || BM == BN, "symmetric products have square tiles");
   constexpr int WAVES_M = BM / WM, WAVES_N = BN / WN, NW = WAVES_M * WAVES_N, NT = NW * 64;  // of a k group
   constexpr int FM = WM / 16, FN = WN / 16;
-  constexpr int BK = 64, KS = 2;
+  constexpr int BK = 64, KS = 2;   // of a stage in LDS
+  constexpr int STEP_K = BOTH ? 32 : BK;  // of the sum
   static_assert(FN == 4, "the epilogue's rows are 64 columns");
   static_assert((KS * FM) % 2 == 0, "the A fragments alternate between two sets across stages");
   using OpA = Operand<BM, false, NW, BK>;
@@ -413,7 +433,7 @@ __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void orth_tile_
   at.start(p, id);
   const int mat = at.mat, mt = at.mt, nt = at.nt;
   // the slice's stages
-  const int all = p.K / BK, slice = (int)(part - id * slices);
+  const int all = p.K / STEP_K, slice = (int)(part - id * slices);
   const int first_stage = slice * all / slices, stages = (slice + 1) * all / slices - first_stage;
   const int m0 = mt * BM, n0 = nt * BN;
   const int m_valid = min(BM, p.M - m0), n_valid = min(BN, p.N - n0);
@@ -425,31 +445,39 @@ __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void orth_tile_
   const int wm = wave / WAVES_N, wn = wave % WAVES_N;
   const int wave_u = __builtin_amdgcn_readfirstlane(wave);
 
-  const half_t *Ab = p.A + mat * p.strideA + (int64_t)m0 * p.lda + first_stage * BK;
-  const half_t *Bb = p.B + mat * p.strideB + (BKM ? (int64_t)n0 : (int64_t)n0 * p.ldb + first_stage * BK);
+  const half_t *Ab = p.A + mat * p.strideA + (int64_t)m0 * p.lda + first_stage * STEP_K;
+  const half_t *Bb = p.B + mat * p.strideB + (BKM ? (int64_t)n0 : (int64_t)n0 * p.ldb + first_stage * STEP_K);
   OpA opa;
   OpB opb;
   opa.init(Ab, p.lda, m_valid, wave, lane, [&](int r) { return r < m_valid ? r : m_valid - 1; });
   opb.init(Bb, p.ldb, n_valid, wave, lane, [&](int r) { return BKM || r < n_valid ? r : n_valid - 1; });
-  // the chunks' order is pingpong.h's, whose fragments are these
-  auto reorder = [&](auto &op, int valid, bool km) {
+  // the chunks' order is pingpong.h's, whose fragments are these; lo: from a high half to its low one
+  auto reorder = [&](auto &op, int valid, bool km, int64_t lo) {
     using Op = std::remove_reference_t<decltype(op)>;
 #pragma unroll
     for (int i = 0; i < Op::NDMA; ++i) {
       const int r = (i * NW + wave) * Op::RPI + lane / Op::CPR, phys = lane % Op::CPR;
+      if constexpr (BOTH) {
+        if (km) {
+          if (r & 32) op.ptr[i] += lo;
+          op.krow[i] = r & 31;
+        } else if ((phys ^ pp_swz(r)) & 4) {
+          op.ptr[i] += lo - 32;
+        }
+      }
       if (km) op.ptr[i] += min((phys ^ pp_swz_km(r)) * 8, valid - 8) - min((phys ^ (4 * (r & 3))) * 8, valid - 8);
       else op.ptr[i] += ((phys ^ pp_swz(r)) - (phys ^ swz(r))) * 8;
     }
   };
-  reorder(opa, m_valid, false);
-  reorder(opb, n_valid, BKM);
+  reorder(opa, m_valid, false, p.Alo - p.A);
+  reorder(opb, n_valid, BKM, p.Blo - p.B);
 
   const uint32_t lds0 = (uint32_t)(uintptr_t)ldsc;
   auto issue = [&](int kt) {  // the group's stage kt
     const uint32_t sb = lds0 + (uint32_t)(kt % STAGES * STAGE_BYTES);
     const int ks = kt * KG + kg;
-    opa.issue(ks * BK, p.lda, p.K, sb, wave_u);
-    opb.issue(ks * BK, p.ldb, p.K, sb + OpA::BYTES, wave_u);
+    opa.issue(ks * STEP_K, p.lda, p.K, sb, wave_u);
+    opb.issue(ks * STEP_K, p.ldb, p.K, sb + OpA::BYTES, wave_u);
   };
   // 8 consecutive k of row lane & 15 from 8 (lane >> 4) on
   auto rows16 = [&](const char *tile, int rb, int ks) {
@@ -502,7 +530,10 @@ __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void orth_tile_
     if (st < nk) issue(st);
   wait_stages(min(nk, STAGES) - 1);
   barrier();
-  fa[0] = load_a(0, 0, 0);
+  // BOTH: A's low half first, so that the products behind the barrier need the low
+  // half of B alone, whose registers the next stage does not fill yet
+  auto a_half = [](int g) { return BOTH ? 1 - g / FM : g / FM; };
+  fa[0] = load_a(0, a_half(0), 0);
 #pragma unroll
   for (int j = 0; j < FN; ++j) fb[0][j] = load_b(0, 0, j);
 
@@ -514,13 +545,15 @@ __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void orth_tile_
 #pragma unroll
       for (int g = 0; g < NG - 1; ++g) {
         const int ks = g / FM, i = g % FM;
-        fa[(g + 1) & 1] = load_a(slot, (g + 1) / FM, (g + 1) % FM);
+        fa[(g + 1) & 1] = load_a(slot, a_half(g + 1), (g + 1) % FM);
         if (i == 0 && ks + 1 < KS) {
 #pragma unroll
           for (int j = 0; j < FN; ++j) fb[(ks + 1) & 1][j] = load_b(slot, ks + 1, j);
         }
-        mma(i, g & 1, ks & 1);
+        mma(i, g & 1, BOTH ? 0 : ks & 1);
+        if (BOTH && ks == 1) mma(i, g & 1, 1);
       }
+      if constexpr (BOTH) mma(FM - 1, 1, 0);
     }
     // every fragment of this stage is in registers: its slot takes stage
     // kt + STAGES once all wavefronts are here, and stage kt + 1 has landed
@@ -532,7 +565,7 @@ __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void orth_tile_
     // the first fragments of the next stage (on the last pass a harmless
     // read of a stale slot)
     const int nslot = (kt + 1) % STAGES;
-    fa[0] = load_a(nslot, 0, 0);
+    fa[0] = load_a(nslot, a_half(0), 0);
 #pragma unroll
     for (int j = 0; j < FN; ++j) fb[0][j] = load_b(nslot, 0, j);
     if (mine) mma(FM - 1, 1, (KS - 1) & 1);
@@ -565,12 +598,12 @@ __global__ __launch_bounds__(KG * (BM / WM) * (BN / WN) * 64, 2) void orth_tile_
   }
   // scratch: behind the groups' sums
   char *scr = reinterpret_cast<char *>(lds) + (KG - 1) * BM * BN * 4 + wave * RowBlock::kBytes;
-  orth_epilogue<FM, MODE>(p, acc, scr, mat, m0, m_valid, wm * WM, n0 + wn * WN, mt != nt);
+  orth_epilogue<FM, MODE, BOTH>(p, acc, scr, mat, m0, m_valid, wm * WM, n0 + wn * WN, mt != nt);
 }
 
 // The slices' sums of a symmetric product's tiles, added in order, to the epilogue, in
 // the threads' places that the tiles' kernel has.
-template <int BM, int WM, int WN, int MODE>
+template <int BM, int WM, int WN, int MODE, bool BOTH>
 __global__ __launch_bounds__((BM / WM) * (BM / WN) * 64, 2) void orth_sum_kernel(OrthTileParams p) {
   constexpr int WAVES_N = BM / WN, NW = BM / WM * WAVES_N, NT = NW * 64, FM = WM / 16, FN = WN / 16;
   __shared__ u32x4_t lds[NW * RowBlock::kBytes / 16];
@@ -595,10 +628,10 @@ __global__ __launch_bounds__((BM / WM) * (BM / WN) * 64, 2) void orth_sum_kernel
     }
   }
   char *scr = reinterpret_cast<char *>(lds) + wave * RowBlock::kBytes;
-  orth_epilogue<FM, MODE>(p, acc, scr, at.mat, m0, min(BM, p.M - m0), wm * WM, n0 + wn * WN, at.mt != at.nt);
+  orth_epilogue<FM, MODE, BOTH>(p, acc, scr, at.mat, m0, min(BM, p.M - m0), wm * WM, n0 + wn * WN, at.mt != at.nt);
 }
 
-template <int BM, int BN, int WM, int WN, int KG, int STAGES, int MODE>
+template <int BM, int BN, int WM, int WN, int KG, int STAGES, int MODE, bool BOTH>
 hipError_t run_orth_tile(OrthTileParams p, int64_t batch, hipStream_t s) {
   constexpr int NT = KG * (BM / WM) * (BN / WN) * 64;
   p.m_tiles = (p.M + BM - 1) / BM;
@@ -607,17 +640,17 @@ hipError_t run_orth_tile(OrthTileParams p, int64_t batch, hipStream_t s) {
   p.total = batch * p.tiles;
   if (MODE != ORTH_GRAM || KG > 1 || p.slices < 1) p.slices = 1;
   const unsigned grid = (unsigned)(ceil_div(p.total * p.slices, 8) * 8);
-  orth_tile_kernel<BM, BN, WM, WN, KG, STAGES, MODE><<<dim3(grid), NT, 0, s>>>(p);
+  orth_tile_kernel<BM, BN, WM, WN, KG, STAGES, MODE, BOTH><<<dim3(grid), NT, 0, s>>>(p);
   return hipGetLastError();
 }
 
 // Behind run_orth_tile with slices, on the same tiles.
-template <int BM, int WM, int WN, int MODE>
+template <int BM, int WM, int WN, int MODE, bool BOTH>
 hipError_t run_orth_sum(OrthTileParams p, int64_t batch, hipStream_t s) {
   p.m_tiles = p.n_tiles = (p.M + BM - 1) / BM;
   p.tiles = p.m_tiles * (p.m_tiles + 1) / 2;
   p.total = batch * p.tiles;
-  orth_sum_kernel<BM, WM, WN, MODE><<<dim3((unsigned)p.total), (BM / WM) * (BM / WN) * 64, 0, s>>>(p);
+  orth_sum_kernel<BM, WM, WN, MODE, BOTH><<<dim3((unsigned)p.total), (BM / WM) * (BM / WN) * 64, 0, s>>>(p);
   return hipGetLastError();
 }
 

@@ -446,6 +446,9 @@ OrthWorkspace orth_workspace(int64_t batch, int rows, int cols) {
   }
   w.a = take(n * (size_t)w.S * (size_t)w.S * 2);
   w.b = take(n * (size_t)w.S * (size_t)w.S * 2);
+  const size_t low = orth_both_halves(w.S) ? n * (size_t)w.S * (size_t)w.S * 2 : 0;
+  w.alo = take(low);
+  w.blo = take(low);
   w.da = take(n * (size_t)w.S * 4);
   w.db = take(n * (size_t)w.S * 4);
   w.sums = take(batch > 0 && orth_gram_sliced(w.S, w.L) ? (size_t)kOrthSliceTiles * 128 * 128 * 4 : 0);

@@ -146,15 +146,25 @@ moe_status validate_muon(const moe_muon_config *cfg, std::string *why);
 struct OrthWorkspace {
   int S, L;                              // padded short and long side
   int parts;                             // partial sums of a matrix
-  size_t partial, hi[2], lo[2], a, b, da, db, sums, total;  // byte offsets
+  size_t partial, hi[2], lo[2], a, b, alo, blo, da, db, sums, total;  // byte offsets (alo, blo: both halves)
 };
+// Short sides up to which every tensor of the iteration is held and multiplied in two
+// fp16 halves (three products for one), so that the result is fp32's: with X alone in
+// two, the roundings that fewer terms average cost 1e-3 to 2e-3 of the norm at 8 x 8,
+// 9e-4 at 40 x 40, 7e-4 at 128 x 128, 6e-4 at 300 x 300, and 4e-4 to 6e-4 at every
+// longer side. Muon step in us, one half against both: 64 x 64 70, 82; 11 of 62 x 14 80, 89; 64
+// of 100 x 100 88, 107; 8 of 88 x 141 86, 101; 5 of 419 x 328 110, 156; 3 of 1001 x 333
+// 129, 189; 64 x 8192 200, 357; and past the border 64 of 512 x 512 571, 1002; 64 of 640
+// x 640 864, 1784.
+constexpr int kOrthBothSide = 384;
+inline bool orth_both_halves(int S) { return S <= kOrthBothSide; }
 // Slices of the sum of the product X X^T on 128 x 128 tiles, `tiles` of them, where
 // they leave CUs idle, and the tiles' partial sums at most (of every batch whose
 // sides are S and L): of 1365 terms at least, as many as make two workgroups a CU,
 // and three or none; of more tiles than half the CUs only sums from 6144 on. The
 // launch that joins them takes 8 us. Muon step in us, whole against in 3 to 6 slices,
 // (matrices x) S x L: 1472 x 4096 441, 410; 1500 x 4200 467, 428; 5 x 700 x 4100 503,
-// 495; 20 x 320 x 4096 608, 601; 2048 x 6144 726, 715; 2048 x 8192 906, 846; 2176 x
+// 495; 2048 x 6144 726, 715; 2048 x 8192 906, 846; 2176 x
 // 8192 1167, 1127; 2 x 1408 x 8192 1035, 972; 9 x 512 x 8192 1056, 940; 1472 x 16384
 // 1327, 1040; 2048 x 16384 1675, 1491. On the other side: 2176 x 4096 611, 657; 2 x 1408
 // x 4096 547, 560; 2048 x 3008 485, 502; 2048 x 2048 381, 406 (2048 x 4096 568, 560, and
