@@ -1,5 +1,5 @@
-"""The dense product's weight gradients of the large tiles, added to gradients
-that are there already: one rounding at the size of the sum, which is that of
+"""The dense product's weight gradients, added to gradients that are there
+already: one rounding at the size of the sum, which is that of
 one fp32 addition of what the call writes where it does not add."""
 import pytest
 
@@ -9,7 +9,8 @@ from tests.test_linear_plan_host import LARGE
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("T,K,N", [s[:3] for s in LARGE])
+# the large tiles, and the small ones in one slice, a few and many
+@pytest.mark.parametrize("T,K,N", [s[:3] for s in LARGE] + [(700, 1088, 576), (1300, 512, 1408), (20011, 128, 192), (65600, 128, 256)])
 def test_one_rounding_at_the_size_of_the_sum(T, K, N):
     import torch
     m = _moe()

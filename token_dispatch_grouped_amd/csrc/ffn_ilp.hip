@@ -53,7 +53,8 @@ struct WgradReduce {
   const float *partial[2];
   float *dw[2];
   int64_t n4[2];  // 16-byte chunks of the gradient; 0: nothing to do
-  int slices, accumulate;
+  int slices;
+  int accumulate;  // 1: from the gradient already there on; 2: that one added to the slices' sum, in one rounding
 };
 
 __global__ __launch_bounds__(256) void ffn_wgrad_reduce_kernel(WgradReduce p) {
@@ -63,13 +64,18 @@ __global__ __launch_bounds__(256) void ffn_wgrad_reduce_kernel(WgradReduce p) {
   if (i >= p.n4[which]) return;
   const f32x4_t *src = reinterpret_cast<const f32x4_t *>(p.partial[which]);
   f32x4_t *dst = reinterpret_cast<f32x4_t *>(p.dw[which]);
-  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-  if (p.accumulate) v = dst[i];
+  f32x4_t v = {0.f, 0.f, 0.f, 0.f}, old = v;
+  if (p.accumulate == 1) v = dst[i];
+  if (p.accumulate == 2) old = dst[i];
 #pragma unroll 4
   for (int s = 0; s < p.slices; ++s) {
     const f32x4_t q = src[s * p.n4[which] + i];
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] += q[e];
+  }
+  if (p.accumulate == 2) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += old[e];
   }
   dst[i] = v;
 }
@@ -90,12 +96,12 @@ struct WgradProduct {
   float *dw;
 };
 
-static hipError_t wgrad(const WgradProduct *prod, int count, const FfnWgrad &plan, int64_t T, float *ws, bool accumulate,
+static hipError_t wgrad(const WgradProduct *prod, int count, const FfnWgrad &plan, int64_t T, float *ws, int accumulate,
                         const char *name, hipStream_t s) {
   WgradParams w{};
   WgradReduce r{};
   w.T = (int)T;
-  r.accumulate = accumulate ? 1 : 0;
+  r.accumulate = accumulate;
   const int slices = plan.slices;  // 0 without tokens
   r.slices = slices;
   w.chunk = plan.chunk;
@@ -134,14 +140,15 @@ static hipError_t wgrad(const WgradProduct *prod, int count, const FfnWgrad &pla
 
 hipError_t launch_ffn_dense_wgrad(const FfnArgs &a, hipStream_t s) {
   const WgradProduct prod[2] = {{a.dh, a.x, 2 * a.F, a.d, a.dw_gu}, {a.dy, a.a, a.d, a.F, a.dw_down}};
-  return wgrad(prod, 2, ffn_wgrad_plan(a.T, a.d, a.F), a.T, static_cast<float *>(a.partial), a.accumulate, "ffn_wgrad", s);
+  return wgrad(prod, 2, ffn_wgrad_plan(a.T, a.d, a.F), a.T, static_cast<float *>(a.partial), a.accumulate ? 1 : 0,
+               "ffn_wgrad", s);
 }
 
 // The dense product's weight gradient dW = dz^T x on the small tiles: the same
 // launch with one product.
 hipError_t launch_linear_dw(const LinearArgs &a, hipStream_t s) {
   const WgradProduct prod = {a.dz, a.x, a.N, a.K, a.dw};
-  return wgrad(&prod, 1, linear_wgrad_plan(a.T, a.K, a.N), a.T, a.partial, a.accumulate, "linear_wgrad", s);
+  return wgrad(&prod, 1, linear_wgrad_plan(a.T, a.K, a.N), a.T, a.partial, a.accumulate ? 2 : 0, "linear_wgrad", s);
 }
 
 }  // namespace moe
