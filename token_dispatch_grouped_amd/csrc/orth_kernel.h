@@ -24,8 +24,8 @@
 // (orth_both_halves) X, A' and B' are held in two halves throughout and each
 // product is high x high + high x low + low x high, 2e-7 of the norm.
 //
-// The kernel is the dense block's tile (ffn_kernel.h): a ring of 64-deep
-// stages filled by the LDS DMA, MFMAs with swapped operands, KG
+// The kernel is the dense block's tile (ffn_kernel.h): a ring of stages of 64 k (32 in
+// both halves) filled by the LDS DMA, MFMAs with swapped operands, KG
 // groups of wavefronts sharing a tile's stages where tiles are few. The two
 // symmetric products compute the tiles on and below the diagonal and store
 // each twice.
@@ -68,7 +68,7 @@ struct OrthTileParams {
   int S;                    // stride of the diagonals
   int m_tiles, n_tiles, tiles;        // tiles: of one matrix
   int64_t total;            // tiles of all matrices
-  int slices;               // GRAM: of the sum, a multiple of 64 k each, in `sums`
+  int slices;               // GRAM: of the sum, whole stages each, in `sums`
   f32x4_t *sums;            // [tile, slice, fragment, thread]
   OrthOut out;              // LAST
   const half_t *Alo, *Blo;  // BOTH: the operands' low halves
